@@ -23,16 +23,12 @@
 #include <mutex>
 #include <type_traits>
 
+#include "hinm_device.h"
 #include "hinm_internal.h"
 
 using hinm::fail;
 
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;        // waves per workgroup, 16 rows each
 constexpr int kRowsPerWg = 64;
@@ -133,33 +129,6 @@ __device__ inline int64_t y_row(const SpmmArgs& a, int64_t r) {
   if (!a.out_rows) return r;
   const int64_t d = a.out_rows[r];
   return (d >= 0 && d < a.cout) ? d : -1;
-}
-
-__device__ inline uint16_t bf16_rne(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);  // NaN stays NaN
-  u += 0x7fffu + ((u >> 16) & 1u);
-  return (uint16_t)(u >> 16);
-}
-
-// Split-K hand-over: one workgroup of `splits` counts itself in on an
-// agent-scope counter; true for the last to arrive.  The increment wraps (the
-// hardware's atomic inc: old >= splits - 1 stores 0), so the counter is back
-// at 0 after the last arrival without a separate store.
-//
-// Why the partial sums are visible to the last arriver without a cache
-// writeback (gfx950 follows the gfx942 memory model of the LLVM AMDGPU
-// back end): the partials are written and read only with agent-scope atomic
-// stores and loads, which are issued with the sc1 bit and so are coherent
-// across the XCDs' L2 caches (a store writes through to the device-coherent
-// level, a load reads from it).  Each workgroup waits for its partial stores
-// to be acknowledged (s_waitcnt vmcnt(0)) before its increment, and the last
-// arriver issues its partial loads only after its increment has returned.
-// A release / acquire pair would add an L2 writeback and invalidate, which
-// are needed only for data written with ordinary stores; none is read here.
-__device__ inline bool arrive(unsigned* ctr, int splits) {
-  return __builtin_amdgcn_atomic_inc32(ctr, (unsigned)(splits - 1), __ATOMIC_RELAXED, "agent") ==
-         (unsigned)(splits - 1);
 }
 
 // Copies the X rows of one K-block into LDS as xt[n][k] (k fastest): row
@@ -300,16 +269,6 @@ __global__ __launch_bounds__(256) void reduce_kernel(const float* __restrict__ w
 // So lane (i) of a group addresses LDS row "position(4r + i/4)" at token
 // column base + 4*(i%4) to deliver slots 4r..4r+3 of its B operand.
 // ---------------------------------------------------------------------------
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-__device__ inline v4i16 tr_read(const uint16_t* lds_elem) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_v4i16*)((__attribute__((address_space(3))) char*)((__attribute__((address_space(3))) uint16_t*)lds_elem)));
-}
-
 // Loads 16 bytes (8 tokens) of X row c starting at token nb; zeros past the
 // batch, for a -1 index, or when nb is past the batch.
 __device__ inline u32x4 load_x_chunk(const SpmmArgs& a, int c, int nb) {
@@ -437,11 +396,6 @@ __global__ __launch_bounds__(kDecWaves * 64) void decode3_kernel(SpmmArgs a) {
     if (n0 + n < a.batch && yr >= 0) a.y[yr * a.ldy + n0 + n] = bf16_rne(sum);
   }
 }
-
-// Buffer resources (raw buffers, 32-bit offsets; an offset past the end
-// reads zero).
-constexpr int kBufferWord3 = 0x00020000;   // raw buffer, 32-bit data format (gfx9)
-constexpr uint32_t kOob = 0xFFFFFFF0u;     // offset past every buffer: loads return zeros
 
 struct BufRes {
   __amdgpu_buffer_rsrc_t x, vd, vs, meta, id, is;
@@ -1189,28 +1143,6 @@ __device__ inline void prefill_phase(const SpmmArgs& a, const BufRes& res, uint1
   if (b < nb) step(std::integral_constant<int, 0>{}, b);
   if (b + 1 < nb) step(std::integral_constant<int, 1>{}, b + 1);
   if (b + 2 < nb) step(std::integral_constant<int, 2>{}, b + 2);
-}
-
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-// s_waitcnt with only the vector-memory count: vmcnt(n), nothing else.
-template <int N>
-__device__ inline void wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
-// A buffer load whose 16 bytes per lane go straight to LDS: lane l's bytes
-// land at lds + 16 l (an offset past the buffer writes zeros).  The sc0 bit
-// (cache policy 1) makes the load miss in the CU's L1 and read from L2: a
-// gathered X row is used once per workgroup, so L1 allocation buys nothing
-// (0.5-1% faster on every batch-1024/2048 shape measured).
-__device__ inline void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(lds_u8*)lds, 16, off, 0, 0, 1);
-}
-
-__device__ inline v4i16 tr_read_b(const uint8_t* lds) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(lds_u8*)lds);
 }
 
 // prefill_phase with the X rows loaded straight into LDS (buffer loads into
