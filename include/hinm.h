@@ -509,6 +509,174 @@ int hinm_gyro_permute(const hinm_plan_t* plan, const float* importance, int64_t 
                       int32_t cluster_size, int32_t kmeans_iters, const uint8_t* sample, const int32_t* init,
                       double* cost_trace, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixture-of-experts layers on packed weights: a router picks experts for every
+ * token and orders the (token, expert) pairs by expert; hinm_dispatch gathers
+ * the token columns into that order, hinm_spmm_experts multiplies every
+ * expert's columns by its own packed weight in one launch, and hinm_combine
+ * adds each token's expert columns back together.  Activations stay
+ * [channels][tokens] throughout.  Forward only, as every product here.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the router's logits. */
+#define HINM_BF16 0
+#define HINM_FP32 1
+
+/* Limits of the router. */
+#define HINM_MAX_EXPERTS 1024
+#define HINM_MAX_TOP_K 16
+#define HINM_MAX_ALIGN 256
+
+/* Columns that any routing of n_tokens tokens to top_k of n_experts experts
+ * fits into when every expert's range starts at a multiple of `align`:
+ * n_tokens * top_k + min(n_experts, n_tokens * top_k) * (align - 1), rounded
+ * up to a multiple of `align`.  Host only.  Errors: HINM_EINVAL, HINM_ESHAPE. */
+int hinm_route_columns(int64_t n_tokens, int32_t n_experts, int32_t top_k, int32_t align, int64_t* n_cols);
+
+/* Device scratch of hinm_route, in bytes (host only); holds nothing between calls. */
+int hinm_route_workspace_bytes(int64_t n_tokens, int32_t n_experts, size_t* bytes);
+
+/* Router: top-k experts of every token, their weights, and the order of the
+ * (token, expert) pairs by expert.
+ *   logits (device) [n_experts][ldl], ldl >= n_tokens, bf16 (HINM_BF16) or
+ *     fp32 (HINM_FP32).  A NaN or -inf logit makes its expert ineligible for
+ *     that token, so a token whose logits are all -inf is routed nowhere.
+ *   ids int32 [n_tokens][top_k]: the token's eligible experts in descending
+ *     order of their logits, equal logits in ascending order of the expert; -1
+ *     where fewer than top_k are eligible.
+ *   weights fp32 [n_tokens][top_k]: exp(l - m) / S, m the token's largest
+ *     logit, S the sum of exp(l - m) over the chosen experts (renormalize != 0)
+ *     or over every eligible expert (0); 0 where ids is -1.  Logits of +inf
+ *     share the weight equally.
+ *   counts int32 [n_experts]: tokens of every expert.
+ *   starts int32 [n_experts + 1]: first column of every expert, multiples of
+ *     `align`: starts[0] = 0, starts[e + 1] = starts[e] + counts[e] rounded up
+ *     to a multiple of align.
+ *   slots int32 [n_tokens][top_k]: the pair's column, starts[e] plus the number
+ *     of lower-numbered tokens that chose e; -1 where ids is -1.
+ *   src int32 [n_cols]: the token of every column, -1 where there is none.
+ * n_cols (of src) must be at least hinm_route_columns.  1 <= n_experts <=
+ * HINM_MAX_EXPERTS, 1 <= top_k <= min(n_experts, HINM_MAX_TOP_K), align a power
+ * of two up to HINM_MAX_ALIGN.  n_tokens == 0 writes starts, counts and src.
+ * Nothing here depends on the order of atomics: the same logits give the same
+ * outputs.  workspace (device, 256-byte aligned) of
+ * hinm_route_workspace_bytes bytes, may be NULL when that is 0.  Asynchronous
+ * on `stream`.  Errors: HINM_EINVAL, HINM_ESHAPE, HINM_EALIGN, HINM_EWORKSPACE,
+ * HINM_EHIP, HINM_EDEVICE. */
+int hinm_route(const void* logits, int32_t logits_type, int64_t n_tokens, int64_t ldl, int32_t n_experts,
+               int32_t top_k, int32_t renormalize, int32_t align, int32_t* ids, float* weights, int32_t* slots,
+               int32_t* starts, int32_t* counts, int32_t* src, int64_t n_cols, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/* Token columns into the experts' order: XS[c][i] = X[c][src[i]] for i in
+ * 0 .. n_cols - 1, and +0 where src[i] is outside 0 .. n_tokens - 1.
+ * X (device) bf16 [channels][ldx], ldx >= n_tokens; XS (device) bf16
+ * [channels][ldxs], ldxs >= n_cols, every element of XS[:, 0:n_cols] is
+ * written and nothing else.  The bits of X are copied.  X and XS must be
+ * 2-byte aligned and must not overlap.  channels == 0 or n_cols == 0 is a
+ * no-op.  Asynchronous on `stream`.  Errors: HINM_EINVAL, HINM_ESHAPE,
+ * HINM_EALIGN, HINM_EHIP, HINM_EDEVICE. */
+int hinm_dispatch(const void* x_bf16, int64_t channels, int64_t n_tokens, int64_t ldx, const int32_t* src,
+                  int64_t n_cols, void* xs_bf16, int64_t ldxs, void* stream);
+
+/* The experts' columns back to their tokens:
+ *     Y[c][n] = sum over j of weights[n][j] * YS[c][slots[n][j]],
+ * j ascending, in fp32, rounded to bf16 once (nearest even).  A slot outside
+ * 0 .. n_cols - 1 adds nothing, whatever its weight; a token without any slot
+ * gives +0.  YS (device) bf16 [channels][ldys], ldys >= n_cols; Y (device)
+ * bf16 [channels][ldy], ldy >= n_tokens, every element of Y[:, 0:n_tokens] is
+ * written and nothing else; they must not overlap.  1 <= top_k <=
+ * HINM_MAX_TOP_K.  Alignment, no-ops and errors as hinm_dispatch. */
+int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_cols, int64_t ldys, const int32_t* slots,
+                 const float* weights, int64_t n_tokens, int32_t top_k, void* y_bf16, int64_t ldy, void* stream);
+
+/* One product per expert over its own columns, in one launch:
+ *     Y[:, i] = (W_e (.) M_e) X[:, i]  for starts[e] <= i < starts[e] + counts[e].
+ * `stack` describes n_experts packed weights of one plan laid end to end:
+ * every buffer holds n_experts times the plan's bytes, expert e at e times
+ * them (hinm_pack fills one expert when its output pointers are offset so).
+ * X (device) bf16 [cin][ldx], ldx >= n_cols; Y (device) bf16 [cout][ldy], ldy
+ * >= n_cols.  starts, counts (device) int32 [n_experts] are read on the
+ * device, so a routing needs no host synchronisation; ranges are clipped to
+ * 0 .. n_cols, and should not overlap.  Y columns outside every range are left
+ * as they were.  Requires tile_rows % 64 == 0 and each expert's buffers below
+ * 2^31 bytes (HINM_ESHAPE).  X rows that are 16-byte aligned (X aligned, ldx %
+ * 8 == 0) and ranges that start at multiples of 8 (align 8 in hinm_route) run
+ * fastest.  Rounding, determinism, workspace (zero-filled before its first
+ * use, from hinm_spmm_experts_workspace_bytes) and errors as hinm_spmm; the
+ * options of hinm_set_option do not apply. */
+int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_t n_experts, int64_t n_cols, size_t* bytes);
+int hinm_spmm_experts(const hinm_packed_t* stack, int32_t n_experts, const void* x_bf16, int64_t n_cols, int64_t ldx,
+                      const int32_t* starts, const int32_t* counts, void* y_bf16, int64_t ldy, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit microscaled values (the OCP Microscaling format MXFP4).  Every K-block
+ * of the packed layout, dense or 2:4, holds exactly 32 kept values a row: one
+ * microscaling block.  A block is 32 E2M1 codes and one E8M0 scale byte,
+ * value = code * 2^(scale - 127):
+ *   scale = max(exponent field of the largest magnitude - 2, 0), that is
+ *           2^(floor(log2(max |v|)) - 2) clamped from below at 2^-127;
+ *           0 for an all-zero block;
+ *   code  = v / 2^(scale - 127) rounded to the nearest of
+ *           +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, half-way cases to the even code,
+ *           magnitudes above 6 to 6; sign in bit 3.
+ * A block that holds a NaN or an infinity gets scale 255: all its values are
+ * NaN.  Every other value is a bf16 value, so products with 4-bit values run
+ * the same bf16 matrix instructions as those with bf16 values. */
+
+/* Version of the layout described at hinm_mx4_t. */
+#define HINM_MX4_FORMAT_VERSION 1
+
+/* A packed weight with 4-bit microscaled values: the plan plus seven
+ * caller-owned device buffers, each 16-byte aligned (a buffer of size 0 may be
+ * NULL).  Requires tile_rows % 64 == 0.  Rows come in groups of 64; row r of a
+ * group is f = r / 16, i = r % 16, so that the 16 lanes that hold one K chunk
+ * of 16 rows find the codes of four such row sets in 16 adjacent bytes.
+ *   val_dense    uint32 [n_tiles][n_dense_pad/32][tile_rows/64][4 q][16 i][4 f]
+ *                codes of values 8q .. 8q+7 of the row's block, value 8q + u at
+ *                bits 4u .. 4u+3                       (bytes_val_dense / 4)
+ *   scale_dense  uint8  [n_tiles][n_dense_pad/32][tile_rows/64][16 i][4 f]
+ *                                                      (bytes_val_dense / 64)
+ *   idx_dense    int32, as in hinm_packed_t
+ *   val_24       uint32 [n_tiles][n_24_pad/64][tile_rows/64][4 q][16 i][4 f]
+ *   scale_24     uint8  [n_tiles][n_24_pad/64][tile_rows/64][16 i][4 f]
+ *   meta_24      uint16 [n_tiles][n_24_pad/64][tile_rows/64][4 q][16 i][4 f]
+ *                bits 16q .. 16q+15 of the row's metadata word
+ *   idx_24       int32, as in hinm_packed_t */
+typedef struct {
+  hinm_plan_t plan;
+  uint32_t* val_dense;
+  uint8_t* scale_dense;
+  int32_t* idx_dense;
+  uint32_t* val_24;
+  uint8_t* scale_24;
+  uint16_t* meta_24;
+  int32_t* idx_24;
+} hinm_mx4_t;
+
+/* Rounds the values of n_weights packed weights laid end to end (1 for a
+ * plain hinm_packed_t; see hinm_spmm_experts) to 4-bit microscaled values.
+ * out->plan is set to packed->plan; out's buffers, n_weights times the sizes
+ * above, are written whole (metadata reordered, index lists copied).
+ * Asynchronous on `stream`.  Errors: HINM_EINVAL, HINM_ESHAPE (tile_rows % 64),
+ * HINM_EALIGN, HINM_EHIP, HINM_EDEVICE. */
+int hinm_mx4_quantize(const hinm_packed_t* packed, int32_t n_weights, hinm_mx4_t* out, void* stream);
+
+/* The bf16 packed weights that stand for the same values (exact); out->flags
+ * is set to 0.  Arguments and errors as hinm_mx4_quantize. */
+int hinm_mx4_dequantize(const hinm_mx4_t* packed, int32_t n_weights, hinm_packed_t* out, void* stream);
+
+/* hinm_spmm and hinm_spmm_experts with 4-bit microscaled values.  Everything
+ * but the values' format is as there; the workspaces are those of
+ * hinm_spmm_mx4_workspace_bytes and hinm_spmm_experts_workspace_bytes. */
+int hinm_spmm_mx4_workspace_bytes(const hinm_plan_t* plan, int64_t batch, size_t* bytes);
+int hinm_spmm_mx4(const hinm_mx4_t* packed, const void* x_bf16, int64_t batch, int64_t ldx, void* y_bf16, int64_t ldy,
+                  void* workspace, size_t workspace_bytes, void* stream);
+int hinm_spmm_experts_mx4(const hinm_mx4_t* stack, int32_t n_experts, const void* x_bf16, int64_t n_cols, int64_t ldx,
+                          const int32_t* starts, const int32_t* counts, void* y_bf16, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* hinm_status_str(int status);
 

@@ -24,6 +24,8 @@ LIB_PATH = os.path.join(_HERE, "libhinm.so")
 HINM_ABI_VERSION = 2
 HINM_PACKED_WINDOWED = 1     # flags bit: block-diagonal perms (blocks of 64), see include/hinm.h
 HINM_FORMAT_VERSION = 1       # packed-buffer layout version (include/hinm.h)
+HINM_MX4_FORMAT_VERSION = 1   # layout version of 4-bit microscaled values (include/hinm.h)
+HINM_BF16, HINM_FP32 = 0, 1   # element types of the router's logits
 HINM_NOALLOC_SCRATCH_BYTES = 65536 + (32 << 20)   # hinm_spmm_noalloc's device array (include/hinm.h)
 STATUS = {0: "HINM_OK", 1: "HINM_EINVAL", 2: "HINM_ESHAPE", 3: "HINM_EPERM", 4: "HINM_EIMPORTANCE",
           5: "HINM_EALIGN", 6: "HINM_EWORKSPACE", 7: "HINM_EHIP", 8: "HINM_EDEVICE"}
@@ -35,7 +37,10 @@ EXPORTS = ("hinm_abi_version", "hinm_plan", "hinm_pack_workspace_bytes", "hinm_p
            "hinm_pack_tiles_workspace_bytes", "hinm_pack_tiles", "hinm_spmm_tiles_workspace_bytes",
            "hinm_spmm_tiles", "hinm_boundary_search_tiles", "hinm_gyro_workspace_bytes", "hinm_gyro_permute",
            "hinm_set_option", "hinm_get_option", "hinm_spmm_noalloc", "hinm_spmm_group_workspace_bytes",
-           "hinm_spmm_group", "hinm_status_str", "hinm_last_error")
+           "hinm_spmm_group", "hinm_route_columns", "hinm_route_workspace_bytes", "hinm_route", "hinm_dispatch",
+           "hinm_combine", "hinm_spmm_experts_workspace_bytes", "hinm_spmm_experts", "hinm_mx4_quantize",
+           "hinm_mx4_dequantize", "hinm_spmm_mx4_workspace_bytes", "hinm_spmm_mx4", "hinm_spmm_experts_mx4",
+           "hinm_status_str", "hinm_last_error")
 
 # Launch-shape options (hinm_set_option): name -> HINM_OPT_* key.
 OPTIONS = {"decode_path": 1, "decode_wgs": 2, "prefill_nt": 3, "prefill_splits": 4, "prefill_path": 5,
@@ -65,6 +70,12 @@ class PackedT(ctypes.Structure):
     _fields_ = [("plan", PlanT), ("val_dense", ctypes.c_void_p), ("idx_dense", ctypes.c_void_p),
                 ("val_24", ctypes.c_void_p), ("meta_24", ctypes.c_void_p), ("idx_24", ctypes.c_void_p),
                 ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class Mx4T(ctypes.Structure):
+    _fields_ = [("plan", PlanT), ("val_dense", ctypes.c_void_p), ("scale_dense", ctypes.c_void_p),
+                ("idx_dense", ctypes.c_void_p), ("val_24", ctypes.c_void_p), ("scale_24", ctypes.c_void_p),
+                ("meta_24", ctypes.c_void_p), ("idx_24", ctypes.c_void_p)]
 
 
 class TPlanT(ctypes.Structure):
@@ -125,6 +136,21 @@ def library() -> ctypes.CDLL:
             "hinm_spmm_noalloc": ([ctypes.POINTER(PackedT), VP, I64, I64, VP, I64, VP], ctypes.c_int),
             "hinm_spmm_group_workspace_bytes": ([ctypes.c_int, VP, I64, ctypes.POINTER(S)], ctypes.c_int),
             "hinm_spmm_group": ([ctypes.c_int, VP, VP, I64, I64, VP, VP, VP, S, VP], ctypes.c_int),
+            "hinm_route_columns": ([I64, I32, I32, I32, ctypes.POINTER(I64)], ctypes.c_int),
+            "hinm_route_workspace_bytes": ([I64, I32, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_route": ([VP, I32, I64, I64, I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, I64, VP, S, VP],
+                           ctypes.c_int),
+            "hinm_dispatch": ([VP, I64, I64, I64, VP, I64, VP, I64, VP], ctypes.c_int),
+            "hinm_combine": ([VP, I64, I64, I64, VP, VP, I64, I32, VP, I64, VP], ctypes.c_int),
+            "hinm_spmm_experts_workspace_bytes": ([P, I32, I64, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_spmm_experts": ([ctypes.POINTER(PackedT), I32, VP, I64, I64, VP, VP, VP, I64, VP, S, VP],
+                                  ctypes.c_int),
+            "hinm_spmm_experts_mx4": ([ctypes.POINTER(Mx4T), I32, VP, I64, I64, VP, VP, VP, I64, VP, S, VP],
+                                      ctypes.c_int),
+            "hinm_mx4_quantize": ([ctypes.POINTER(PackedT), I32, ctypes.POINTER(Mx4T), VP], ctypes.c_int),
+            "hinm_mx4_dequantize": ([ctypes.POINTER(Mx4T), I32, ctypes.POINTER(PackedT), VP], ctypes.c_int),
+            "hinm_spmm_mx4_workspace_bytes": ([P, I64, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_spmm_mx4": ([ctypes.POINTER(Mx4T), VP, I64, I64, VP, I64, VP, S, VP], ctypes.c_int),
             "hinm_get_option": ([ctypes.c_int, ctypes.POINTER(I64)], ctypes.c_int),
             "hinm_status_str": ([ctypes.c_int], ctypes.c_char_p),
             "hinm_last_error": ([], ctypes.c_char_p),
@@ -237,12 +263,12 @@ class HinmPacked:
 _BUFFERS = ("val_dense", "idx_dense", "val_24", "meta_24", "idx_24")
 
 
-def _check_format(sd: dict, kind: str) -> None:
+def _check_format(sd: dict, kind: str, version: int = HINM_FORMAT_VERSION) -> None:
     if not isinstance(sd, dict) or sd.get("format") != kind:
         raise ValueError(f"not a stored {kind} weight")
-    if sd.get("format_version") != HINM_FORMAT_VERSION:
+    if sd.get("format_version") != version:
         raise ValueError(f"stored layout version {sd.get('format_version')!r}, this library reads "
-                         f"{HINM_FORMAT_VERSION}: pack the weight again")
+                         f"{version}: pack the weight again")
 
 
 def _checked_buffers(sd: dict, want: dict, device) -> dict:
@@ -524,8 +550,13 @@ def spmm(packed: HinmPacked, x: torch.Tensor, out: Optional[torch.Tensor] = None
     Asynchronous on the current stream.  ``workspace`` (uint8, device, zero-filled before its first use) may
     be given; otherwise each stream has its own default workspace, so products on different streams may
     overlap.  The per-call host work is kept to argument checks and one C call, so that small products are
-    not bound by Python.
+    not bound by Python.  A weight with 4-bit microscaled values (quantize_mx4) runs hinm_spmm_mx4; it takes no
+    ``out_rows``.
     """
+    if isinstance(packed, HinmMx4):
+        if out_rows is not None:
+            raise ValueError("out_rows is not supported with 4-bit values")
+        return _spmm_mx4(packed, x, out, workspace)
     p = packed.plan
     dev = x.device
     tiled = isinstance(packed, HinmTPacked)
@@ -746,8 +777,365 @@ def boundary_search_tiles(importance: torch.Tensor, perm: Optional[torch.Tensor]
     return [v[i] for i in range(T)], [pts[i] for i in range(T)]
 
 
+# ---------------------------------------------------------------------------
+# Mixture-of-experts layers and 4-bit microscaled values.
+# ---------------------------------------------------------------------------
+
+def _matrix(t: torch.Tensor, rows: Optional[int], cols: Optional[int], dev: torch.device, what: str) -> int:
+    """Checks a bf16 matrix and returns its row stride in elements."""
+    if (t.dtype != torch.bfloat16 or t.dim() != 2 or t.device != dev or (rows is not None and t.shape[0] != rows)
+            or (cols is not None and t.shape[1] != cols)):
+        raise ValueError(f"{what} must be bf16 [{'channels' if rows is None else rows}, "
+                         f"{'columns' if cols is None else cols}] on {dev}")
+    n = t.shape[1]
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    ld = t.stride(0)
+    if t.shape[0] > 1 and ld < n:
+        raise ValueError(f"{what} must have a row stride of at least its {n} columns")
+    return ld if ld > n else n
+
+
+def _index(t: torch.Tensor, shape, dev: torch.device, what: str, dtype=torch.int32) -> None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {str(dtype).split('.')[1]} {list(shape)} tensor on {dev}")
+
+
+def _call(dev: torch.device, fn, *args) -> None:
+    """One C call with ``dev`` current."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
+
+
+def _split_workspace(dev: torch.device, stream: int, nbytes: int) -> Optional[torch.Tensor]:
+    """The default workspace of an expert or 4-bit product: the stream's own, as for spmm; while a graph is
+    captured, a new one out of the graph's memory, cleared by a node of the graph, so that graphs captured on one
+    stream and replayed on several never share one."""
+    if nbytes and torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    return _workspace(dev, stream, nbytes)
+
+
+@dataclasses.dataclass
+class Routing:
+    """Where every token goes (hinm_route): its experts, their weights, and the column order by expert."""
+
+    ids: torch.Tensor       # int32 [tokens, top_k]: experts, best first; -1: none
+    weights: torch.Tensor   # fp32 [tokens, top_k]
+    slots: torch.Tensor     # int32 [tokens, top_k]: column of each (token, choice); -1: none
+    starts: torch.Tensor    # int32 [experts + 1]: first column of every expert
+    counts: torch.Tensor    # int32 [experts]
+    src: torch.Tensor       # int32 [columns]: token of every column; -1: none
+
+    @property
+    def n_tokens(self) -> int:
+        return self.slots.shape[0]
+
+    @property
+    def top_k(self) -> int:
+        return self.slots.shape[1]
+
+    @property
+    def n_experts(self) -> int:
+        return self.counts.shape[0]
+
+    @property
+    def n_cols(self) -> int:
+        return self.src.shape[0]
+
+
+def route_columns(n_tokens: int, n_experts: int, top_k: int, align: int = 8) -> int:
+    """Columns any such routing fits into (hinm_route_columns, host only)."""
+    n = ctypes.c_int64()
+    _check(library().hinm_route_columns(n_tokens, n_experts, top_k, align, ctypes.byref(n)))
+    return n.value
+
+
+def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, align: int = 8) -> Routing:
+    """Router (hinm_route): logits bf16 or fp32 [experts, tokens] (unit column stride) -> Routing.
+
+    Experts with NaN or -inf logits are not eligible; weights are softmax over the chosen experts
+    (``renormalize``) or over all eligible ones.  Every expert's columns start at a multiple of ``align``.
+    Asynchronous on the current stream; the column count depends on the sizes alone."""
+    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D bf16 or fp32 CUDA tensor [experts, tokens]")
+    e, n = logits.shape
+    ld = logits.stride(0)
+    if (n > 1 and logits.stride(1) != 1) or (e > 1 and ld < n):
+        raise ValueError("logits must have unit column stride and rows that do not overlap")
+    dev, lib = logits.device, library()
+    cols = route_columns(n, e, top_k, align)
+    need = ctypes.c_size_t()
+    _check(lib.hinm_route_workspace_bytes(n, e, ctypes.byref(need)))
+    ints = torch.empty(2 * n * top_k + 2 * e + 1 + cols, dtype=torch.int32, device=dev)
+    a, b = n * top_k, 2 * n * top_k
+    r = Routing(ints[:a].view(n, top_k), torch.empty((n, top_k), dtype=torch.float32, device=dev),
+                ints[a:b].view(n, top_k), ints[b:b + e + 1], ints[b + e + 1:b + 2 * e + 1], ints[b + 2 * e + 1:])
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    _call(dev, lib.hinm_route, logits.data_ptr(), HINM_BF16 if logits.dtype == torch.bfloat16 else HINM_FP32, n,
+          max(ld, n), e, top_k, int(renormalize), align, r.ids.data_ptr(), r.weights.data_ptr(), r.slots.data_ptr(),
+          r.starts.data_ptr(), r.counts.data_ptr(), r.src.data_ptr(), cols, ws.data_ptr() if ws is not None else None,
+          need.value, _stream_ptr(dev))
+    return r
+
+
+def dispatch(x: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Token columns in the experts' order (hinm_dispatch): x bf16 [channels, tokens] -> bf16 [channels, columns],
+    zeros in columns without a token.  Asynchronous on the current stream."""
+    dev = routing.src.device
+    ldx = _matrix(x, None, routing.n_tokens, dev, "x")
+    _index(routing.src, (routing.n_cols,), dev, "routing.src")
+    c, cols = x.shape[0], routing.n_cols
+    if out is None:
+        out = torch.empty((c, cols), dtype=torch.bfloat16, device=dev)
+    ldo = _matrix(out, c, cols, dev, "out")
+    _call(dev, library().hinm_dispatch, x.data_ptr(), c, routing.n_tokens, ldx, routing.src.data_ptr(), cols,
+          out.data_ptr(), ldo, _stream_ptr(dev))
+    return out
+
+
+def combine(y: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Weighted sum of every token's expert columns (hinm_combine): y bf16 [channels, columns] -> bf16
+    [channels, tokens].  Asynchronous on the current stream."""
+    dev = routing.slots.device
+    ldy = _matrix(y, None, routing.n_cols, dev, "y")
+    n, k, c = routing.n_tokens, routing.top_k, y.shape[0]
+    _index(routing.slots, (n, k), dev, "routing.slots")
+    _index(routing.weights, (n, k), dev, "routing.weights", torch.float32)
+    if out is None:
+        out = torch.empty((c, n), dtype=torch.bfloat16, device=dev)
+    ldo = _matrix(out, c, n, dev, "out")
+    _call(dev, library().hinm_combine, y.data_ptr(), c, routing.n_cols, ldy, routing.slots.data_ptr(),
+          routing.weights.data_ptr(), n, k, out.data_ptr(), ldo, _stream_ptr(dev))
+    return out
+
+
+def _ptr(t: torch.Tensor) -> Optional[int]:
+    return t.data_ptr() if t.numel() else None
+
+
+@dataclasses.dataclass
+class Experts:
+    """Packed weights of one plan laid end to end, one per expert: HinmPacked's buffers with a leading expert
+    axis (all contiguous; the tensors must not be replaced afterwards)."""
+
+    plan: Plan
+    val_dense: torch.Tensor
+    idx_dense: torch.Tensor
+    val_24: torch.Tensor
+    meta_24: torch.Tensor
+    idx_24: torch.Tensor
+
+    @classmethod
+    def stack(cls, packed) -> "Experts":
+        """Copies packed weights (HinmPacked of equal plans on one device) into one stack."""
+        packed = list(packed)
+        if not packed or any(not isinstance(p, HinmPacked) for p in packed):
+            raise ValueError("a stack takes one or more uniform packed weights (pack, not pack_tiles)")
+        p0 = packed[0]
+        for p in packed:
+            if p.plan != p0.plan or p.device != p0.device:
+                raise ValueError("stacked weights must have equal plans and be on one device")
+        return cls(p0.plan, *[torch.stack([getattr(p, k) for p in packed]) for k in _BUFFERS])
+
+    @property
+    def n_experts(self) -> int:
+        return self.idx_24.shape[0]
+
+    @property
+    def device(self) -> torch.device:
+        return self.idx_24.device
+
+    def nbytes(self) -> int:
+        return self.n_experts * self.plan.packed_bytes
+
+    def struct(self) -> PackedT:
+        st = self.__dict__.get("_struct")
+        if st is None:
+            st = self.__dict__["_struct"] = PackedT(self.plan.raw, *[_ptr(getattr(self, k)) for k in _BUFFERS], 0, 0)
+        return st
+
+    def state_dict(self) -> dict:
+        """As HinmPacked.state_dict, every buffer with its expert axis."""
+        p = self.plan
+        return {"format": "hinm-experts", "format_version": HINM_FORMAT_VERSION, "n_experts": self.n_experts,
+                "cout": p.cout, "cin": p.cin, "tile_rows": p.tile_rows, "t_s": p.t_s, "v_s": p.v_s,
+                **{k: getattr(self, k) for k in _BUFFERS}}
+
+    @classmethod
+    def from_state_dict(cls, sd: dict, device=None) -> "Experts":
+        _check_format(sd, "hinm-experts")
+        p = plan(int(sd["cout"]), int(sd["cin"]), int(sd["tile_rows"]), float(sd["t_s"]), float(sd["v_s"]))
+        n = int(sd["n_experts"])
+        if n < 1:
+            raise ValueError("a stored stack needs at least one expert")
+        return cls(p, **_checked_buffers(sd, {k: ((n, *s), t) for k, (s, t) in _packed_shapes(p).items()}, device))
+
+
+def _packed_shapes(p: Plan) -> dict:
+    T, R, D, S = p.n_tiles, p.tile_rows, p.n_dense_pad, p.n_24_pad
+    return {"val_dense": ((T, D // 32, R, 32), torch.int16), "idx_dense": ((T, D), torch.int32),
+            "val_24": ((T, S // 64, R, 32), torch.int16), "meta_24": ((T, S // 64, R), torch.int64),
+            "idx_24": ((T, S), torch.int32)}
+
+
+def _mx4_shapes(p: Plan) -> dict:
+    T, G, D, S = p.n_tiles, p.tile_rows // 64, p.n_dense_pad, p.n_24_pad
+    return {"val_dense": ((T, D // 32, G, 4, 16, 4), torch.int32), "scale_dense": ((T, D // 32, G, 16, 4), torch.uint8),
+            "idx_dense": ((T, D), torch.int32), "val_24": ((T, S // 64, G, 4, 16, 4), torch.int32),
+            "scale_24": ((T, S // 64, G, 16, 4), torch.uint8), "meta_24": ((T, S // 64, G, 4, 16, 4), torch.int16),
+            "idx_24": ((T, S), torch.int32)}
+
+
+_MX4_BUFFERS = ("val_dense", "scale_dense", "idx_dense", "val_24", "scale_24", "meta_24", "idx_24")
+
+
+@dataclasses.dataclass
+class HinmMx4:
+    """A packed weight, or a stack of them, with 4-bit microscaled values (hinm_mx4_t; buffers of a stack have a
+    leading expert axis).  Made by quantize_mx4; the tensors must not be replaced afterwards."""
+
+    plan: Plan
+    val_dense: torch.Tensor    # int32 bits of 8 codes
+    scale_dense: torch.Tensor  # uint8
+    idx_dense: torch.Tensor    # int32
+    val_24: torch.Tensor
+    scale_24: torch.Tensor
+    meta_24: torch.Tensor      # int16 bits of uint16
+    idx_24: torch.Tensor
+    n_experts: Optional[int] = None   # None: one weight
+
+    @property
+    def device(self) -> torch.device:
+        return self.idx_24.device
+
+    def nbytes(self) -> int:
+        return sum(getattr(self, k).numel() * getattr(self, k).element_size() for k in _MX4_BUFFERS)
+
+    def struct(self) -> Mx4T:
+        st = self.__dict__.get("_struct")
+        if st is None:
+            st = self.__dict__["_struct"] = Mx4T(self.plan.raw, *[_ptr(getattr(self, k)) for k in _MX4_BUFFERS])
+            self.__dict__["_ws_need"] = {}
+        return st
+
+    def dequantize(self):
+        """The bf16 packed weight (or Experts stack) of the same values, exact (hinm_mx4_dequantize)."""
+        lead = () if self.n_experts is None else (self.n_experts,)
+        bufs = {k: _empty((*lead, *s), t, self.device) for k, (s, t) in _packed_shapes(self.plan).items()}
+        out = (HinmPacked if self.n_experts is None else Experts)(self.plan, **bufs)
+        _call(self.device, library().hinm_mx4_dequantize, ctypes.byref(self.struct()), self.n_experts or 1,
+              ctypes.byref(out.struct()), _stream_ptr(self.device))
+        return out
+
+    def state_dict(self) -> dict:
+        """As HinmPacked.state_dict; n_experts 0 marks a single weight."""
+        p = self.plan
+        return {"format": "hinm-mx4", "format_version": HINM_MX4_FORMAT_VERSION, "n_experts": self.n_experts or 0,
+                "cout": p.cout, "cin": p.cin, "tile_rows": p.tile_rows, "t_s": p.t_s, "v_s": p.v_s,
+                **{k: getattr(self, k) for k in _MX4_BUFFERS}}
+
+    @classmethod
+    def from_state_dict(cls, sd: dict, device=None) -> "HinmMx4":
+        _check_format(sd, "hinm-mx4", HINM_MX4_FORMAT_VERSION)
+        p = plan(int(sd["cout"]), int(sd["cin"]), int(sd["tile_rows"]), float(sd["t_s"]), float(sd["v_s"]))
+        n = int(sd["n_experts"])
+        if n < 0 or p.tile_rows % 64:
+            raise ValueError("a stored 4-bit weight needs tile_rows % 64 == 0 and n_experts >= 0")
+        lead = (n,) if n else ()
+        want = {k: ((*lead, *s), t) for k, (s, t) in _mx4_shapes(p).items()}
+        return cls(p, **_checked_buffers(sd, want, device), n_experts=n or None)
+
+
+def quantize_mx4(packed) -> HinmMx4:
+    """Rounds the values of a packed weight or an Experts stack to 4-bit microscaled values
+    (hinm_mx4_quantize): blocks of 32 kept values of a row, E2M1 codes, one E8M0 scale.  Needs tile_rows a multiple
+    of 64.  Asynchronous on the current stream."""
+    if not isinstance(packed, (HinmPacked, Experts)):
+        raise ValueError("quantize_mx4 takes a HinmPacked weight or an Experts stack")
+    p, n = packed.plan, packed.n_experts if isinstance(packed, Experts) else None
+    lead = () if n is None else (n,)
+    dev = packed.device
+    out = HinmMx4(p, **{k: _empty((*lead, *s), t, dev) for k, (s, t) in _mx4_shapes(p).items()}, n_experts=n)
+    _call(dev, library().hinm_mx4_quantize, ctypes.byref(packed.struct()), n or 1, ctypes.byref(out.struct()),
+          _stream_ptr(dev))
+    return out
+
+
+def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
+    if packed.n_experts is not None:
+        raise ValueError("spmm takes one weight; multiply a stack with spmm_experts")
+    p, dev = packed.plan, packed.idx_24.device
+    ldx = _matrix(x, p.cin, None, dev, "x")
+    batch = x.shape[1]
+    if out is None:
+        out = torch.empty((p.cout, batch), dtype=torch.bfloat16, device=dev)
+    ldy = _matrix(out, p.cout, batch, dev, "out")
+    st, lib = packed.struct(), library()
+    needs = packed.__dict__["_ws_need"]
+    need = needs.get(batch)
+    if need is None:
+        n = ctypes.c_size_t()
+        _check(lib.hinm_spmm_mx4_workspace_bytes(ctypes.byref(p.raw), batch, ctypes.byref(n)))
+        need = needs[batch] = n.value
+    stream = _stream_ptr(dev)
+    if workspace is None:
+        workspace = _split_workspace(dev, stream, need)
+    _call(dev, lib.hinm_spmm_mx4, ctypes.byref(st), x.data_ptr(), batch, ldx, out.data_ptr(), ldy,
+          workspace.data_ptr() if workspace is not None else None, workspace.numel() if workspace is not None else 0,
+          stream)
+    return out
+
+
+def spmm_experts_workspace_bytes(p: Plan, n_experts: int, n_cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(library().hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), n_experts, n_cols, ctypes.byref(n)))
+    return n.value
+
+
+def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Every expert's product over its own columns (hinm_spmm_experts, or hinm_spmm_experts_mx4 for a quantised
+    stack): x bf16 [cin, columns] in the routing's order -> bf16 [cout, columns].
+
+    Columns that belong to no expert are left as they were in ``out`` (unspecified in a new one).  The ranges are
+    read on the device: no host synchronisation.  Asynchronous on the current stream; workspace as in spmm, but
+    while a graph is captured each call has its own."""
+    mx4 = isinstance(experts, HinmMx4)
+    if not (mx4 and experts.n_experts is not None) and not isinstance(experts, Experts):
+        raise ValueError("spmm_experts takes an Experts stack or a quantised one")
+    p, dev, e = experts.plan, experts.idx_24.device, experts.n_experts
+    ldx = _matrix(x, p.cin, None, dev, "x")
+    cols = x.shape[1]
+    if routing.counts.shape[0] != e:
+        raise ValueError(f"the routing has {routing.counts.shape[0]} experts, the stack {e}")
+    _index(routing.starts, (e + 1,), dev, "routing.starts")
+    _index(routing.counts, (e,), dev, "routing.counts")
+    if out is None:
+        out = torch.empty((p.cout, cols), dtype=torch.bfloat16, device=dev)
+    ldy = _matrix(out, p.cout, cols, dev, "out")
+    needs = experts.__dict__.setdefault("_expert_need", {})
+    need = needs.get(cols)
+    if need is None:
+        need = needs[cols] = spmm_experts_workspace_bytes(p, e, cols)
+    stream = _stream_ptr(dev)
+    if workspace is None:
+        workspace = _split_workspace(dev, stream, need)
+    lib = library()
+    _call(dev, lib.hinm_spmm_experts_mx4 if mx4 else lib.hinm_spmm_experts, ctypes.byref(experts.struct()), e,
+          x.data_ptr(), cols, ldx, routing.starts.data_ptr(), routing.counts.data_ptr(), out.data_ptr(), ldy,
+          workspace.data_ptr() if workspace is not None else None, workspace.numel() if workspace is not None else 0,
+          stream)
+    return out
+
+
 __all__ = ["HinmError", "HinmPacked", "Plan", "plan", "pack", "spmm", "spmm_noalloc", "Group", "spmm_group", "set_option", "get_option", "options",
            "OPTIONS", "translate_indices", "boundary_search", "plan_tiles", "pack_tiles", "boundary_search_tiles",
            "HinmTPacked", "TilePlan", "spmm_tiles_workspace_bytes", "alloc_packed",
            "pack_workspace_bytes",
-           "spmm_workspace_bytes", "library", "LIB_PATH", "EXPORTS"]
+           "spmm_workspace_bytes", "Routing", "route", "route_columns", "dispatch", "combine", "Experts",
+           "spmm_experts", "spmm_experts_workspace_bytes", "HinmMx4", "quantize_mx4",
+           "library", "LIB_PATH", "EXPORTS"]

@@ -1,0 +1,536 @@
+// Mixture-of-experts routing on [channels][tokens] activations: top-k experts
+// and the column order by expert (hinm_route), token columns into that order
+// (hinm_dispatch) and back (hinm_combine).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "hinm_device.h"
+#include "hinm_internal.h"
+
+using hinm::fail;
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Router.  Tokens are cut into blocks of kTok; a counting sort by expert needs
+// three facts per (token, choice): the expert's first column (a prefix sum
+// over the experts' totals), the choices of that expert in earlier blocks,
+// and those of earlier tokens in the same block.  topk_kernel finds the
+// choices and every block's expert counts; place_kernel adds the counts up
+// and writes the order.  Up to kTok tokens, one workgroup does both in one
+// launch; past kGroup blocks, sum_kernel first adds the counts of every kGroup
+// blocks, so that place_kernel reads n_blocks / kGroup + kGroup rows of them
+// and not n_blocks.
+// ---------------------------------------------------------------------------
+constexpr int kTok = 64;           // tokens of a block: one wave's lanes
+constexpr int kGroup = 32;         // blocks of a group
+constexpr int kRouteThreads = 256;
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ldl;
+  int n_tokens, n_experts, top_k, renormalize, align, bf16;
+  int32_t *ids, *slots, *starts, *counts, *src;
+  float* weights;
+  int64_t n_cols;
+  int n_blocks, n_groups;          // n_groups: 0 when the groups are not summed
+  int32_t *hist, *gsum;            // [n_blocks][n_experts], [n_groups][n_experts]
+};
+
+__device__ inline float load_logit(const RouteArgs& a, int e, int n) {
+  const int64_t at = (int64_t)e * a.ldl + n;
+  const float l = a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16)
+                         : static_cast<const float*>(a.logits)[at];
+  return l == l ? l : -INFINITY;                 // NaN: not eligible
+}
+
+// A list of the K largest logits so far, descending, equal ones in the order
+// they came in; -1 marks an empty place (no -inf logit enters).
+template <int K>
+struct Best {
+  float v[K];
+  int id[K];
+  __device__ inline void clear() {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      v[j] = -INFINITY;
+      id[j] = -1;
+    }
+  }
+  __device__ inline void add(float l, int e) {
+    if (!(l > v[K - 1])) return;
+    bool down = false;                           // once one entry moves, all after it do
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      down = down || l > v[j];
+      const float tv = v[j];
+      const int ti = id[j];
+      v[j] = down ? l : tv;
+      id[j] = down ? e : ti;
+      l = down ? tv : l;
+      e = down ? ti : e;
+    }
+  }
+};
+
+// Shared memory of the router's kernels, by phase.
+template <int K>
+struct RouteShared {
+  union {
+    struct {                                     // waves' lists and partial sums
+      float v[4][K][kTok];
+      int id[4][K][kTok];
+    };
+    unsigned long long mask[HINM_MAX_EXPERTS];   // per expert: the block's tokens that chose it
+  };
+  double sum[4][kTok];
+  float top[kTok];
+  int hist[HINM_MAX_EXPERTS];                    // the block's counts
+  int before[HINM_MAX_EXPERTS];                  // counts of earlier blocks, then the block's first column
+  int total[HINM_MAX_EXPERTS];
+  int start[HINM_MAX_EXPERTS + 1];
+  int part[kRouteThreads];
+};
+
+// Choices and weights of tokens b * kTok ..; their experts' counts in s.hist.
+// The four waves take a quarter of the experts each, one token a lane, and
+// the first wave merges the four lists (in expert order, so equal logits stay
+// in it).  Each thread ends up with its token's choices in the first wave.
+template <int K>
+__device__ inline void topk_block(const RouteArgs& a, RouteShared<K>& s, int b, Best<K>& best) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = b * kTok + lane;
+  const bool live = n < a.n_tokens;
+  const int per = (a.n_experts + 3) / 4;
+  const int e0 = min(wave * per, a.n_experts), e1 = min(e0 + per, a.n_experts);
+  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) s.hist[e] = 0;
+  best.clear();
+  if (live) {
+    int e = e0;
+    for (; e + 8 <= e1; e += 8) {                // eight loads in flight
+      float l[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) l[u] = load_logit(a, e + u, n);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) best.add(l[u], e + u);
+    }
+    for (; e < e1; ++e) best.add(load_logit(a, e, n), e);
+  }
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    s.v[wave][j][lane] = best.v[j];
+    s.id[wave][j][lane] = best.id[j];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+      for (int j = 0; j < K; ++j) best.add(s.v[w][j][lane], s.id[w][j][lane]);
+    s.top[lane] = best.v[0];
+  }
+  __syncthreads();
+  // exp(l - m), where l == m gives 1 also for infinities.  The sum over all
+  // experts is kept in 64 bits: up to 1024 terms, added one by one.
+  const float m = s.top[lane];
+  auto term = [&](float l) { return l == m ? 1.f : expf(l - m); };
+  if (!a.renormalize) {
+    double sum = 0.0;
+    if (live && m > -INFINITY)
+      for (int e = e0; e < e1; ++e) {
+        const float l = load_logit(a, e, n);
+        if (l > -INFINITY) sum += (double)term(l);
+      }
+    s.sum[wave][lane] = sum;
+    __syncthreads();
+  }
+  if (wave == 0 && live) {
+    double sum = 0.0;
+    if (a.renormalize) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (j < a.top_k && best.id[j] >= 0) sum += (double)term(best.v[j]);
+    } else {
+      sum = s.sum[0][lane] + s.sum[1][lane] + s.sum[2][lane] + s.sum[3][lane];
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (j < a.top_k) {
+        const int e = best.id[j];
+        a.ids[(int64_t)n * a.top_k + j] = e;
+        a.weights[(int64_t)n * a.top_k + j] = e >= 0 ? (float)((double)term(best.v[j]) / sum) : 0.f;
+        if (e >= 0) atomicAdd(&s.hist[e], 1);    // whole numbers: the order does not matter
+      }
+  }
+  __syncthreads();
+}
+
+// Every expert's total and first column, and the block's first column of
+// every expert (s.before); `rows` adds the counts to s.before and s.total.
+template <int K>
+__device__ inline void scan_experts(const RouteArgs& a, RouteShared<K>& s) {
+  // exclusive prefix sum of the padded totals: each thread a run of experts
+  const int per = (a.n_experts + kRouteThreads - 1) / kRouteThreads;
+  const int e0 = min((int)threadIdx.x * per, a.n_experts), e1 = min(e0 + per, a.n_experts);
+  const int mask = a.align - 1;
+  int run = 0;
+  for (int e = e0; e < e1; ++e) run += (s.total[e] + mask) & ~mask;
+  s.part[threadIdx.x] = run;
+  __syncthreads();
+  for (int d = 1; d < kRouteThreads; d *= 2) {
+    const int v = (int)threadIdx.x >= d ? s.part[threadIdx.x - d] : 0;
+    __syncthreads();
+    s.part[threadIdx.x] += v;
+    __syncthreads();
+  }
+  int at = s.part[threadIdx.x] - run;
+  for (int e = e0; e < e1; ++e) {
+    s.start[e] = at;
+    s.before[e] += at;
+    at += (s.total[e] + mask) & ~mask;
+  }
+  if (threadIdx.x == kRouteThreads - 1) s.start[a.n_experts] = s.part[kRouteThreads - 1];
+  __syncthreads();
+}
+
+// The order of block b's choices (ids of lane's token in `id`, -1 past the
+// batch), and this block's share of the table of ranges and of the columns
+// without a token.  s.before holds the first column of every expert for this
+// block.
+template <int K>
+__device__ inline void place_block(const RouteArgs& a, RouteShared<K>& s, int b, const int (&id)[K]) {
+  const int lane = threadIdx.x & 63;
+  const int n = b * kTok + lane;
+  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) s.mask[e] = 0ull;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (j < a.top_k && id[j] >= 0) atomicOr(&s.mask[id[j]], 1ull << lane);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64 && n < a.n_tokens) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (j < a.top_k) {
+        int slot = -1;
+        if (id[j] >= 0) {
+          slot = s.before[id[j]] + __popcll(s.mask[id[j]] & ((1ull << lane) - 1ull));
+          if (slot < a.n_cols) a.src[slot] = n;  // always, given the columns the host asked for
+        }
+        a.slots[(int64_t)n * a.top_k + j] = slot;
+      }
+  }
+  if (b == 0)
+    for (int e = threadIdx.x; e <= a.n_experts; e += kRouteThreads) {
+      a.starts[e] = s.start[e];
+      if (e < a.n_experts) a.counts[e] = s.total[e];
+    }
+  for (int e = b; e < a.n_experts; e += a.n_blocks)
+    for (int64_t c = s.start[e] + s.total[e] + threadIdx.x; c < min((int64_t)s.start[e + 1], a.n_cols);
+         c += kRouteThreads)
+      a.src[c] = -1;
+  for (int64_t c = s.start[a.n_experts] + (int64_t)b * kRouteThreads + threadIdx.x; c < a.n_cols;
+       c += (int64_t)a.n_blocks * kRouteThreads)
+    a.src[c] = -1;
+}
+
+template <int K, bool ONE>
+__global__ __launch_bounds__(kRouteThreads) void topk_kernel(RouteArgs a) {
+  __shared__ RouteShared<K> s;
+  Best<K> best;
+  topk_block<K>(a, s, blockIdx.x, best);
+  if constexpr (ONE) {
+    for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) {
+      s.total[e] = s.hist[e];
+      s.before[e] = 0;
+    }
+    __syncthreads();
+    scan_experts<K>(a, s);
+    const bool live = (int)threadIdx.x < a.n_tokens;
+#pragma unroll
+    for (int j = 0; j < K; ++j) best.id[j] = live ? best.id[j] : -1;
+    place_block<K>(a, s, 0, best.id);
+  } else {
+    for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads)
+      a.hist[(int64_t)blockIdx.x * a.n_experts + e] = s.hist[e];
+  }
+}
+
+// Sums of kGroup blocks' counts.
+__global__ __launch_bounds__(kRouteThreads) void sum_kernel(RouteArgs a) {
+  const int b0 = blockIdx.x * kGroup, b1 = min(b0 + kGroup, a.n_blocks);
+  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) {
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += a.hist[(int64_t)b * a.n_experts + e];
+    a.gsum[(int64_t)blockIdx.x * a.n_experts + e] = sum;
+  }
+}
+
+template <int K>
+__global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a) {
+  __shared__ RouteShared<K> s;
+  const int b = blockIdx.x, lane = threadIdx.x & 63, n = b * kTok + lane;
+  int id[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    id[j] = threadIdx.x < 64 && n < a.n_tokens && j < a.top_k ? a.ids[(int64_t)n * a.top_k + j] : -1;
+  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) s.total[e] = s.before[e] = 0;
+  __syncthreads();
+  // rows of counts: [0, mine) precede this block; all of them make the totals
+  auto rows = [&](const int32_t* t, int r0, int r1, int mine, bool total) {
+    const int64_t lo = (int64_t)r0 * a.n_experts, hi = (int64_t)r1 * a.n_experts;
+    for (int64_t q = lo + threadIdx.x; q < hi; q += kRouteThreads) {
+      const int v = t[q], r = (int)(q / a.n_experts), e = (int)(q - (int64_t)r * a.n_experts);
+      if (v) {
+        if (r < mine) atomicAdd(&s.before[e], v);
+        if (total) atomicAdd(&s.total[e], v);
+      }
+    }
+  };
+  if (a.n_groups) {
+    const int g = b / kGroup;
+    rows(a.gsum, 0, a.n_groups, g, true);
+    rows(a.hist, g * kGroup, b, b, false);
+  } else {
+    rows(a.hist, 0, a.n_blocks, b, true);
+  }
+  __syncthreads();
+  scan_experts<K>(a, s);
+  place_block<K>(a, s, b, id);
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch and combine: a thread owns eight adjacent columns (their sources
+// or slots stay in registers) and walks the channels.
+// ---------------------------------------------------------------------------
+constexpr int kMoveRows = 16;      // channels a workgroup walks
+
+__device__ inline void store8(uint16_t* dst, const uint16_t (&v)[8], int n, bool vec) {
+  if (vec && n >= 8) {
+    u32x4 w;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = (uint32_t)v[2 * u] | ((uint32_t)v[2 * u + 1] << 16);
+    *reinterpret_cast<u32x4*>(dst) = w;
+  } else {
+    for (int u = 0; u < 8 && u < n; ++u) dst[u] = v[u];
+  }
+}
+
+__global__ __launch_bounds__(256) void dispatch_kernel(const uint16_t* __restrict__ x, int64_t channels, int n_tokens,
+                                                       int64_t ldx, const int32_t* __restrict__ src, int64_t n_cols,
+                                                       uint16_t* __restrict__ xs, int64_t ldxs, int vec) {
+  const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (col >= n_cols) return;
+  const int left = (int)min((int64_t)8, n_cols - col);
+  int t[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) t[u] = u < left ? src[col + u] : -1;
+  for (int64_t c0 = (int64_t)blockIdx.y * kMoveRows; c0 < channels; c0 += (int64_t)gridDim.y * kMoveRows)
+    for (int64_t c = c0; c < min(c0 + kMoveRows, channels); ++c) {
+      uint16_t v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = t[u] >= 0 && t[u] < n_tokens ? x[c * ldx + t[u]] : (uint16_t)0;
+      store8(xs + c * ldxs + col, v, left, vec);
+    }
+}
+
+__global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ ys, int64_t channels,
+                                                      int64_t n_cols, int64_t ldys, const int32_t* __restrict__ slots,
+                                                      const float* __restrict__ weights, int n_tokens, int top_k,
+                                                      uint16_t* __restrict__ y, int64_t ldy) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= n_tokens) return;
+  for (int64_t c0 = (int64_t)blockIdx.y * kMoveRows; c0 < channels; c0 += (int64_t)gridDim.y * kMoveRows)
+    for (int64_t c = c0; c < min(c0 + kMoveRows, channels); ++c) {
+      float acc = 0.f;
+      for (int j = 0; j < top_k; ++j) {
+        const int64_t s = slots[(int64_t)n * top_k + j];
+        if (s >= 0 && s < n_cols)
+          acc = fmaf(weights[(int64_t)n * top_k + j], __uint_as_float((uint32_t)ys[c * ldys + s] << 16), acc);
+      }
+      y[c * ldy + n] = bf16_rne(acc);
+    }
+}
+
+int launch_status(const char* what) {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? HINM_OK : fail(HINM_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+int check_router(int64_t n_tokens, int32_t n_experts) {
+  if (n_tokens < 0) return fail(HINM_ESHAPE, "n_tokens=%lld is negative", (long long)n_tokens);
+  if (n_experts < 1 || n_experts > HINM_MAX_EXPERTS)
+    return fail(HINM_ESHAPE, "n_experts=%d; 1 to %d are supported", n_experts, HINM_MAX_EXPERTS);
+  if (n_tokens > (1 << 26)) return fail(HINM_ESHAPE, "n_tokens=%lld exceeds 2^26", (long long)n_tokens);
+  return HINM_OK;
+}
+
+int check_choice(int64_t n_tokens, int32_t n_experts, int32_t top_k, int32_t align) {
+  const int st = check_router(n_tokens, n_experts);
+  if (st) return st;
+  if (top_k < 1 || top_k > n_experts || top_k > HINM_MAX_TOP_K)
+    return fail(HINM_ESHAPE, "top_k=%d; 1 to min(n_experts=%d, %d) are supported", top_k, n_experts, HINM_MAX_TOP_K);
+  if (align < 1 || align > HINM_MAX_ALIGN || (align & (align - 1)))
+    return fail(HINM_EINVAL, "align=%d is not a power of two up to %d", align, HINM_MAX_ALIGN);
+  return HINM_OK;
+}
+
+int64_t route_columns(int64_t n_tokens, int32_t n_experts, int32_t top_k, int32_t align) {
+  const int64_t used = n_tokens * top_k;
+  return (used + std::min<int64_t>(n_experts, used) * (align - 1) + align - 1) / align * align;
+}
+
+// [counts of every block][sums of every kGroup blocks]
+void route_shape(int64_t n_tokens, int32_t n_experts, int* n_blocks, int* n_groups, size_t* bytes) {
+  *n_blocks = (int)std::max<int64_t>(1, (n_tokens + kTok - 1) / kTok);
+  *n_groups = *n_blocks > kGroup ? (*n_blocks + kGroup - 1) / kGroup : 0;
+  *bytes = *n_blocks == 1 ? 0 : (size_t)(*n_blocks + *n_groups) * n_experts * sizeof(int32_t);
+}
+
+template <int K>
+int launch_route(const RouteArgs& a, hipStream_t stream) {
+  if (a.n_blocks == 1) {
+    hipLaunchKernelGGL((topk_kernel<K, true>), dim3(1), dim3(kRouteThreads), 0, stream, a);
+    return launch_status("route");
+  }
+  hipLaunchKernelGGL((topk_kernel<K, false>), dim3(a.n_blocks), dim3(kRouteThreads), 0, stream, a);
+  int st = launch_status("route");
+  if (st) return st;
+  if (a.n_groups) {
+    hipLaunchKernelGGL(sum_kernel, dim3(a.n_groups), dim3(kRouteThreads), 0, stream, a);
+    st = launch_status("route");
+    if (st) return st;
+  }
+  hipLaunchKernelGGL(place_kernel<K>, dim3(a.n_blocks), dim3(kRouteThreads), 0, stream, a);
+  return launch_status("route");
+}
+
+}  // namespace
+
+extern "C" int hinm_route_columns(int64_t n_tokens, int32_t n_experts, int32_t top_k, int32_t align,
+                                  int64_t* n_cols) {
+  hinm::clear_error();
+  const int st = check_choice(n_tokens, n_experts, top_k, align);
+  if (st) return st;
+  if (!n_cols) return fail(HINM_EINVAL, "n_cols is NULL");
+  *n_cols = route_columns(n_tokens, n_experts, top_k, align);
+  return HINM_OK;
+}
+
+extern "C" int hinm_route_workspace_bytes(int64_t n_tokens, int32_t n_experts, size_t* bytes) {
+  hinm::clear_error();
+  const int st = check_router(n_tokens, n_experts);
+  if (st) return st;
+  if (!bytes) return fail(HINM_EINVAL, "bytes is NULL");
+  int nb, ng;
+  route_shape(n_tokens, n_experts, &nb, &ng, bytes);
+  return HINM_OK;
+}
+
+extern "C" int hinm_route(const void* logits, int32_t logits_type, int64_t n_tokens, int64_t ldl, int32_t n_experts,
+                          int32_t top_k, int32_t renormalize, int32_t align, int32_t* ids, float* weights,
+                          int32_t* slots, int32_t* starts, int32_t* counts, int32_t* src, int64_t n_cols,
+                          void* workspace, size_t workspace_bytes, void* stream_) {
+  hinm::clear_error();
+  int st = check_choice(n_tokens, n_experts, top_k, align);
+  if (st) return st;
+  if (logits_type != HINM_BF16 && logits_type != HINM_FP32)
+    return fail(HINM_EINVAL, "logits_type=%d is neither HINM_BF16 nor HINM_FP32", logits_type);
+  if (ldl < n_tokens) return fail(HINM_ESHAPE, "ldl=%lld is below n_tokens=%lld", (long long)ldl, (long long)n_tokens);
+  const int64_t need = route_columns(n_tokens, n_experts, top_k, align);
+  if (n_cols < need)
+    return fail(HINM_ESHAPE, "n_cols=%lld, this routing needs %lld", (long long)n_cols, (long long)need);
+  if (n_cols > INT32_MAX) return fail(HINM_ESHAPE, "n_cols=%lld does not fit in int32", (long long)n_cols);
+  if (!starts || !counts || (n_cols > 0 && !src) || (n_tokens > 0 && (!logits || !ids || !weights || !slots)))
+    return fail(HINM_EINVAL, "logits and the outputs must be non-NULL");
+  if (!hinm::aligned(logits, logits_type == HINM_BF16 ? 2 : 4)) return fail(HINM_EALIGN, "logits is misaligned");
+  for (const void* p : {(const void*)ids, (const void*)weights, (const void*)slots, (const void*)starts,
+                        (const void*)counts, (const void*)src})
+    if (!hinm::aligned(p, 4)) return fail(HINM_EALIGN, "the outputs must be 4-byte aligned");
+  RouteArgs a;
+  size_t bytes;
+  route_shape(n_tokens, n_experts, &a.n_blocks, &a.n_groups, &bytes);
+  if (bytes > 0) {
+    if (!workspace || workspace_bytes < bytes)
+      return fail(HINM_EWORKSPACE, "route workspace of %zu bytes given, %zu needed", workspace_bytes, bytes);
+    if (!hinm::aligned(workspace, 256)) return fail(HINM_EALIGN, "workspace is not 256-byte aligned");
+  }
+  st = hinm::ensure_device();
+  if (st) return st;
+  a.logits = logits;
+  a.ldl = ldl;
+  a.n_tokens = (int)n_tokens;
+  a.n_experts = n_experts;
+  a.top_k = top_k;
+  a.renormalize = renormalize != 0;
+  a.align = align;
+  a.bf16 = logits_type == HINM_BF16;
+  a.ids = ids;
+  a.weights = weights;
+  a.slots = slots;
+  a.starts = starts;
+  a.counts = counts;
+  a.src = src;
+  a.n_cols = n_cols;
+  a.hist = static_cast<int32_t*>(workspace);
+  a.gsum = a.hist ? a.hist + (size_t)a.n_blocks * n_experts : nullptr;
+  hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
+  if (top_k == 1) return launch_route<1>(a, stream);
+  if (top_k == 2) return launch_route<2>(a, stream);
+  if (top_k <= 4) return launch_route<4>(a, stream);
+  if (top_k <= 8) return launch_route<8>(a, stream);
+  return launch_route<16>(a, stream);
+}
+
+extern "C" int hinm_dispatch(const void* x_bf16, int64_t channels, int64_t n_tokens, int64_t ldx, const int32_t* src,
+                             int64_t n_cols, void* xs_bf16, int64_t ldxs, void* stream) {
+  hinm::clear_error();
+  if (channels < 0 || n_tokens < 0 || n_cols < 0)
+    return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must not be negative");
+  if (channels > INT32_MAX || n_tokens > INT32_MAX || n_cols > INT32_MAX)
+    return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must fit in int32");
+  if (ldx < n_tokens || ldxs < n_cols)
+    return fail(HINM_ESHAPE, "ldx=%lld must be >= n_tokens=%lld and ldxs=%lld >= n_cols=%lld", (long long)ldx,
+                (long long)n_tokens, (long long)ldxs, (long long)n_cols);
+  if (channels == 0 || n_cols == 0) return HINM_OK;
+  if (!src || !xs_bf16 || (n_tokens > 0 && !x_bf16)) return fail(HINM_EINVAL, "x, src and xs must be non-NULL");
+  if (!hinm::aligned(x_bf16, 2) || !hinm::aligned(xs_bf16, 2) || !hinm::aligned(src, 4))
+    return fail(HINM_EALIGN, "x and xs must be 2-byte aligned, src 4-byte aligned");
+  const int st = hinm::ensure_device();
+  if (st) return st;
+  const int vec = hinm::aligned(xs_bf16, 16) && ldxs % 8 == 0;
+  const dim3 grid((unsigned)((n_cols + 2047) / 2048), (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));
+  hipLaunchKernelGGL(dispatch_kernel, grid, dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                     static_cast<const uint16_t*>(x_bf16), channels, (int)n_tokens, ldx, src, n_cols,
+                     static_cast<uint16_t*>(xs_bf16), ldxs, vec);
+  return launch_status("dispatch");
+}
+
+extern "C" int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_cols, int64_t ldys, const int32_t* slots,
+                            const float* weights, int64_t n_tokens, int32_t top_k, void* y_bf16, int64_t ldy,
+                            void* stream) {
+  hinm::clear_error();
+  if (channels < 0 || n_tokens < 0 || n_cols < 0)
+    return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must not be negative");
+  if (channels > INT32_MAX || n_tokens > INT32_MAX || n_cols > INT32_MAX)
+    return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must fit in int32");
+  if (top_k < 1 || top_k > HINM_MAX_TOP_K) return fail(HINM_ESHAPE, "top_k=%d; 1 to %d are supported", top_k, HINM_MAX_TOP_K);
+  if (ldy < n_tokens || ldys < n_cols)
+    return fail(HINM_ESHAPE, "ldy=%lld must be >= n_tokens=%lld and ldys=%lld >= n_cols=%lld", (long long)ldy,
+                (long long)n_tokens, (long long)ldys, (long long)n_cols);
+  if (channels == 0 || n_tokens == 0) return HINM_OK;
+  if (!slots || !weights || !y_bf16 || (n_cols > 0 && !ys_bf16))
+    return fail(HINM_EINVAL, "ys, slots, weights and y must be non-NULL");
+  if (!hinm::aligned(ys_bf16, 2) || !hinm::aligned(y_bf16, 2) || !hinm::aligned(slots, 4) || !hinm::aligned(weights, 4))
+    return fail(HINM_EALIGN, "ys and y must be 2-byte aligned, slots and weights 4-byte aligned");
+  const int st = hinm::ensure_device();
+  if (st) return st;
+  const dim3 grid((unsigned)((n_tokens + 255) / 256), (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));
+  hipLaunchKernelGGL(combine_kernel, grid, dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+                     static_cast<const uint16_t*>(ys_bf16), channels, n_cols, ldys, slots, weights, (int)n_tokens, top_k,
+                     static_cast<uint16_t*>(y_bf16), ldy);
+  return launch_status("combine");
+}
