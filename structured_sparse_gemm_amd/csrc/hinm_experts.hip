@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "hinm_device.h"
 #include "hinm_internal.h"
@@ -113,6 +114,683 @@ __global__ __launch_bounds__(256) void experts_general_kernel(ExpArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Schedule shared by the fast kernels.  The ranges are known on the device
+// only, so every workgroup works out the same schedule from them: range e is
+// cut into ceil(n_e / NT) token blocks, numbered through all experts
+// (pre[e] = blocks before expert e), and an item is one token block times one
+// 64-row block.  When the items leave workgroups idle, each item's K-blocks
+// are dealt to `splits` workgroups and the partial sums meet in the workspace.
+// ---------------------------------------------------------------------------
+constexpr int kMaxWgs = 512;         // workgroups of a launch: two a compute unit
+
+__device__ inline int plan_blocks(const ExpArgs& a, int nt, int* pre) {
+  if (!a.starts) return (a.n_cols + nt - 1) / nt;
+  if (threadIdx.x < 64) {
+    int carry = 0;
+    for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
+      const int e = e0 + (int)threadIdx.x;
+      int lo = 0, hi = 0;
+      if (e < a.n_experts) range_of(a, e, lo, hi);
+      const int nb = (hi - lo + nt - 1) / nt;
+      int sum = nb;
+      for (int d = 1; d < 64; d *= 2) {
+        const int v = __shfl_up(sum, d);
+        sum += (int)threadIdx.x >= d ? v : 0;
+      }
+      if (e < a.n_experts) pre[e] = carry + sum - nb;
+      carry += __shfl(sum, 63);
+    }
+    if (threadIdx.x == 0) pre[a.n_experts] = carry;
+  }
+  __syncthreads();
+  return pre[a.n_experts];
+}
+
+// The expert that token block q belongs to: the last one with pre[e] <= q
+// (an empty expert shares its number with the next).
+__device__ inline int find_expert(const ExpArgs& a, const int* pre, int q) {
+  if (!a.starts) return 0;
+  int n = 0;
+  for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
+    const int e = e0 + (int)(threadIdx.x & 63);
+    const int c = __popcll(__ballot(e < a.n_experts && pre[min(e, a.n_experts)] <= q));
+    n += c;
+    if (c < 64) break;
+  }
+  return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)(uint32_t)bytes, kBufferWord3);
+}
+
+__device__ inline void x_buffer(const ExpArgs& a, __amdgpu_buffer_rsrc_t& x) {
+  x = buffer(a.x, ((int64_t)(a.cin - 1) * a.ldx + a.n_cols) * 2);
+}
+
+// The buffer of X ends with its last row's last column, and the range check
+// of a buffer load zeroes a dword that crosses the end: with an odd number of
+// elements from a chunk's start to that end, the very last element would read
+// as zero.  Whoever stages that element (row cin - 1, column n_cols - 1)
+// writes its value, read alone, over it.
+__device__ inline uint16_t last_element(const ExpArgs& a) { return a.x[(int64_t)(a.cin - 1) * a.ldx + a.n_cols - 1]; }
+
+// Partial sums of a split item: agent-scope stores and loads, as arrive()
+// explains; part[(item * splits + split)][n], added in split order by the last
+// workgroup to arrive.
+template <int N>
+__device__ inline bool join_splits(float (&v)[N], float* part, unsigned* counters, int item, int split, int splits,
+                                   int* s_last) {
+  float* my = part + (int64_t)(item * splits + split) * N * 256 + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < N; ++k) __hip_atomic_store(my + k * 256, v[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) *s_last = arrive(counters + item, splits);
+  __syncthreads();
+  if (!*s_last) return false;
+  const float* p0 = part + (int64_t)item * splits * N * 256 + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    float t[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      t[k] = __hip_atomic_load(p0 + (int64_t)s * N * 256 + k * 256, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += t[k];
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens an expert: bound by the packed bytes.  Workgroup = 64 rows x NT
+// tokens; its four waves deal the K-blocks among themselves and each works
+// alone - 64 rows x NT tokens of its blocks - so the main loop has no barrier
+// and every load is some blocks ahead: index words 2 D blocks, X rows, values
+// and metadata D blocks.  X rows pass through the wave's own LDS slot for the
+// transposed reads.  At the end the waves' sums meet in LDS, in wave order.
+// ---------------------------------------------------------------------------
+template <int NT>
+__device__ inline int x_granule(int p, int g) {     // 32-byte granule of position p, 16 tokens g; conflict-free
+  if constexpr (NT == 16) return p ^ (((p >> 3) & 1) << 2);
+  else if constexpr (NT == 32) return 2 * p + (g ^ ((p >> 3) & 1));
+  else return 4 * p + (g ^ (((p >> 1) & 1) | (((p >> 3) & 1) << 1)));
+}
+
+// One block's values and metadata of one lane: 64 rows' fragments f = 0..3.
+template <bool MX4>
+struct DecA {
+  u32x4 v[4];
+  uint32_t m[4];
+};
+template <>
+struct DecA<true> {
+  u32x4 v;                 // the codes of the four fragments
+  uint32_t scale;
+  uint32_t m[2];
+};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <bool MX4, int NT>
+__global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float* __restrict__ part,
+                                                                unsigned* __restrict__ counters) {
+  constexpr int NB = NT / 16;
+  constexpr int XL = NT / 8;                       // X loads a lane for 64 positions
+  constexpr int D = NT == 64 ? 2 : NT == 32 && !MX4 ? 3 : 4;   // blocks in flight (registers)
+  constexpr int kRed = NT + 4;                     // row pitch of the waves' sums (floats)
+  __shared__ __attribute__((aligned(16))) union {
+    uint16_t xs[4][64 * NT];
+    float red[4][64 * kRed];
+  } sh;
+  __shared__ int pre[HINM_MAX_EXPERTS + 1];
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, kc = lane >> 4;
+  const int nrb = a.rows / 64, n_rb = a.n_tiles * nrb, nblk = a.nkb_d + a.nkb_s;
+  uint16_t* const xs = sh.xs[wave];
+
+  const int items = plan_blocks(a, NT, pre) * n_rb;
+  // every wave keeps at least two blocks
+  int splits = 1;
+  while (items * splits * 2 <= (int)gridDim.x && nblk >= 16 * splits) splits *= 2;
+
+  // this lane's share of a block's X rows: position and first token of load j
+  int xpos[XL], xtok[XL];
+#pragma unroll
+  for (int j = 0; j < XL; ++j) {
+    const int chunk = 64 * j + lane, s = chunk >> 1;
+    int p, g;
+    if constexpr (NT == 16) p = s ^ (((s >> 3) & 1) << 2), g = 0;
+    else if constexpr (NT == 32) p = s >> 1, g = (s & 1) ^ ((p >> 3) & 1);
+    else p = s >> 2, g = (s & 3) ^ (((p >> 1) & 1) | (((p >> 3) & 1) << 1));
+    xpos[j] = p;
+    xtok[j] = 16 * g + 8 * (chunk & 1);
+  }
+  int ro[4][NB];                                   // transposed reads: positions 8 kc + i16 / 4 + {0, 4, 32, 36}
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      ro[k][nb] = x_granule<NT>(8 * kc + (i16 >> 2) + 4 * (k & 1) + 32 * (k >> 1), nb) * 16 + 4 * (i16 & 3);
+
+  __amdgpu_buffer_rsrc_t rx;
+  x_buffer(a, rx);
+  const uint32_t ldx_bytes = (uint32_t)a.ldx * 2u;
+
+  for (int work = blockIdx.x; work < items * splits; work += gridDim.x) {
+    const int item = work / splits, split = work % splits;
+    const int tb = item / n_rb, trb = item % n_rb, t = trb / nrb, rb = trb % nrb;
+    const int e = find_expert(a, pre, tb);
+    int lo, hi;
+    range_of(a, e, lo, hi);
+    const int n0 = lo + (tb - (a.starts ? pre[e] : 0)) * NT;
+    const __amdgpu_buffer_rsrc_t rvd = buffer(a.val_d + e * a.bytes_val_d, a.bytes_val_d);
+    const __amdgpu_buffer_rsrc_t rvs = buffer(a.val_s + e * a.bytes_val_s, a.bytes_val_s);
+    const __amdgpu_buffer_rsrc_t rm = buffer(a.meta + e * a.bytes_meta, a.bytes_meta);
+    const __amdgpu_buffer_rsrc_t rid = buffer(a.idx_d + e * a.n_idx_d, a.n_idx_d * 4);
+    const __amdgpu_buffer_rsrc_t ris = buffer(a.idx_s + e * a.n_idx_s, a.n_idx_s * 4);
+    __amdgpu_buffer_rsrc_t rsd, rss;
+    if constexpr (MX4) {
+      rsd = buffer(a.scale_d + e * (a.bytes_val_d / 16), a.bytes_val_d / 16);
+      rss = buffer(a.scale_s + e * (a.bytes_val_s / 16), a.bytes_val_s / 16);
+    }
+    uint32_t xcol[XL];                             // byte offset in a row, past the buffer for tokens past the range
+    // the loads that hold column n_cols - 1 (a lane's loads may be of several positions), as bits, and that
+    // column's place in such a load
+    uint32_t lastj = 0;
+    const int last_at = (a.n_cols - 1 - n0) & 7;
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+      const int n = n0 + xtok[j];
+      xcol[j] = n < hi ? (uint32_t)n * 2u : 0x80000000u;
+      if (n <= a.n_cols - 1 && n + 8 > a.n_cols - 1) lastj |= 1u << j;
+    }
+    const bool touch = n0 + NT >= a.n_cols;
+    const uint16_t xlast = touch ? last_element(a) : (uint16_t)0;
+
+    // worker v of nw takes blocks v, v + nw, ...
+    const int v = split * 4 + wave, nw = splits * 4;
+    const int cnt = v < nblk ? (nblk - v + nw - 1) / nw : 0;
+
+    f32x4 acc[4][NB];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[f][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    DecA<MX4> A[D];
+    u32x4 X[D][XL];
+    int I[D];
+    uint32_t P[D];                                 // loads that hold the buffer's last element
+
+    auto load_idx = [&](int i) -> int {
+      const int b = v + nw * i;
+      const bool dense = b < a.nkb_d;
+      const uint32_t at = dense ? (uint32_t)(t * a.nkb_d + b) * 32u + (lane & 31)
+                                : (uint32_t)(t * a.nkb_s + b - a.nkb_d) * 64u + lane;
+      return (int)__builtin_amdgcn_raw_buffer_load_b32(dense ? rid : ris, i < cnt ? at * 4u : kOob, 0, 0);
+    };
+    auto load_a = [&](int i, DecA<MX4>& A) {
+      const int b = v + nw * i;
+      const bool dense = b < a.nkb_d;
+      const uint32_t kb = dense ? (uint32_t)(t * a.nkb_d + b) : (uint32_t)(t * a.nkb_s + b - a.nkb_d);
+      const __amdgpu_buffer_rsrc_t rv = dense ? rvd : rvs;
+      if constexpr (MX4) {
+        const uint32_t u = i < cnt ? kb * (uint32_t)nrb + rb : 0u;
+        A.v = __builtin_amdgcn_raw_buffer_load_b128(rv, i < cnt ? u * 1024u + 256u * kc + 16u * i16 : kOob, 0, 0);
+        A.scale = __builtin_amdgcn_raw_buffer_load_b32(dense ? rsd : rss, i < cnt ? u * 64u + 4u * i16 : kOob, 0, 0);
+        const u32x2 m = __builtin_amdgcn_raw_buffer_load_b64(
+            rm, i < cnt && !dense ? u * 512u + 128u * kc + 8u * i16 : kOob, 0, 0);
+        A.m[0] = m[0];
+        A.m[1] = m[1];
+      } else {
+        const uint32_t row = kb * (uint32_t)a.rows + rb * 64u + i16;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          A.v[f] = __builtin_amdgcn_raw_buffer_load_b128(rv, i < cnt ? (row + 16u * f) * 64u + 16u * kc : kOob, 0, 0);
+          A.m[f] = __builtin_amdgcn_raw_buffer_load_b16(rm, i < cnt && !dense ? (row + 16u * f) * 8u + 2u * kc : kOob,
+                                                        0, 0);
+        }
+      }
+    };
+    // X rows of block i from its index word; a dense block fills 32 positions
+    auto load_x = [&](int i, int iw, u32x4 (&x)[XL], uint32_t& p) {
+      const bool dense = v + nw * i < a.nkb_d;
+      p = 0;
+#pragma unroll
+      for (int j = 0; j < XL; ++j) {
+        if (dense && 2 * j >= XL) break;
+        const int c = __shfl(iw, xpos[j]);
+        x[j] = __builtin_amdgcn_raw_buffer_load_b128(
+            rx, i < cnt && c >= 0 ? __umul24((uint32_t)c, ldx_bytes) + xcol[j] : kOob, 0, 0);
+        if (touch) p |= c == a.cin - 1 ? lastj & (1u << j) : 0u;
+      }
+    };
+    auto compute = [&](int i, const DecA<MX4>& A, const u32x4 (&x)[XL], uint32_t p) {
+      const bool dense = v + nw * i < a.nkb_d;
+#pragma unroll
+      for (int j = 0; j < XL; ++j) {
+        if (dense && 2 * j >= XL) break;
+        *reinterpret_cast<u32x4*>(xs + 8 * (64 * j + lane)) = x[j];
+      }
+      if (touch) {
+#pragma unroll
+        for (int j = 0; j < XL; ++j)
+          if (p & (1u << j)) xs[8 * (64 * j + lane) + last_at] = xlast;
+      }
+      __builtin_amdgcn_wave_barrier();
+      bf16x8 av[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        if constexpr (MX4) av[f] = mx4_expand(A.v[f], mx4_scale((A.scale >> (8 * f)) & 255u));
+        else av[f] = __builtin_bit_cast(bf16x8, A.v[f]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const v4i16 b0 = tr_read(xs + ro[0][nb]), b1 = tr_read(xs + ro[1][nb]);
+        const bf16x8 lo8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
+        if (dense) {
+#pragma unroll
+          for (int f = 0; f < 4; ++f) acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[f], lo8, acc[f][nb], 0, 0, 0);
+        } else {
+          const v4i16 b2 = tr_read(xs + ro[2][nb]), b3 = tr_read(xs + ro[3][nb]);
+          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b2, b3, 0, 1, 2, 3, 4, 5, 6, 7));
+          const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            int sidx;
+            if constexpr (MX4) sidx = (int)((A.m[f >> 1] >> (16 * (f & 1))) & 0xffffu);
+            else sidx = (int)A.m[f];
+            acc[f][nb] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[f], bv, acc[f][nb], sidx, 0, 0);
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    };
+
+#pragma unroll
+    for (int k = 0; k < D; ++k) I[k] = load_idx(k);
+#pragma unroll
+    for (int k = 0; k < D; ++k) load_a(k, A[k]);
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+      load_x(k, I[k], X[k], P[k]);
+      I[k] = load_idx(k + D);
+    }
+    for (int i = 0; i < cnt; i += D) {
+#pragma unroll
+      for (int k = 0; k < D; ++k) {
+        if (i + k < cnt) {
+          compute(i + k, A[k], X[k], P[k]);
+          load_a(i + k + D, A[k]);
+          load_x(i + k + D, I[k], X[k], P[k]);
+          I[k] = load_idx(i + k + 2 * D);
+        }
+      }
+    }
+
+    // the waves' sums, added in wave order; acc[f][nb][q] is row 16 f + 4 kc + q, token 16 nb + i16
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sh.red[wave][(16 * f + 4 * kc + q) * kRed + 16 * nb + i16] = acc[f][nb][q];
+    __syncthreads();
+    constexpr int OUT = NT / 4;                    // outputs a thread: row threadIdx.x / 4, OUT adjacent tokens
+    const int row = threadIdx.x >> 2, col = (threadIdx.x & 3) * OUT;
+    float sum[OUT];
+#pragma unroll
+    for (int q = 0; q < OUT; ++q) {
+      const int at = row * kRed + col + q;
+      sum[q] = sh.red[0][at] + sh.red[1][at] + sh.red[2][at] + sh.red[3][at];
+    }
+    if (splits == 1 || join_splits(sum, part, counters, item, split, splits, &s_last)) {
+      uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + row) * a.ldy + n0 + col;
+#pragma unroll
+      for (int q = 0; q < OUT; ++q)
+        if (n0 + col + q < hi) dst[q] = bf16_rne(sum[q]);
+    }
+    __syncthreads();                               // the sums share LDS with the next item's X rows
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens an expert: bound by the gathered X rows on their way through
+// the L2 caches.  Workgroup = 64 rows x NT tokens, four waves of 64 rows x
+// NT / 4 tokens.  X rows go straight from memory into a double-buffered LDS
+// tile (one block ahead); bf16 values follow through registers and LDS (two
+// blocks ahead), 4-bit values stay in registers - a wave's 64 rows of a block
+// are 1 KiB - and become bf16 there.  The regions' loops are separate, dense
+// on 32x32x16 MFMA, 2:4 on 32x32x32 SMFMAC.
+//
+// An XCD takes a contiguous range of the items, row blocks fastest, so its
+// workgroups share one token block's X rows in its L2.
+//
+// Tile layout: position p's row of 2 NT bytes, its 16-byte chunk c at chunk
+// c ^ 4 (p % 4), so that a 32-lane half of a transposed read covers every bank
+// once.
+// ---------------------------------------------------------------------------
+template <bool MX4>
+struct PreA {
+  u32x4 v;                  // 16 of the block's 64 x 64 bytes
+  uint32_t m;               // threads 0..127: a dword of its metadata
+};
+template <>
+struct PreA<true> {
+  u32x2 c[2];               // codes of K step s for the two 32-row tiles
+  uint32_t m[2];
+  uint32_t scale;
+};
+
+template <bool MX4, int NT>
+struct Pre {
+  static constexpr int TW = NT / 4;            // tokens of a wave
+  static constexpr int NTB = TW / 32;          // 32-token tiles of a wave
+  static constexpr int CPR = NT / 8;           // 16-byte chunks of a row
+  static constexpr int TILE = 64 * NT * 2;     // bytes of an X tile
+  static constexpr int ATILE = MX4 ? 16 : 64 * 64;
+};
+
+template <bool MX4, int NT, bool DENSE>
+__device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1, uint8_t* a0, uint8_t* a1,
+                                      uint32_t* m0, uint32_t* m1, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t rv,
+                                      __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rm, __amdgpu_buffer_rsrc_t ri,
+                                      int kbase, int nb, int rb, int n0, int hi, bool touch, uint16_t xlast,
+                                      f32x16 (&acc)[2][Pre<MX4, NT>::NTB]) {
+  using C = Pre<MX4, NT>;
+  constexpr int KPOS = DENSE ? 32 : 64;        // positions of a block
+  constexpr int RPW = KPOS / 4;                // positions a wave stages
+  constexpr int RPL = 64 / C::CPR;             // positions of one load
+  constexpr int NJ = RPW / RPL;                // X loads of a wave
+  constexpr int XROW = 2 * NT;
+  if (nb == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tok_w = wave * C::TW;
+  const int g = lane >> 4, i = lane & 15, kcb = g >> 1, kca = lane >> 5, m32 = lane & 31;
+  const int q = lane / C::CPR, sl = lane % C::CPR;
+  const int nrb = a.rows / 64;
+  const uint32_t ldx_bytes = (uint32_t)a.ldx * 2u;
+  uint32_t xoff[NJ];                           // source bytes in a row; past the buffer for tokens past the range
+  int xn[NJ];                                  // first token of the chunk
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    xn[j] = n0 + 8 * (sl ^ (4 * ((j * RPL + q) & 3)));
+    xoff[j] = xn[j] < hi ? (uint32_t)xn[j] * 2u : 0x80000000u;
+  }
+  const uint32_t ipos = (uint32_t)(wave * RPW + (lane % RPW));
+  auto load_idx = [&](int b) -> int {
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, ((uint32_t)(kbase + min(b, nb - 1)) * KPOS + ipos) * 4u, 0, 0);
+  };
+  auto spread_idx = [&](int iw, int (&ci)[NJ]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      int c = __builtin_amdgcn_readlane(iw, j * RPL);
+#pragma unroll
+      for (int u = 1; u < RPL; ++u) {
+        const int m = -(int)(q == u);            // a mask: a select would become a branch around the readlane
+        c = (c & ~m) | (__builtin_amdgcn_readlane(iw, j * RPL + u) & m);
+      }
+      ci[j] = c;
+    }
+  };
+  auto load_x = [&](const int (&ci)[NJ], uint8_t* xs) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      load_lds16(rx, xs + (wave * RPW + j * RPL) * XROW, ci[j] < 0 ? kOob : __umul24((uint32_t)ci[j], ldx_bytes) + xoff[j]);
+  };
+  auto patch_x = [&](const int (&ci)[NJ], uint8_t* xs) {   // the buffer's last element, see last_element()
+    if (touch) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (ci[j] == a.cin - 1 && xn[j] <= a.n_cols - 1 && xn[j] + 8 > a.n_cols - 1)
+          reinterpret_cast<uint16_t*>(xs + (wave * RPW + j * RPL) * XROW)[8 * lane + a.n_cols - 1 - xn[j]] = xlast;
+    }
+  };
+  const int arow = threadIdx.x >> 2;
+  const int aofs = arow * 64 + 16 * ((threadIdx.x & 3) ^ ((arow >> 2) & 3));
+  constexpr int PA = MX4 ? (DENSE ? 4 : 6) : (DENSE ? 2 : 3);   // loads a step issues after its X rows
+  auto load_a = [&](int b, PreA<MX4>& A) {
+    const uint32_t kb = (uint32_t)(kbase + min(b, nb - 1));
+    if constexpr (MX4) {
+      const uint32_t u = kb * (uint32_t)nrb + rb, at = 16u * (m32 & 15) + 8u * (m32 >> 4);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        A.c[s] = __builtin_amdgcn_raw_buffer_load_b64(rv, u * 1024u + 256u * (2 * s + kca) + at, 0, 0);
+        if constexpr (!DENSE) A.m[s] = __builtin_amdgcn_raw_buffer_load_b32(rm, u * 512u + 128u * (2 * s + kca) + at / 2, 0, 0);
+      }
+      A.scale = __builtin_amdgcn_raw_buffer_load_b16(rs, u * 64u + at / 4, 0, 0);
+    } else {
+      const uint32_t row = kb * (uint32_t)a.rows + rb * 64u;
+      A.v = __builtin_amdgcn_raw_buffer_load_b128(rv, row * 64u + 16u * threadIdx.x, 0, 0);
+      if constexpr (!DENSE)
+        A.m = __builtin_amdgcn_raw_buffer_load_b32(rm, threadIdx.x < 128 ? row * 8u + 4u * threadIdx.x : kOob, 0, 0);
+    }
+  };
+  auto store_a = [&](uint8_t* as, uint32_t* ms, const PreA<MX4>& A) {
+    if constexpr (!MX4) {
+      *reinterpret_cast<u32x4*>(as + aofs) = A.v;
+      if constexpr (!DENSE)
+        if (threadIdx.x < 128) ms[threadIdx.x] = A.m;
+    }
+  };
+  const uint32_t cb0 = (uint32_t)(tok_w / 8 + 2 * (g & 1) + ((i >> 1) & 1));
+  const uint32_t bsw = (uint32_t)(4 * ((i >> 2) & 3));
+  const bool idle = n0 + tok_w >= hi;          // none of this wave's tokens is in the range
+  auto compute = [&](const uint8_t* xb, const uint8_t* as, const uint32_t* ms, const PreA<MX4>& A) {
+    if (idle) return;
+    bf16x8 av[2][2];
+    int sidx[2][2];
+    if constexpr (MX4) {
+      const float sc[2] = {mx4_scale(A.scale & 255u), mx4_scale((A.scale >> 8) & 255u)};
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          av[r][s] = mx4_expand(A.c[s][r], sc[r]);
+          if constexpr (!DENSE) sidx[r][s] = (int)((A.m[s] >> (16 * r)) & 0xffffu);
+        }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 32 * r + m32;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          av[r][s] = *reinterpret_cast<const bf16x8*>(as + row * 64 + 16 * ((2 * s + kca) ^ ((row >> 2) & 3)));
+          if constexpr (!DENSE) sidx[r][s] = (int)reinterpret_cast<const uint16_t*>(ms)[row * 4 + 2 * s + kca];
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j) {
+        const uint8_t* base = xb + 16u * ((cb0 + 4u * j) ^ bsw) + 8u * (i & 1) +
+                              ((DENSE ? 16 : 32) * s + 8 * kcb + (i >> 2)) * XROW;
+        const v4i16 b0 = tr_read_b(base), b1 = tr_read_b(base + 4 * XROW);
+        const bf16x8 lo8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
+        if constexpr (DENSE) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[r][s], lo8, acc[r][j], 0, 0, 0);
+        } else {
+          const v4i16 b2 = tr_read_b(base + 16 * XROW), b3 = tr_read_b(base + 20 * XROW);
+          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b2, b3, 0, 1, 2, 3, 4, 5, 6, 7));
+          const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            acc[r][j] = __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av[r][s], bv, acc[r][j], sidx[r][s], 0, 0);
+        }
+      }
+  };
+
+  uint8_t* const xt[2] = {x0, x1};
+  uint8_t* const at[2] = {a0, a1};
+  uint32_t* const mt[2] = {m0, m1};
+  // Register sets by block number: values of four blocks (block b's are free
+  // once they are in LDS, at step b - 1, or multiplied, at step b), index
+  // words and spread indices of two.
+  constexpr int AHEAD = MX4 ? 3 : 4;
+  PreA<MX4> A[4];
+  int Iw[2], CI[2][NJ];
+  __syncthreads();                             // the tiles may still be read by the previous region
+  Iw[0] = load_idx(0);
+  Iw[1] = load_idx(1);
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) load_a(d, A[d]);
+  spread_idx(Iw[0], CI[0]);
+  spread_idx(Iw[1], CI[1]);
+  load_x(CI[0], xt[0]);
+  __builtin_amdgcn_sched_barrier(0);           // wait_vm counts the loads behind the X rows
+  Iw[0] = load_idx(2);
+  store_a(at[0], mt[0], A[0]);
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vm<1>();                                // block 0's X rows
+  patch_x(CI[0], xt[0]);
+  __syncthreads();
+  // Step b: X rows of b + 1 into the other tile, index word of b + 3, values
+  // of b + AHEAD; multiply b; the values of b + 1 into LDS; wait for the X rows.
+  auto step = [&](auto kk, int b) {
+    constexpr int k = decltype(kk)::value, k2 = k % 2;
+    __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
+    if (b + 1 < nb) load_x(CI[1 - k2], xt[1 - k2]);
+    __builtin_amdgcn_sched_barrier(0);
+    Iw[1 - k2] = load_idx(b + 3);
+    load_a(b + AHEAD, A[(k + AHEAD) % 4]);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
+    compute(xt[k2], at[k2], mt[k2], A[k]);
+    store_a(at[1 - k2], mt[1 - k2], A[(k + 1) % 4]);
+    spread_idx(Iw[k2], CI[k2]);                // indices of b + 2
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<PA>();
+    if (b + 1 < nb) patch_x(CI[1 - k2], xt[1 - k2]);
+    __syncthreads();
+  };
+  int b = 0;
+  for (; b + 4 <= nb; b += 4) {
+    step(std::integral_constant<int, 0>{}, b);
+    step(std::integral_constant<int, 1>{}, b + 1);
+    step(std::integral_constant<int, 2>{}, b + 2);
+    step(std::integral_constant<int, 3>{}, b + 3);
+  }
+  if (b < nb) step(std::integral_constant<int, 0>{}, b);
+  if (b + 1 < nb) step(std::integral_constant<int, 1>{}, b + 1);
+  if (b + 2 < nb) step(std::integral_constant<int, 2>{}, b + 2);
+}
+
+template <bool MX4, int NT>
+__global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, float* __restrict__ part,
+                                                                 unsigned* __restrict__ counters) {
+  using C = Pre<MX4, NT>;
+  // separate LDS objects: loads into one tile never hold up reads of the other
+  __shared__ __attribute__((aligned(16))) uint8_t xs_a[C::TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t xs_b[C::TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t as_a[C::ATILE];
+  __shared__ __attribute__((aligned(16))) uint8_t as_b[C::ATILE];
+  __shared__ __attribute__((aligned(16))) uint32_t ms_a[MX4 ? 4 : 128];
+  __shared__ __attribute__((aligned(16))) uint32_t ms_b[MX4 ? 4 : 128];
+  __shared__ int pre[HINM_MAX_EXPERTS + 1];
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nrb = a.rows / 64, n_rb = a.n_tiles * nrb;
+  const int tok_w = wave * C::TW;
+
+  const int items = plan_blocks(a, NT, pre) * n_rb;
+  int splits = 1;
+  while (splits < 4 && items * splits * 2 <= (int)gridDim.x && a.nkb_d + 2 * a.nkb_s >= 16 * splits) splits *= 2;
+  const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8, per_xcd = gridDim.x / 8;
+  const int w_lo = (int)((int64_t)xcd * items * splits / 8), w_hi = (int)((int64_t)(xcd + 1) * items * splits / 8);
+  __amdgpu_buffer_rsrc_t rx;
+  x_buffer(a, rx);
+
+  for (int work = w_lo + slot; work < w_hi; work += per_xcd) {
+    const int item = work / splits, split = work % splits;
+    const int tb = item / n_rb, trb = item % n_rb, t = trb / nrb, rb = trb % nrb;
+    const int e = find_expert(a, pre, tb);
+    int lo, hi;
+    range_of(a, e, lo, hi);
+    const int n0 = lo + (tb - (a.starts ? pre[e] : 0)) * NT;
+    const __amdgpu_buffer_rsrc_t rvd = buffer(a.val_d + e * a.bytes_val_d, a.bytes_val_d);
+    const __amdgpu_buffer_rsrc_t rvs = buffer(a.val_s + e * a.bytes_val_s, a.bytes_val_s);
+    const __amdgpu_buffer_rsrc_t rm = buffer(a.meta + e * a.bytes_meta, a.bytes_meta);
+    const __amdgpu_buffer_rsrc_t rid = buffer(a.idx_d + e * a.n_idx_d, a.n_idx_d * 4);
+    const __amdgpu_buffer_rsrc_t ris = buffer(a.idx_s + e * a.n_idx_s, a.n_idx_s * 4);
+    const __amdgpu_buffer_rsrc_t rsd = buffer(a.scale_d + e * (a.bytes_val_d / 16), MX4 ? a.bytes_val_d / 16 : 0);
+    const __amdgpu_buffer_rsrc_t rss = buffer(a.scale_s + e * (a.bytes_val_s / 16), MX4 ? a.bytes_val_s / 16 : 0);
+    const bool touch = n0 + NT >= a.n_cols;
+    const uint16_t xlast = touch ? last_element(a) : (uint16_t)0;
+
+    f32x16 acc[2][C::NTB];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[r][j][q] = 0.f;
+
+    // this split's share of the K-blocks, by cost: a dense block one unit, a 2:4 block two
+    const int units = a.nkb_d + 2 * a.nkb_s;
+    const int u0 = (int)((int64_t)split * units / splits), u1 = (int)((int64_t)(split + 1) * units / splits);
+    const int d0 = min(u0, a.nkb_d), d1 = min(u1, a.nkb_d);
+    const int k0 = (max(u0, a.nkb_d) - a.nkb_d) / 2, k1 = split + 1 == splits ? a.nkb_s : (max(u1, a.nkb_d) - a.nkb_d) / 2;
+    prefill_region<MX4, NT, true>(a, xs_a, xs_b, as_a, as_b, ms_a, ms_b, rx, rvd, rsd, rm, rid, t * a.nkb_d + d0, d1 - d0,
+                                  rb, n0, hi, touch, xlast, acc);
+    prefill_region<MX4, NT, false>(a, xs_a, xs_b, as_a, as_b, ms_a, ms_b, rx, rvs, rss, rm, ris, t * a.nkb_s + k0,
+                                   k1 - k0, rb, n0, hi, touch, xlast, acc);
+    __syncthreads();
+
+    if (splits > 1) {
+      float flat[2 * C::NTB * 16];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) flat[(r * C::NTB + j) * 16 + q] = acc[r][j][q];
+      if (!join_splits(flat, part, counters, item, split, splits, &s_last)) continue;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[r][j][q] = flat[(r * C::NTB + j) * 16 + q];
+    }
+
+    // Y through LDS, 32 rows at a time: acc[r][j][q] is row m = 8 (q / 4) + 4 (lane / 32) + q % 4 of tile r (bf16
+    // values: row 32 r + m; codes: row 32 (m / 16) + 16 r + m % 16), token tok_w + 32 j + lane % 32
+    uint16_t* const ya = reinterpret_cast<uint16_t*>(xs_a);
+    uint16_t* const yb = reinterpret_cast<uint16_t*>(xs_b);
+    const bool vec = (n0 % 8 == 0) && (a.ldy % 8 == 0) && ((uintptr_t)a.y % 16 == 0);
+    constexpr int PITCH = NT + 8;
+    static_assert(32 * PITCH * 2 <= C::TILE, "32 rows of Y fit a tile");
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          (r ? yb : ya)[(8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * PITCH + tok_w + 32 * j + (lane & 31)] = bf16_rne(acc[r][j][q]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 64 * C::CPR; c += 256) {
+      const int rr = c / C::CPR, n = n0 + 8 * (c % C::CPR), m = rr & 31, r = rr >> 5;
+      if (n >= hi) continue;
+      const int row = MX4 ? 32 * (m >> 4) + 16 * r + (m & 15) : rr;
+      uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + row) * a.ldy + n;
+      const uint16_t* src = (r ? yb : ya) + m * PITCH + 8 * (c % C::CPR);
+      if (vec && n + 8 <= hi) *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
+      else
+        for (int q = 0; q < 8 && n + q < hi; ++q) dst[q] = src[q];
+    }
+    __syncthreads();                           // the tiles are the next item's
+  }
+}
+
 int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n_cols, int64_t ldx, const void* y,
                int64_t ldy) {
   if (p.tile_rows % 64 != 0) return fail(HINM_ESHAPE, "tile_rows=%d is not a multiple of 64", p.tile_rows);
@@ -147,11 +825,20 @@ int check_bufs(const Buf* b, int n) {
   return HINM_OK;
 }
 
+// Tokens a workgroup takes: from the columns an expert has on average, so that
+// most experts fit one block while few lanes stay empty.
+int token_block(int32_t n_experts, int64_t n_cols) {
+  const int64_t avg = (n_cols + n_experts - 1) / n_experts;
+  return avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : avg < 1024 ? 128 : 256;
+}
+
+// Arrival counters, then the partial sums of at most kMaxWgs workgroups.
 int64_t ws_bytes(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
-  (void)p;
-  (void)n_experts;
-  (void)n_cols;
-  return 0;
+  if (n_cols == 0) return 0;
+  const int nt = token_block(n_experts, n_cols);
+  const int64_t fewest = (p.cout / 64) * (n_experts == 1 ? (n_cols + nt - 1) / nt : 1);   // items, if any
+  if (fewest * 2 > kMaxWgs) return 0;             // never split
+  return hinm::kWsCounterBytes + (int64_t)kMaxWgs * nt * 64 * 4;
 }
 
 // The product behind every entry point; `a` holds the weights' pointers.
@@ -182,9 +869,25 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
   a.nkb_d = p.n_dense_pad / HINM_KB_DENSE;
   a.nkb_s = p.n_24_pad / HINM_KB_24;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-  const int64_t tbs = n_cols / kGenTok + std::min<int64_t>(n_experts, n_cols);
-  const dim3 grid((unsigned)(p.cout / 64), (unsigned)std::min<int64_t>(tbs, 65535));
-  hipLaunchKernelGGL(experts_general_kernel<MX4>, grid, dim3(256), 0, stream, a);
+  // The fast kernels address X with 32-bit buffer offsets and 24-bit
+  // multiplies (row number, row pitch in bytes).
+  const int64_t x_bytes = ((int64_t)(p.cin - 1) * ldx + n_cols) * 2;
+  if (x_bytes >= ((int64_t)1 << 31) || ldx * 2 >= (1 << 24) || p.cin > (1 << 24)) {
+    const int64_t tbs = n_cols / kGenTok + std::min<int64_t>(n_experts, n_cols);
+    const dim3 grid((unsigned)(p.cout / 64), (unsigned)std::min<int64_t>(tbs, 65535));
+    hipLaunchKernelGGL(experts_general_kernel<MX4>, grid, dim3(256), 0, stream, a);
+  } else {
+    unsigned* ctr = static_cast<unsigned*>(workspace);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need ? hinm::kWsCounterBytes : 0));
+    const dim3 grid(kMaxWgs), block(256);
+    switch (token_block(n_experts, n_cols)) {
+      case 16: hipLaunchKernelGGL((experts_decode_kernel<MX4, 16>), grid, block, 0, stream, a, part, ctr); break;
+      case 32: hipLaunchKernelGGL((experts_decode_kernel<MX4, 32>), grid, block, 0, stream, a, part, ctr); break;
+      case 64: hipLaunchKernelGGL((experts_decode_kernel<MX4, 64>), grid, block, 0, stream, a, part, ctr); break;
+      case 128: hipLaunchKernelGGL((experts_prefill_kernel<MX4, 128>), grid, block, 0, stream, a, part, ctr); break;
+      default: hipLaunchKernelGGL((experts_prefill_kernel<MX4, 256>), grid, block, 0, stream, a, part, ctr); break;
+    }
+  }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? HINM_OK : fail(HINM_EHIP, "experts launch: %s", hipGetErrorString(e));
 }
