@@ -602,10 +602,13 @@ int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_cols, int64_t 
  * as they were.  Requires tile_rows % 64 == 0 and each expert's buffers below
  * 2^31 bytes (HINM_ESHAPE).  X rows that are 16-byte aligned (X aligned, ldx %
  * 8 == 0) and ranges that start at multiples of 8 (align 8 in hinm_route) run
- * fastest.  Rounding, determinism, workspace (zero-filled before its first
- * use, from hinm_spmm_experts_workspace_bytes) and errors as hinm_spmm; the
- * options of hinm_set_option do not apply. */
-int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_t n_experts, int64_t n_cols, size_t* bytes);
+ * fastest.  Rounding, determinism, workspace (its first 64 KiB zero-filled
+ * before its first use) and errors as hinm_spmm; the options of
+ * hinm_set_option do not apply.  The workspace query's x_aligned says whether
+ * X rows are 16-byte aligned; with unaligned rows and many tokens the
+ * workspace also holds a copy of X whose rows are. */
+int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_t n_experts, int64_t n_cols, int32_t x_aligned,
+                                      size_t* bytes);
 int hinm_spmm_experts(const hinm_packed_t* stack, int32_t n_experts, const void* x_bf16, int64_t n_cols, int64_t ldx,
                       const int32_t* starts, const int32_t* counts, void* y_bf16, int64_t ldy, void* workspace,
                       size_t workspace_bytes, void* stream);
@@ -670,7 +673,7 @@ int hinm_mx4_dequantize(const hinm_mx4_t* packed, int32_t n_weights, hinm_packed
 /* hinm_spmm and hinm_spmm_experts with 4-bit microscaled values.  Everything
  * but the values' format is as there; the workspaces are those of
  * hinm_spmm_mx4_workspace_bytes and hinm_spmm_experts_workspace_bytes. */
-int hinm_spmm_mx4_workspace_bytes(const hinm_plan_t* plan, int64_t batch, size_t* bytes);
+int hinm_spmm_mx4_workspace_bytes(const hinm_plan_t* plan, int64_t batch, int32_t x_aligned, size_t* bytes);
 int hinm_spmm_mx4(const hinm_mx4_t* packed, const void* x_bf16, int64_t batch, int64_t ldx, void* y_bf16, int64_t ldy,
                   void* workspace, size_t workspace_bytes, void* stream);
 int hinm_spmm_experts_mx4(const hinm_mx4_t* stack, int32_t n_experts, const void* x_bf16, int64_t n_cols, int64_t ldx,

@@ -142,14 +142,14 @@ def library() -> ctypes.CDLL:
                            ctypes.c_int),
             "hinm_dispatch": ([VP, I64, I64, I64, VP, I64, VP, I64, VP], ctypes.c_int),
             "hinm_combine": ([VP, I64, I64, I64, VP, VP, I64, I32, VP, I64, VP], ctypes.c_int),
-            "hinm_spmm_experts_workspace_bytes": ([P, I32, I64, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_spmm_experts_workspace_bytes": ([P, I32, I64, I32, ctypes.POINTER(S)], ctypes.c_int),
             "hinm_spmm_experts": ([ctypes.POINTER(PackedT), I32, VP, I64, I64, VP, VP, VP, I64, VP, S, VP],
                                   ctypes.c_int),
             "hinm_spmm_experts_mx4": ([ctypes.POINTER(Mx4T), I32, VP, I64, I64, VP, VP, VP, I64, VP, S, VP],
                                       ctypes.c_int),
             "hinm_mx4_quantize": ([ctypes.POINTER(PackedT), I32, ctypes.POINTER(Mx4T), VP], ctypes.c_int),
             "hinm_mx4_dequantize": ([ctypes.POINTER(Mx4T), I32, ctypes.POINTER(PackedT), VP], ctypes.c_int),
-            "hinm_spmm_mx4_workspace_bytes": ([P, I64, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_spmm_mx4_workspace_bytes": ([P, I64, I32, ctypes.POINTER(S)], ctypes.c_int),
             "hinm_spmm_mx4": ([ctypes.POINTER(Mx4T), VP, I64, I64, VP, I64, VP, S, VP], ctypes.c_int),
             "hinm_get_option": ([ctypes.c_int, ctypes.POINTER(I64)], ctypes.c_int),
             "hinm_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -812,10 +812,12 @@ def _call(dev: torch.device, fn, *args) -> None:
 
 def _split_workspace(dev: torch.device, stream: int, nbytes: int) -> Optional[torch.Tensor]:
     """The default workspace of an expert or 4-bit product: the stream's own, as for spmm; while a graph is
-    captured, a new one out of the graph's memory, cleared by a node of the graph, so that graphs captured on one
-    stream and replayed on several never share one."""
+    captured, a new one out of the graph's memory, its arrival counters cleared by a node of the graph, so that graphs
+    captured on one stream and replayed on several never share one."""
     if nbytes and torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws[:65536].zero_()
+        return ws
     return _workspace(dev, stream, nbytes)
 
 
@@ -1076,11 +1078,12 @@ def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
     ldy = _matrix(out, p.cout, batch, dev, "out")
     st, lib = packed.struct(), library()
     needs = packed.__dict__["_ws_need"]
-    need = needs.get(batch)
+    key = (batch, ldx % 8 == 0 and x.data_ptr() % 16 == 0)
+    need = needs.get(key)
     if need is None:
         n = ctypes.c_size_t()
-        _check(lib.hinm_spmm_mx4_workspace_bytes(ctypes.byref(p.raw), batch, ctypes.byref(n)))
-        need = needs[batch] = n.value
+        _check(lib.hinm_spmm_mx4_workspace_bytes(ctypes.byref(p.raw), batch, key[1], ctypes.byref(n)))
+        need = needs[key] = n.value
     stream = _stream_ptr(dev)
     if workspace is None:
         workspace = _split_workspace(dev, stream, need)
@@ -1090,9 +1093,10 @@ def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
     return out
 
 
-def spmm_experts_workspace_bytes(p: Plan, n_experts: int, n_cols: int) -> int:
+def spmm_experts_workspace_bytes(p: Plan, n_experts: int, n_cols: int, x_aligned: bool = True) -> int:
     n = ctypes.c_size_t()
-    _check(library().hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), n_experts, n_cols, ctypes.byref(n)))
+    _check(library().hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), n_experts, n_cols, int(x_aligned),
+                                                       ctypes.byref(n)))
     return n.value
 
 
@@ -1118,9 +1122,10 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
         out = torch.empty((p.cout, cols), dtype=torch.bfloat16, device=dev)
     ldy = _matrix(out, p.cout, cols, dev, "out")
     needs = experts.__dict__.setdefault("_expert_need", {})
-    need = needs.get(cols)
+    key = (cols, ldx % 8 == 0 and x.data_ptr() % 16 == 0)
+    need = needs.get(key)
     if need is None:
-        need = needs[cols] = spmm_experts_workspace_bytes(p, e, cols)
+        need = needs[key] = spmm_experts_workspace_bytes(p, e, *key)
     stream = _stream_ptr(dev)
     if workspace is None:
         workspace = _split_workspace(dev, stream, need)

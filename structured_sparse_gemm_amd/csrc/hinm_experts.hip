@@ -17,6 +17,9 @@ using hinm::fail;
 
 namespace {
 
+// 16 bytes at any 2-byte aligned address (one access: the device takes them).
+typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+
 // The weights of all experts and the activations.  Strides are per expert.
 struct ExpArgs {
   const uint8_t *val_d, *val_s;      // bf16 values or codes
@@ -27,6 +30,7 @@ struct ExpArgs {
   const uint16_t* x;
   uint16_t* y;
   int64_t ldx, ldy;
+  int x_end;                         // 1: the buffer of X ends with row cin - 1's last column (0: its rows are padded)
   const int32_t *starts, *counts;    // NULL: one range, all columns
   int n_experts, n_cols;
   int cin, cout, rows, n_tiles, nkb_d, nkb_s;
@@ -166,7 +170,7 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
 }
 
 __device__ inline void x_buffer(const ExpArgs& a, __amdgpu_buffer_rsrc_t& x) {
-  x = buffer(a.x, ((int64_t)(a.cin - 1) * a.ldx + a.n_cols) * 2);
+  x = buffer(a.x, ((int64_t)(a.cin - 1) * a.ldx + (a.x_end ? a.n_cols : a.ldx)) * 2);
 }
 
 // The buffer of X ends with its last row's last column, and the range check
@@ -462,9 +466,8 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
 // Many tokens an expert: bound by the gathered X rows on their way through
 // the L2 caches.  Workgroup = 64 rows x NT tokens, four waves of 64 rows x
 // NT / 4 tokens.  X rows go straight from memory into a double-buffered LDS
-// tile (one block ahead); bf16 values follow through registers and LDS (two
-// blocks ahead), 4-bit values stay in registers - a wave's 64 rows of a block
-// are 1 KiB - and become bf16 there.  The regions' loops are separate, dense
+// tile (one block ahead); values follow through registers and LDS (four
+// blocks ahead), 4-bit ones becoming bf16 on the way, once a workgroup.  The regions' loops are separate, dense
 // on 32x32x16 MFMA, 2:4 on 32x32x32 SMFMAC.
 //
 // An XCD takes a contiguous range of the items, row blocks fastest, so its
@@ -474,34 +477,31 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
 // c ^ 4 (p % 4), so that a 32-lane half of a transposed read covers every bank
 // once.
 // ---------------------------------------------------------------------------
+// Vector-memory instructions do not move across; everything else may.
+__device__ inline void vmem_fence() { __builtin_amdgcn_sched_barrier(0x78f); }
+
 template <bool MX4>
 struct PreA {
-  u32x4 v;                  // 16 of the block's 64 x 64 bytes
-  uint32_t m;               // threads 0..127: a dword of its metadata
-};
-template <>
-struct PreA<true> {
-  u32x2 c[2];               // codes of K step s for the two 32-row tiles
-  uint32_t m[2];
-  uint32_t scale;
+  typename std::conditional<MX4, uint32_t, u32x4>::type v;   // 8 values of a row
+  uint32_t scale;                                            // 4-bit: the row's scale byte
+  uint32_t m;                                                // threads 0..127: a dword of the block's metadata
 };
 
-template <bool MX4, int NT>
+template <int NT>
 struct Pre {
   static constexpr int TW = NT / 4;            // tokens of a wave
   static constexpr int NTB = TW / 32;          // 32-token tiles of a wave
   static constexpr int CPR = NT / 8;           // 16-byte chunks of a row
   static constexpr int TILE = 64 * NT * 2;     // bytes of an X tile
-  static constexpr int ATILE = MX4 ? 16 : 64 * 64;
 };
 
-template <bool MX4, int NT, bool DENSE>
+template <bool MX4, int NT, bool DENSE, bool LAST>
 __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1, uint8_t* a0, uint8_t* a1,
                                       uint32_t* m0, uint32_t* m1, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t rv,
                                       __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rm, __amdgpu_buffer_rsrc_t ri,
-                                      int kbase, int nb, int rb, int n0, int hi, bool touch, uint16_t xlast,
-                                      f32x16 (&acc)[2][Pre<MX4, NT>::NTB]) {
-  using C = Pre<MX4, NT>;
+                                      int kbase, int nb, int rot, int rb, int n0, int hi, uint16_t xlast,
+                                      f32x16 (&acc)[2][Pre<NT>::NTB]) {
+  using C = Pre<NT>;
   constexpr int KPOS = DENSE ? 32 : 64;        // positions of a block
   constexpr int RPW = KPOS / 4;                // positions a wave stages
   constexpr int RPL = 64 / C::CPR;             // positions of one load
@@ -523,8 +523,12 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
     xoff[j] = xn[j] < hi ? (uint32_t)xn[j] * 2u : 0x80000000u;
   }
   const uint32_t ipos = (uint32_t)(wave * RPW + (lane % RPW));
+  auto block = [&](int b) -> uint32_t {        // the order starts at block rot and wraps around
+    b = min(b, nb - 1) + rot;
+    return (uint32_t)(kbase + (b < nb ? b : b - nb));
+  };
   auto load_idx = [&](int b) -> int {
-    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, ((uint32_t)(kbase + min(b, nb - 1)) * KPOS + ipos) * 4u, 0, 0);
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, (block(b) * KPOS + ipos) * 4u, 0, 0);
   };
   auto spread_idx = [&](int iw, int (&ci)[NJ]) {
 #pragma unroll
@@ -544,26 +548,26 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
       load_lds16(rx, xs + (wave * RPW + j * RPL) * XROW, ci[j] < 0 ? kOob : __umul24((uint32_t)ci[j], ldx_bytes) + xoff[j]);
   };
   auto patch_x = [&](const int (&ci)[NJ], uint8_t* xs) {   // the buffer's last element, see last_element()
-    if (touch) {
+    if constexpr (LAST) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         if (ci[j] == a.cin - 1 && xn[j] <= a.n_cols - 1 && xn[j] + 8 > a.n_cols - 1)
           reinterpret_cast<uint16_t*>(xs + (wave * RPW + j * RPL) * XROW)[8 * lane + a.n_cols - 1 - xn[j]] = xlast;
     }
   };
-  const int arow = threadIdx.x >> 2;
-  const int aofs = arow * 64 + 16 * ((threadIdx.x & 3) ^ ((arow >> 2) & 3));
-  constexpr int PA = MX4 ? (DENSE ? 4 : 6) : (DENSE ? 2 : 3);   // loads a step issues after its X rows
+  // the row and chunk of 8 values that this thread brings: in the order of the packed bytes
+  const int arow = MX4 ? 16 * (threadIdx.x & 3) + ((threadIdx.x >> 2) & 15) : threadIdx.x >> 2;
+  const int achk = MX4 ? wave : threadIdx.x & 3;
+  const int aofs = arow * 64 + 16 * (achk ^ ((arow >> 2) & 3));
+  constexpr int PA = (MX4 ? 3 : 2) + (DENSE ? 0 : 1);       // loads a step issues after its X rows
   auto load_a = [&](int b, PreA<MX4>& A) {
-    const uint32_t kb = (uint32_t)(kbase + min(b, nb - 1));
+    const uint32_t kb = block(b);
     if constexpr (MX4) {
-      const uint32_t u = kb * (uint32_t)nrb + rb, at = 16u * (m32 & 15) + 8u * (m32 >> 4);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        A.c[s] = __builtin_amdgcn_raw_buffer_load_b64(rv, u * 1024u + 256u * (2 * s + kca) + at, 0, 0);
-        if constexpr (!DENSE) A.m[s] = __builtin_amdgcn_raw_buffer_load_b32(rm, u * 512u + 128u * (2 * s + kca) + at / 2, 0, 0);
-      }
-      A.scale = __builtin_amdgcn_raw_buffer_load_b16(rs, u * 64u + at / 4, 0, 0);
+      const uint32_t u = kb * (uint32_t)nrb + rb;
+      A.v = __builtin_amdgcn_raw_buffer_load_b32(rv, u * 1024u + 4u * threadIdx.x, 0, 0);
+      A.scale = __builtin_amdgcn_raw_buffer_load_b8(rs, u * 64u + lane, 0, 0);
+      if constexpr (!DENSE)
+        A.m = __builtin_amdgcn_raw_buffer_load_b32(rm, threadIdx.x < 128 ? u * 512u + 4u * threadIdx.x : kOob, 0, 0);
     } else {
       const uint32_t row = kb * (uint32_t)a.rows + rb * 64u;
       A.v = __builtin_amdgcn_raw_buffer_load_b128(rv, row * 64u + 16u * threadIdx.x, 0, 0);
@@ -572,37 +576,25 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
     }
   };
   auto store_a = [&](uint8_t* as, uint32_t* ms, const PreA<MX4>& A) {
-    if constexpr (!MX4) {
-      *reinterpret_cast<u32x4*>(as + aofs) = A.v;
-      if constexpr (!DENSE)
-        if (threadIdx.x < 128) ms[threadIdx.x] = A.m;
-    }
+    if constexpr (MX4) *reinterpret_cast<bf16x8*>(as + aofs) = mx4_expand(A.v, mx4_scale(A.scale));
+    else *reinterpret_cast<u32x4*>(as + aofs) = A.v;
+    if constexpr (!DENSE)
+      if (threadIdx.x < 128) ms[threadIdx.x] = A.m;
   };
   const uint32_t cb0 = (uint32_t)(tok_w / 8 + 2 * (g & 1) + ((i >> 1) & 1));
   const uint32_t bsw = (uint32_t)(4 * ((i >> 2) & 3));
-  const bool idle = n0 + tok_w >= hi;          // none of this wave's tokens is in the range
-  auto compute = [&](const uint8_t* xb, const uint8_t* as, const uint32_t* ms, const PreA<MX4>& A) {
-    if (idle) return;
+  auto compute = [&](const uint8_t* xb, const uint8_t* as, const uint32_t* ms) {
     bf16x8 av[2][2];
     int sidx[2][2];
-    if constexpr (MX4) {
-      const float sc[2] = {mx4_scale(A.scale & 255u), mx4_scale((A.scale >> 8) & 255u)};
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
+      const int row = 32 * r + m32;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          av[r][s] = mx4_expand(A.c[s][r], sc[r]);
-          if constexpr (!DENSE) sidx[r][s] = (int)((A.m[s] >> (16 * r)) & 0xffffu);
-        }
-    } else {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 32 * r + m32;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          av[r][s] = *reinterpret_cast<const bf16x8*>(as + row * 64 + 16 * ((2 * s + kca) ^ ((row >> 2) & 3)));
-          if constexpr (!DENSE) sidx[r][s] = (int)reinterpret_cast<const uint16_t*>(ms)[row * 4 + 2 * s + kca];
-        }
+      for (int s = 0; s < 2; ++s) {
+        const int q = 2 * s + kca;             // values and metadata 8q.. of the row
+        av[r][s] = *reinterpret_cast<const bf16x8*>(as + row * 64 + 16 * (q ^ ((row >> 2) & 3)));
+        if constexpr (!DENSE)
+          sidx[r][s] = (int)reinterpret_cast<const uint16_t*>(ms)[MX4 ? q * 64 + (row & 15) * 4 + (row >> 4) : row * 4 + q];
       }
     }
 #pragma unroll
@@ -632,10 +624,9 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
   uint8_t* const at[2] = {a0, a1};
   uint32_t* const mt[2] = {m0, m1};
   // Register sets by block number: values of four blocks (block b's are free
-  // once they are in LDS, at step b - 1, or multiplied, at step b), index
-  // words and spread indices of two.
-  constexpr int AHEAD = MX4 ? 3 : 4;
-  PreA<MX4> A[4];
+  // once they are in LDS, at step b - 1), index words and spread indices of two.
+  constexpr int AHEAD = 4;
+  PreA<MX4> A[AHEAD];
   int Iw[2], CI[2][NJ];
   __syncthreads();                             // the tiles may still be read by the previous region
   Iw[0] = load_idx(0);
@@ -645,10 +636,10 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
   spread_idx(Iw[0], CI[0]);
   spread_idx(Iw[1], CI[1]);
   load_x(CI[0], xt[0]);
-  __builtin_amdgcn_sched_barrier(0);           // wait_vm counts the loads behind the X rows
+  vmem_fence();                                // wait_vm counts the loads behind the X rows
   Iw[0] = load_idx(2);
   store_a(at[0], mt[0], A[0]);
-  __builtin_amdgcn_sched_barrier(0);
+  vmem_fence();
   wait_vm<1>();                                // block 0's X rows
   patch_x(CI[0], xt[0]);
   __syncthreads();
@@ -658,15 +649,15 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
     constexpr int k = decltype(kk)::value, k2 = k % 2;
     __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
     if (b + 1 < nb) load_x(CI[1 - k2], xt[1 - k2]);
-    __builtin_amdgcn_sched_barrier(0);
+    vmem_fence();
     Iw[1 - k2] = load_idx(b + 3);
-    load_a(b + AHEAD, A[(k + AHEAD) % 4]);
-    __builtin_amdgcn_sched_barrier(0);
+    load_a(b + AHEAD, A[k]);
+    vmem_fence();
     __builtin_amdgcn_s_setprio(0);
-    compute(xt[k2], at[k2], mt[k2], A[k]);
+    compute(xt[k2], at[k2], mt[k2]);
     store_a(at[1 - k2], mt[1 - k2], A[(k + 1) % 4]);
     spread_idx(Iw[k2], CI[k2]);                // indices of b + 2
-    __builtin_amdgcn_sched_barrier(0);
+    vmem_fence();
     wait_vm<PA>();
     if (b + 1 < nb) patch_x(CI[1 - k2], xt[1 - k2]);
     __syncthreads();
@@ -686,14 +677,14 @@ __device__ inline void prefill_region(const ExpArgs& a, uint8_t* x0, uint8_t* x1
 template <bool MX4, int NT>
 __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, float* __restrict__ part,
                                                                  unsigned* __restrict__ counters) {
-  using C = Pre<MX4, NT>;
+  using C = Pre<NT>;
   // separate LDS objects: loads into one tile never hold up reads of the other
   __shared__ __attribute__((aligned(16))) uint8_t xs_a[C::TILE];
   __shared__ __attribute__((aligned(16))) uint8_t xs_b[C::TILE];
-  __shared__ __attribute__((aligned(16))) uint8_t as_a[C::ATILE];
-  __shared__ __attribute__((aligned(16))) uint8_t as_b[C::ATILE];
-  __shared__ __attribute__((aligned(16))) uint32_t ms_a[MX4 ? 4 : 128];
-  __shared__ __attribute__((aligned(16))) uint32_t ms_b[MX4 ? 4 : 128];
+  __shared__ __attribute__((aligned(16))) uint8_t as_a[64 * 64];
+  __shared__ __attribute__((aligned(16))) uint8_t as_b[64 * 64];
+  __shared__ __attribute__((aligned(16))) uint32_t ms_a[128];
+  __shared__ __attribute__((aligned(16))) uint32_t ms_b[128];
   __shared__ int pre[HINM_MAX_EXPERTS + 1];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63;
@@ -723,7 +714,9 @@ __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, floa
     const __amdgpu_buffer_rsrc_t ris = buffer(a.idx_s + e * a.n_idx_s, a.n_idx_s * 4);
     const __amdgpu_buffer_rsrc_t rsd = buffer(a.scale_d + e * (a.bytes_val_d / 16), MX4 ? a.bytes_val_d / 16 : 0);
     const __amdgpu_buffer_rsrc_t rss = buffer(a.scale_s + e * (a.bytes_val_s / 16), MX4 ? a.bytes_val_s / 16 : 0);
-    const bool touch = n0 + NT >= a.n_cols;
+    // the token block that holds the buffer's last element, where a 4-byte load of a chunk may cross the end; its
+    // own instantiation: the check costs 11% (11008x4096, 2048 tokens: 104 -> 117 us with it in every block)
+    const bool touch = n0 + NT >= a.n_cols && ((a.n_cols - n0) & 1) && a.x_end;
     const uint16_t xlast = touch ? last_element(a) : (uint16_t)0;
 
     f32x16 acc[2][C::NTB];
@@ -739,10 +732,18 @@ __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, floa
     const int u0 = (int)((int64_t)split * units / splits), u1 = (int)((int64_t)(split + 1) * units / splits);
     const int d0 = min(u0, a.nkb_d), d1 = min(u1, a.nkb_d);
     const int k0 = (max(u0, a.nkb_d) - a.nkb_d) / 2, k1 = split + 1 == splits ? a.nkb_s : (max(u1, a.nkb_d) - a.nkb_d) / 2;
-    prefill_region<MX4, NT, true>(a, xs_a, xs_b, as_a, as_b, ms_a, ms_b, rx, rvd, rsd, rm, rid, t * a.nkb_d + d0, d1 - d0,
-                                  rb, n0, hi, touch, xlast, acc);
-    prefill_region<MX4, NT, false>(a, xs_a, xs_b, as_a, as_b, ms_a, ms_b, rx, rvs, rss, rm, ris, t * a.nkb_s + k0,
-                                   k1 - k0, rb, n0, hi, touch, xlast, acc);
+    // tiles, and the token blocks that the XCDs work on at one time, start their loops at different blocks, so
+    // that they do not all read the same rows of X or the same values at once
+    auto turn = [&](int n) { return n > 0 ? (int)(((int64_t)t * n / a.n_tiles + (int64_t)((3 * tb) & 7) * n / 8) % n) : 0; };
+    auto regions = [&](auto last) {
+      constexpr bool LAST = decltype(last)::value;
+      prefill_region<MX4, NT, true, LAST>(a, xs_a, xs_b, as_a, as_b, ms_a, ms_b, rx, rvd, rsd, rm, rid, t * a.nkb_d + d0,
+                                          d1 - d0, turn(d1 - d0), rb, n0, hi, xlast, acc);
+      prefill_region<MX4, NT, false, LAST>(a, xs_a, xs_b, as_a, as_b, ms_a, ms_b, rx, rvs, rss, rm, ris,
+                                           t * a.nkb_s + k0, k1 - k0, turn(k1 - k0), rb, n0, hi, xlast, acc);
+    };
+    if (touch) regions(std::true_type{});
+    else regions(std::false_type{});
     __syncthreads();
 
     if (splits > 1) {
@@ -762,11 +763,9 @@ __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, floa
           for (int q = 0; q < 16; ++q) acc[r][j][q] = flat[(r * C::NTB + j) * 16 + q];
     }
 
-    // Y through LDS, 32 rows at a time: acc[r][j][q] is row m = 8 (q / 4) + 4 (lane / 32) + q % 4 of tile r (bf16
-    // values: row 32 r + m; codes: row 32 (m / 16) + 16 r + m % 16), token tok_w + 32 j + lane % 32
+    // Y through LDS, 32 rows at a time: acc[r][j][q] is row m = 8 (q / 4) + 4 (lane / 32) + q % 4 of tile r, token tok_w + 32 j + lane % 32
     uint16_t* const ya = reinterpret_cast<uint16_t*>(xs_a);
     uint16_t* const yb = reinterpret_cast<uint16_t*>(xs_b);
-    const bool vec = (n0 % 8 == 0) && (a.ldy % 8 == 0) && ((uintptr_t)a.y % 16 == 0);
     constexpr int PITCH = NT + 8;
     static_assert(32 * PITCH * 2 <= C::TILE, "32 rows of Y fit a tile");
 #pragma unroll
@@ -777,18 +776,41 @@ __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, floa
         for (int q = 0; q < 16; ++q)
           (r ? yb : ya)[(8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * PITCH + tok_w + 32 * j + (lane & 31)] = bf16_rne(acc[r][j][q]);
     __syncthreads();
-    for (int c = threadIdx.x; c < 64 * C::CPR; c += 256) {
-      const int rr = c / C::CPR, n = n0 + 8 * (c % C::CPR), m = rr & 31, r = rr >> 5;
-      if (n >= hi) continue;
-      const int row = MX4 ? 32 * (m >> 4) + 16 * r + (m & 15) : rr;
-      uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + row) * a.ldy + n;
-      const uint16_t* src = (r ? yb : ya) + m * PITCH + 8 * (c % C::CPR);
-      if (vec && n + 8 <= hi) *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
-      else
-        for (int q = 0; q < 8 && n + q < hi; ++q) dst[q] = src[q];
+    // 16-byte stores at 16-byte aligned addresses whatever the row's alignment: piece 0 of a row is what precedes
+    // its first aligned address (unaligned stores made 11008 rows of 2047 tokens 14 us slower)
+    for (int c = threadIdx.x; c < 64 * (C::CPR + 1); c += 256) {
+      const int rr = c / (C::CPR + 1), k = c % (C::CPR + 1), m = rr & 31;
+      uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + rr) * a.ldy + n0;
+      const int head = (int)(-(uintptr_t)dst / 2 % 8);
+      const int at = k == 0 ? 0 : head + 8 * (k - 1), end = min(k == 0 ? head : at + 8, min(hi - n0, NT));
+      const uint16_t* src = ((rr >> 5) ? yb : ya) + m * PITCH;
+      if (end - at == 8 && at % 8 == 0) {
+        *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
+      } else if (end - at == 8) {
+        u32x4 v;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = (uint32_t)src[at + 2 * u] | ((uint32_t)src[at + 2 * u + 1] << 16);
+        *reinterpret_cast<u32x4*>(dst + at) = v;
+      } else {
+        for (int q = at; q < end; ++q) dst[q] = src[q];
+      }
     }
     __syncthreads();                           // the tiles are the next item's
   }
+}
+
+// X rows into the workspace at a 16-byte aligned pitch, zeros behind them.
+__global__ __launch_bounds__(256) void align_kernel(const uint16_t* __restrict__ x, int64_t ldx, int n_cols,
+                                                    uint16_t* __restrict__ out, int64_t ld, int rows) {
+  for (int r = blockIdx.y; r < rows; r += gridDim.y)
+    for (int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; n < ld; n += (int64_t)gridDim.x * 2048) {
+      const uint16_t* src = x + r * ldx + n;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (n + 8 <= n_cols) v = *reinterpret_cast<const any_u32x4*>(src);
+      else
+        for (int u = 0; u < 8 && n + u < n_cols; ++u) v[u >> 1] |= (uint32_t)src[u] << (16 * (u & 1));
+      *reinterpret_cast<u32x4*>(out + r * ld + n) = v;
+    }
 }
 
 int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n_cols, int64_t ldx, const void* y,
@@ -829,16 +851,28 @@ int check_bufs(const Buf* b, int n) {
 // most experts fit one block while few lanes stay empty.
 int token_block(int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
-  return avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : avg < 1024 ? 128 : 256;
+  return avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : avg < 256 ? 128 : 256;
 }
 
-// Arrival counters, then the partial sums of at most kMaxWgs workgroups.
-int64_t ws_bytes(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
-  if (n_cols == 0) return 0;
+// Workspace: arrival counters and the partial sums of at most kMaxWgs
+// workgroups, where a launch may split; behind them, for the kernel of many
+// tokens and rows that are not 16-byte aligned, a copy of X with aligned rows:
+// gathering unaligned rows made the 11008x4096 product over 2047 tokens 171 us
+// where aligned ones take 111, and the copy takes 10.
+struct Workspace {
+  int64_t split, copy, ld;
+};
+Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols, bool x_aligned) {
+  Workspace w{0, 0, 0};
+  if (n_cols == 0) return w;
   const int nt = token_block(n_experts, n_cols);
   const int64_t fewest = (p.cout / 64) * (n_experts == 1 ? (n_cols + nt - 1) / nt : 1);   // items, if any
-  if (fewest * 2 > kMaxWgs) return 0;             // never split
-  return hinm::kWsCounterBytes + (int64_t)kMaxWgs * nt * 64 * 4;
+  if (fewest * 2 <= kMaxWgs) w.split = hinm::kWsCounterBytes + (int64_t)kMaxWgs * nt * 64 * 4;
+  if (nt >= 128 && !x_aligned) {
+    w.ld = (n_cols + 7) / 8 * 8;
+    w.copy = (p.cin * w.ld * 2 + 255) / 256 * 256;
+  }
+  return w;
 }
 
 // The product behind every entry point; `a` holds the weights' pointers.
@@ -846,7 +880,9 @@ template <bool MX4>
 int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, int64_t n_cols, int64_t ldx,
            const int32_t* starts, const int32_t* counts, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
            void* stream_) {
-  const int64_t need = ws_bytes(p, n_experts, n_cols);
+  const bool x_aligned = hinm::aligned(x, 16) && ldx % 8 == 0;
+  const Workspace w = workspace_of(p, n_experts, n_cols, x_aligned);
+  const int64_t need = w.split + w.copy;
   if (need > 0) {
     if (!workspace || workspace_bytes < (size_t)need)
       return fail(HINM_EWORKSPACE, "workspace of %zu bytes given, %lld needed", workspace_bytes, (long long)need);
@@ -869,16 +905,27 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
   a.nkb_d = p.n_dense_pad / HINM_KB_DENSE;
   a.nkb_s = p.n_24_pad / HINM_KB_24;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
+  a.x_end = 1;
+  if (w.copy) {
+    uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w.split);
+    const dim3 grid((unsigned)((w.ld + 2047) / 2048), (unsigned)std::min(p.cin, 4096));
+    hipLaunchKernelGGL(align_kernel, grid, dim3(256), 0, stream, a.x, ldx, a.n_cols, copy, w.ld, p.cin);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(HINM_EHIP, "experts launch: %s", hipGetErrorString(e));
+    a.x = copy;
+    a.ldx = ldx = w.ld;
+    a.x_end = 0;
+  }
   // The fast kernels address X with 32-bit buffer offsets and 24-bit
   // multiplies (row number, row pitch in bytes).
   const int64_t x_bytes = ((int64_t)(p.cin - 1) * ldx + n_cols) * 2;
-  if (x_bytes >= ((int64_t)1 << 31) || ldx * 2 >= (1 << 24) || p.cin > (1 << 24)) {
+  if (x_bytes >= ((int64_t)1 << 31) - 16 || ldx * 2 >= (1 << 24) || p.cin > (1 << 24)) {
     const int64_t tbs = n_cols / kGenTok + std::min<int64_t>(n_experts, n_cols);
     const dim3 grid((unsigned)(p.cout / 64), (unsigned)std::min<int64_t>(tbs, 65535));
     hipLaunchKernelGGL(experts_general_kernel<MX4>, grid, dim3(256), 0, stream, a);
   } else {
     unsigned* ctr = static_cast<unsigned*>(workspace);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need ? hinm::kWsCounterBytes : 0));
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (w.split ? hinm::kWsCounterBytes : 0));
     const dim3 grid(kMaxWgs), block(256);
     switch (token_block(n_experts, n_cols)) {
       case 16: hipLaunchKernelGGL((experts_decode_kernel<MX4, 16>), grid, block, 0, stream, a, part, ctr); break;
@@ -930,7 +977,7 @@ int run_mx4(const hinm_mx4_t* k, int32_t n_experts, const void* x, int64_t n_col
 }  // namespace
 
 extern "C" int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_t n_experts, int64_t n_cols,
-                                                 size_t* bytes) {
+                                                 int32_t x_aligned, size_t* bytes) {
   hinm::clear_error();
   int st = hinm::check_plan(plan);
   if (st) return st;
@@ -938,12 +985,14 @@ extern "C" int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_
   if (st) return st;
   if (!bytes) return fail(HINM_EINVAL, "bytes is NULL");
   if (n_cols < 0) return fail(HINM_ESHAPE, "%lld columns", (long long)n_cols);
-  *bytes = (size_t)ws_bytes(*plan, n_experts, n_cols);
+  const Workspace w = workspace_of(*plan, n_experts, n_cols, x_aligned != 0);
+  *bytes = (size_t)(w.split + w.copy);
   return HINM_OK;
 }
 
-extern "C" int hinm_spmm_mx4_workspace_bytes(const hinm_plan_t* plan, int64_t batch, size_t* bytes) {
-  return hinm_spmm_experts_workspace_bytes(plan, 1, batch, bytes);
+extern "C" int hinm_spmm_mx4_workspace_bytes(const hinm_plan_t* plan, int64_t batch, int32_t x_aligned,
+                                             size_t* bytes) {
+  return hinm_spmm_experts_workspace_bytes(plan, 1, batch, x_aligned, bytes);
 }
 
 extern "C" int hinm_spmm_experts(const hinm_packed_t* stack, int32_t n_experts, const void* x_bf16, int64_t n_cols,

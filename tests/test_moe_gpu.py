@@ -242,7 +242,7 @@ def _check_product(y, w, x, kept, what):
     assert not bad.any(), f"{what}: {bad.sum()} outputs off, the first at {np.argwhere(bad)[0].tolist()}"
 
 
-@pytest.mark.parametrize("batch", [1, 2, 7, 8, 16, 17, 31, 33, 64, 65, 128, 130, 257, 300])
+@pytest.mark.parametrize("batch", [1, 2, 7, 8, 16, 17, 31, 33, 64, 65, 128, 130, 257, 300, 1031, 1040])
 @pytest.mark.parametrize("cout,cin,rows,t,v", [(128, 300, 64, 0.75, 0.55), (192, 2052, 64, 0.5, 0.25)])
 def test_product_with_four_bit_values(batch, cout, cin, rows, t, v):
     print(f"[mx4 spmm] {cout}x{cin} batch={batch}", flush=True)
@@ -277,7 +277,7 @@ def _ranges(counts, align, gap=0, lead=0):
 
 
 COUNTS = [([3, 0, 1, 9], 8), ([0, 0, 0, 0], 8), ([16, 17, 0, 15], 1), ([1, 1, 1, 1], 1), ([70, 5, 33, 64], 8),
-          ([0, 300, 0, 2], 8), ([129, 128, 127, 130], 1), ([0, 0, 0, 600], 8), ([40, 257, 64, 65], 4)]
+          ([0, 300, 0, 2], 8), ([129, 128, 127, 130], 1), ([0, 0, 0, 600], 8), ([40, 257, 64, 65], 4), ([700, 3, 1025, 0], 8), ([1023, 65, 1, 300], 1)]
 
 
 @pytest.mark.parametrize("counts,align", COUNTS)

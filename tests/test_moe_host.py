@@ -118,6 +118,10 @@ def test_experts_refuse(lib, mx4):
         assert call(k=make(p, scale_24=None)) == 1
     if need:
         assert call(ws=None) == 6 and call(wsn=need - 1) == 6 and call(ws=FAKE + 16) == 5
+    # many tokens, unaligned rows: the workspace also holds a copy of X with aligned rows
+    many = hinm.spmm_experts_workspace_bytes(p, 1, 1001)
+    assert hinm.spmm_experts_workspace_bytes(p, 1, 1001, x_aligned=False) == many + 256 * 1008 * 2
+    assert call(e=1, cols=1001, ldx=1001, ldy=1001, wsn=many) == 6
     q = hinm.plan(96, 256, 32, 0.75, 0.55)                       # tile_rows 32
     assert call(k=make(q)) == 2 and "tile_rows" in _err(lib)
     assert call(cols=0, x=None, y=None, ldx=0, ldy=0) == 0       # no columns: nothing to do
@@ -125,10 +129,10 @@ def test_experts_refuse(lib, mx4):
     bad.plan.n_dense += 1
     assert call(k=bad) == 1
     n = ctypes.c_size_t()
-    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), 0, 40, ctypes.byref(n)) == 2
-    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), 4, -1, ctypes.byref(n)) == 2
-    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), 4, 40, None) == 1
-    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(q.raw), 4, 40, ctypes.byref(n)) == 2
+    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), 0, 40, 1, ctypes.byref(n)) == 2
+    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), 4, -1, 1, ctypes.byref(n)) == 2
+    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), 4, 40, 1, None) == 1
+    assert lib.hinm_spmm_experts_workspace_bytes(ctypes.byref(q.raw), 4, 40, 1, ctypes.byref(n)) == 2
 
 
 def test_mx4_refuses(lib):
@@ -144,7 +148,7 @@ def test_mx4_refuses(lib):
     assert lib.hinm_mx4_dequantize(ref(_mx4(p, meta_24=None)), 1, ref(_packed(p)), None) == 1
     assert lib.hinm_mx4_dequantize(ref(_mx4(q)), 1, ref(_packed(q)), None) == 2
     n = ctypes.c_size_t()
-    assert lib.hinm_spmm_mx4_workspace_bytes(ref(p.raw), 16, ref(n)) == 0
+    assert lib.hinm_spmm_mx4_workspace_bytes(ref(p.raw), 16, 1, ref(n)) == 0
     assert lib.hinm_spmm_mx4(ref(_mx4(p)), FAKE, 16, 15, FAKE, 16, FAKE, n.value, None) == 2
     assert lib.hinm_spmm_mx4(ref(_mx4(p)), None, 16, 16, FAKE, 16, FAKE, n.value, None) == 1
     assert lib.hinm_spmm_mx4(ref(_mx4(q)), FAKE, 16, 16, FAKE, 16, FAKE, n.value, None) == 2
