@@ -303,25 +303,180 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Dispatch and combine: a thread owns eight adjacent columns (their sources
-// or slots stay in registers) and walks the channels.
+// Dispatch and combine: bound by the bytes of the two matrices.  A column's
+// source may be anywhere in a row, and 2-byte gathers from memory run at a
+// quarter of the copy rate, so a workgroup stages G whole rows in LDS,
+// interleaved (a token's G values are one LDS word of 2 G bytes), and one LDS
+// read brings G rows of a column.  G is the largest of 8, 4, 2, 1 whose rows
+// fit 80 KB (two workgroups a compute unit); longer rows are gathered from
+// memory.
 // ---------------------------------------------------------------------------
-constexpr int kMoveRows = 16;      // channels a workgroup walks
+constexpr int kMoveThreads = 512;
+constexpr int kMoveLds = 80 * 1024;
+constexpr int64_t kMoveWgs = 1024;
+constexpr int kMoveRows = 16;      // channels a workgroup of the direct kernels walks
 
-__device__ inline void store8(uint16_t* dst, const uint16_t (&v)[8], int n, bool vec) {
-  if (vec && n >= 8) {
-    u32x4 w;
+typedef u32x4 any_u32x4 __attribute__((aligned(2)));   // 16 bytes at any 2-byte aligned address
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 any_u32x2 __attribute__((aligned(2)));
+
+template <int G>
+struct Rows;                       // a token's values of G rows
+template <>
+struct Rows<8> { u32x4 w; };
+template <>
+struct Rows<4> { u32x2 w; };
+template <>
+struct Rows<2> { uint32_t w[1]; };
+template <>
+struct Rows<1> { uint16_t w[1]; };
+
+// Halves of two words: both low (hi = 0) or both high halves, a's first.
+__device__ inline uint32_t pair(uint32_t a, uint32_t b, int hi) {
+  return __builtin_amdgcn_perm(b, a, hi ? 0x07060302u : 0x05040100u);
+}
+
+// Eight tokens' rows as G rows of eight tokens.
+template <int G>
+__device__ inline void to_rows(const Rows<G> (&t)[8], u32x4 (&v)[G]) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) w[u] = (uint32_t)v[2 * u] | ((uint32_t)v[2 * u + 1] << 16);
-    *reinterpret_cast<u32x4*>(dst) = w;
-  } else {
-    for (int u = 0; u < 8 && u < n; ++u) dst[u] = v[u];
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int r = 0; r < G; ++r) v[r][u] = pair(t[2 * u].w[r / 2], t[2 * u + 1].w[r / 2], r & 1);
+}
+
+// Rows c0 .. c0 + G - 1 of a matrix into LDS (rows past `channels` as zeros).
+// A thread brings two adjacent tokens at a time, so that a wave's LDS stores
+// are contiguous, and four such pairs before it stores any.
+template <int G>
+__device__ inline void stage_rows(const uint16_t* __restrict__ x, int64_t ldx, int n, int64_t c0, int64_t channels,
+                                  Rows<G>* buf) {
+  typedef uint32_t any_u32 __attribute__((aligned(2)));
+  constexpr int P = 4;
+  for (int q0 = threadIdx.x * 2; q0 < n; q0 += kMoveThreads * 2 * P) {
+    uint32_t v[P][G];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int q = q0 + p * kMoveThreads * 2;
+#pragma unroll
+      for (int r = 0; r < G; ++r) {
+        v[p][r] = 0u;
+        if (q < n && c0 + r < channels) {
+          const uint16_t* src = x + (c0 + r) * ldx + q;
+          v[p][r] = q + 1 < n ? *reinterpret_cast<const any_u32*>(src) : (uint32_t)*src;
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int q = q0 + p * kMoveThreads * 2;
+      Rows<G> t[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if constexpr (G == 1) t[u].w[0] = (uint16_t)(v[p][0] >> (16 * u));
+        else
+#pragma unroll
+          for (int k = 0; k < G / 2; ++k) t[u].w[k] = pair(v[p][2 * k], v[p][2 * k + 1], u);
+      }
+      if (q < n) {                               // an odd row's last pair: its second half is never read
+        buf[q] = t[0];
+        buf[q + 1] = t[1];
+      }
+    }
   }
 }
 
-__global__ __launch_bounds__(256) void dispatch_kernel(const uint16_t* __restrict__ x, int64_t channels, int n_tokens,
-                                                       int64_t ldx, const int32_t* __restrict__ src, int64_t n_cols,
-                                                       uint16_t* __restrict__ xs, int64_t ldxs, int vec) {
+template <int G>
+__global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(const uint16_t* __restrict__ x, int64_t channels,
+                                                                int n_tokens, int64_t ldx,
+                                                                const int32_t* __restrict__ src, int n_cols,
+                                                                uint16_t* __restrict__ xs, int64_t ldxs) {
+  __shared__ __attribute__((aligned(16))) Rows<G> buf[kMoveLds / (2 * G)];
+  for (int64_t c0 = (int64_t)blockIdx.x * G; c0 < channels; c0 += (int64_t)gridDim.x * G) {
+    stage_rows<G>(x, ldx, n_tokens, c0, channels, buf);
+    __syncthreads();
+    for (int col = threadIdx.x * 8; col < n_cols; col += kMoveThreads * 8) {
+      const int left = n_cols - col;
+      Rows<G> t[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int s = u < left ? src[col + u] : -1;
+        t[u] = Rows<G>{};
+        if (s >= 0 && s < n_tokens) t[u] = buf[s];
+      }
+      u32x4 v[G];
+      to_rows<G>(t, v);
+#pragma unroll
+      for (int r = 0; r < G; ++r)
+        if (c0 + r < channels) {
+          uint16_t* dst = xs + (c0 + r) * ldxs + col;
+          if (left >= 8) *reinterpret_cast<any_u32x4*>(dst) = v[r];
+          else
+            for (int u = 0; u < 8; ++u)
+              if (u < left) dst[u] = (uint16_t)(v[r][u >> 1] >> (16 * (u & 1)));
+        }
+    }
+    __syncthreads();
+  }
+}
+
+// Four tokens a thread; every token's sum runs over its choices in order.
+template <int G>
+__global__ __launch_bounds__(kMoveThreads) void combine_kernel(const uint16_t* __restrict__ ys, int64_t channels,
+                                                               int n_cols, int64_t ldys,
+                                                               const int32_t* __restrict__ slots,
+                                                               const float* __restrict__ weights, int n_tokens,
+                                                               int top_k, uint16_t* __restrict__ y, int64_t ldy) {
+  __shared__ __attribute__((aligned(16))) Rows<G> buf[kMoveLds / (2 * G)];
+  for (int64_t c0 = (int64_t)blockIdx.x * G; c0 < channels; c0 += (int64_t)gridDim.x * G) {
+    stage_rows<G>(ys, ldys, n_cols, c0, channels, buf);
+    __syncthreads();
+    for (int n = threadIdx.x * 4; n < n_tokens; n += kMoveThreads * 4) {
+      const int left = n_tokens - n;
+      float acc[4][G];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < G; ++r) acc[u][r] = 0.f;
+#pragma unroll 2
+      for (int j = 0; j < top_k; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t at = (int64_t)min(n + u, n_tokens - 1) * top_k + j;
+          const int s = slots[at];
+          const float w = weights[at];
+          if (s >= 0 && s < n_cols) {
+            const Rows<G> t = buf[s];
+#pragma unroll
+            for (int r = 0; r < G; ++r) {
+              const uint32_t h = t.w[r / 2];
+              acc[u][r] = fmaf(w, __uint_as_float(r & 1 ? h & 0xffff0000u : h << 16), acc[u][r]);
+            }
+          }
+        }
+#pragma unroll
+      for (int r = 0; r < G; ++r)
+        if (c0 + r < channels) {
+          uint16_t* dst = y + (c0 + r) * ldy + n;
+          uint16_t h[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) h[u] = bf16_rne(acc[u][r]);
+          if (left >= 4) *reinterpret_cast<any_u32x2*>(dst) = u32x2{h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16)};
+          else
+            for (int u = 0; u < 4; ++u)
+              if (u < left) dst[u] = h[u];
+        }
+    }
+    __syncthreads();
+  }
+}
+
+// Rows too long for LDS: gathered from memory, a thread walking channels with
+// its columns' sources in registers.
+__global__ __launch_bounds__(256) void dispatch_direct_kernel(const uint16_t* __restrict__ x, int64_t channels,
+                                                              int n_tokens, int64_t ldx,
+                                                              const int32_t* __restrict__ src, int n_cols,
+                                                              uint16_t* __restrict__ xs, int64_t ldxs) {
   const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= n_cols) return;
   const int left = (int)min((int64_t)8, n_cols - col);
@@ -330,29 +485,41 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const uint16_t* __restric
   for (int u = 0; u < 8; ++u) t[u] = u < left ? src[col + u] : -1;
   for (int64_t c0 = (int64_t)blockIdx.y * kMoveRows; c0 < channels; c0 += (int64_t)gridDim.y * kMoveRows)
     for (int64_t c = c0; c < min(c0 + kMoveRows, channels); ++c) {
-      uint16_t v[8];
+      u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = t[u] >= 0 && t[u] < n_tokens ? x[c * ldx + t[u]] : (uint16_t)0;
-      store8(xs + c * ldxs + col, v, left, vec);
+      for (int u = 0; u < 8; ++u)
+        if (t[u] >= 0 && t[u] < n_tokens) v[u >> 1] |= (uint32_t)x[c * ldx + t[u]] << (16 * (u & 1));
+      uint16_t* dst = xs + c * ldxs + col;
+      if (left == 8) *reinterpret_cast<any_u32x4*>(dst) = v;
+      else
+        for (int u = 0; u < left; ++u) dst[u] = (uint16_t)(v[u >> 1] >> (16 * (u & 1)));
     }
 }
 
-__global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ ys, int64_t channels,
-                                                      int64_t n_cols, int64_t ldys, const int32_t* __restrict__ slots,
-                                                      const float* __restrict__ weights, int n_tokens, int top_k,
-                                                      uint16_t* __restrict__ y, int64_t ldy) {
+__global__ __launch_bounds__(256) void combine_direct_kernel(const uint16_t* __restrict__ ys, int64_t channels,
+                                                             int n_cols, int64_t ldys,
+                                                             const int32_t* __restrict__ slots,
+                                                             const float* __restrict__ weights, int n_tokens,
+                                                             int top_k, uint16_t* __restrict__ y, int64_t ldy) {
   const int n = blockIdx.x * 256 + threadIdx.x;
   if (n >= n_tokens) return;
   for (int64_t c0 = (int64_t)blockIdx.y * kMoveRows; c0 < channels; c0 += (int64_t)gridDim.y * kMoveRows)
     for (int64_t c = c0; c < min(c0 + kMoveRows, channels); ++c) {
       float acc = 0.f;
       for (int j = 0; j < top_k; ++j) {
-        const int64_t s = slots[(int64_t)n * top_k + j];
+        const int s = slots[(int64_t)n * top_k + j];
         if (s >= 0 && s < n_cols)
           acc = fmaf(weights[(int64_t)n * top_k + j], __uint_as_float((uint32_t)ys[c * ldys + s] << 16), acc);
       }
       y[c * ldy + n] = bf16_rne(acc);
     }
+}
+
+// Rows a workgroup stages for a row of n elements; 0: they do not fit.
+int staged_rows(int64_t n) {
+  for (int g = 8; g; g /= 2)
+    if ((n + 1) * 2 * g <= kMoveLds) return g;   // pairs of elements: one more than an odd row has
+  return 0;
 }
 
 int launch_status(const char* what) {
@@ -501,11 +668,23 @@ extern "C" int hinm_dispatch(const void* x_bf16, int64_t channels, int64_t n_tok
     return fail(HINM_EALIGN, "x and xs must be 2-byte aligned, src 4-byte aligned");
   const int st = hinm::ensure_device();
   if (st) return st;
-  const int vec = hinm::aligned(xs_bf16, 16) && ldxs % 8 == 0;
-  const dim3 grid((unsigned)((n_cols + 2047) / 2048), (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));
-  hipLaunchKernelGGL(dispatch_kernel, grid, dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                     static_cast<const uint16_t*>(x_bf16), channels, (int)n_tokens, ldx, src, n_cols,
-                     static_cast<uint16_t*>(xs_bf16), ldxs, vec);
+  hipStream_t st_ = reinterpret_cast<hipStream_t>(stream);
+  const uint16_t* x = static_cast<const uint16_t*>(x_bf16);
+  uint16_t* xs = static_cast<uint16_t*>(xs_bf16);
+  const int nt = (int)n_tokens, nc = (int)n_cols, g = staged_rows(n_tokens);
+  if (g) {
+    const dim3 grid((unsigned)std::min<int64_t>((channels + g - 1) / g, kMoveWgs)), block(kMoveThreads);
+    switch (g) {
+      case 8: hipLaunchKernelGGL(dispatch_kernel<8>, grid, block, 0, st_, x, channels, nt, ldx, src, nc, xs, ldxs); break;
+      case 4: hipLaunchKernelGGL(dispatch_kernel<4>, grid, block, 0, st_, x, channels, nt, ldx, src, nc, xs, ldxs); break;
+      case 2: hipLaunchKernelGGL(dispatch_kernel<2>, grid, block, 0, st_, x, channels, nt, ldx, src, nc, xs, ldxs); break;
+      default: hipLaunchKernelGGL(dispatch_kernel<1>, grid, block, 0, st_, x, channels, nt, ldx, src, nc, xs, ldxs); break;
+    }
+  } else {
+    const dim3 grid((unsigned)((n_cols + 2047) / 2048),
+                    (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));
+    hipLaunchKernelGGL(dispatch_direct_kernel, grid, dim3(256), 0, st_, x, channels, nt, ldx, src, nc, xs, ldxs);
+  }
   return launch_status("dispatch");
 }
 
@@ -528,9 +707,26 @@ extern "C" int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_col
     return fail(HINM_EALIGN, "ys and y must be 2-byte aligned, slots and weights 4-byte aligned");
   const int st = hinm::ensure_device();
   if (st) return st;
-  const dim3 grid((unsigned)((n_tokens + 255) / 256), (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));
-  hipLaunchKernelGGL(combine_kernel, grid, dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
-                     static_cast<const uint16_t*>(ys_bf16), channels, n_cols, ldys, slots, weights, (int)n_tokens, top_k,
-                     static_cast<uint16_t*>(y_bf16), ldy);
+  hipStream_t st_ = reinterpret_cast<hipStream_t>(stream);
+  const uint16_t* ys = static_cast<const uint16_t*>(ys_bf16);
+  uint16_t* y = static_cast<uint16_t*>(y_bf16);
+  const int nt = (int)n_tokens, nc = (int)n_cols, g = staged_rows(n_cols);
+  if (g) {
+    const dim3 grid((unsigned)std::min<int64_t>((channels + g - 1) / g, kMoveWgs)), block(kMoveThreads);
+#define HINM_COMBINE(G_)                                                                                              \
+  hipLaunchKernelGGL(combine_kernel<G_>, grid, block, 0, st_, ys, channels, nc, ldys, slots, weights, nt, top_k, y, ldy)
+    switch (g) {
+      case 8: HINM_COMBINE(8); break;
+      case 4: HINM_COMBINE(4); break;
+      case 2: HINM_COMBINE(2); break;
+      default: HINM_COMBINE(1); break;
+    }
+#undef HINM_COMBINE
+  } else {
+    const dim3 grid((unsigned)((n_tokens + 255) / 256),
+                    (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));
+    hipLaunchKernelGGL(combine_direct_kernel, grid, dim3(256), 0, st_, ys, channels, nc, ldys, slots, weights, nt,
+                       top_k, y, ldy);
+  }
   return launch_status("combine");
 }

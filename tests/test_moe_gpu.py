@@ -98,7 +98,7 @@ def _routing(n, e, k, seed, align=8, idle=0.1):
 
 
 @pytest.mark.parametrize("c,n,e,k,align", [(1, 1, 1, 1, 1), (5, 17, 3, 2, 8), (64, 300, 8, 2, 8), (130, 1025, 4, 1, 1),
-                                           (3, 40, 16, 16, 4), (33, 9000, 6, 3, 8), (2, 70000, 2, 2, 8)])
+                                           (3, 40, 16, 16, 4), (33, 9000, 6, 3, 8), (3, 15000, 4, 2, 8), (2, 70000, 2, 2, 8)])
 @pytest.mark.parametrize("pad", [0, 3])
 def test_dispatch_and_combine(c, n, e, k, align, pad):
     """Contiguous matrices and slices of wider ones whose surroundings stay as they were."""
