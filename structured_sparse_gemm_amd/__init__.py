@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -869,19 +870,25 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, align: int
     if (n > 1 and logits.stride(1) != 1) or (e > 1 and ld < n):
         raise ValueError("logits must have unit column stride and rows that do not overlap")
     dev, lib = logits.device, library()
-    cols = route_columns(n, e, top_k, align)
-    need = ctypes.c_size_t()
-    _check(lib.hinm_route_workspace_bytes(n, e, ctypes.byref(need)))
-    ints = torch.empty(2 * n * top_k + 2 * e + 1 + cols, dtype=torch.int32, device=dev)
-    a, b = n * top_k, 2 * n * top_k
-    r = Routing(ints[:a].view(n, top_k), torch.empty((n, top_k), dtype=torch.float32, device=dev),
-                ints[a:b].view(n, top_k), ints[b:b + e + 1], ints[b + e + 1:b + 2 * e + 1], ints[b + 2 * e + 1:])
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    cols, need = _route_sizes(n, e, top_k, align)
+    nk = n * top_k
+    ids, slots, starts, counts, src = torch.empty(2 * nk + 2 * e + 1 + cols, dtype=torch.int32, device=dev).split(
+        (nk, nk, e + 1, e, cols))
+    r = Routing(ids.view(n, top_k), torch.empty((n, top_k), dtype=torch.float32, device=dev), slots.view(n, top_k),
+                starts, counts, src)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call(dev, lib.hinm_route, logits.data_ptr(), HINM_BF16 if logits.dtype == torch.bfloat16 else HINM_FP32, n,
-          max(ld, n), e, top_k, int(renormalize), align, r.ids.data_ptr(), r.weights.data_ptr(), r.slots.data_ptr(),
-          r.starts.data_ptr(), r.counts.data_ptr(), r.src.data_ptr(), cols, ws.data_ptr() if ws is not None else None,
-          need.value, _stream_ptr(dev))
+          max(ld, n), e, top_k, int(renormalize), align, ids.data_ptr(), r.weights.data_ptr(), slots.data_ptr(),
+          starts.data_ptr(), counts.data_ptr(), src.data_ptr(), cols, ws.data_ptr() if need else None, need,
+          _stream_ptr(dev))
     return r
+
+
+@functools.lru_cache(maxsize=1024)
+def _route_sizes(n_tokens: int, n_experts: int, top_k: int, align: int):
+    need = ctypes.c_size_t()
+    _check(library().hinm_route_workspace_bytes(n_tokens, n_experts, ctypes.byref(need)))
+    return route_columns(n_tokens, n_experts, top_k, align), need.value
 
 
 def dispatch(x: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = None) -> torch.Tensor:

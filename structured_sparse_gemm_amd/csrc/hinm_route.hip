@@ -19,15 +19,15 @@ namespace {
 // three facts per (token, choice): the expert's first column (a prefix sum
 // over the experts' totals), the choices of that expert in earlier blocks,
 // and those of earlier tokens in the same block.  topk_kernel finds the
-// choices and every block's expert counts; place_kernel adds the counts up
-// and writes the order.  Up to kTok tokens, one workgroup does both in one
-// launch; past kGroup blocks, sum_kernel first adds the counts of every kGroup
-// blocks, so that place_kernel reads n_blocks / kGroup + kGroup rows of them
-// and not n_blocks.
+// choices and every block's expert counts, scan_kernel turns the counts into
+// the counts of the blocks before (a column of them per expert) and the
+// experts' totals, and place_kernel writes the order.  Up to kTok tokens, one
+// workgroup does it all in one launch.
 // ---------------------------------------------------------------------------
 constexpr int kTok = 64;           // tokens of a block: one wave's lanes
-constexpr int kGroup = 32;         // blocks of a group
 constexpr int kRouteThreads = 256;
+constexpr int kScanExperts = 64;   // experts of a workgroup of scan_kernel: a wave's lanes
+constexpr int kScanParts = 16;     // its waves, each a run of blocks
 
 struct RouteArgs {
   const void* logits;
@@ -36,15 +36,27 @@ struct RouteArgs {
   int32_t *ids, *slots, *starts, *counts, *src;
   float* weights;
   int64_t n_cols;
-  int n_blocks, n_groups;          // n_groups: 0 when the groups are not summed
-  int32_t *hist, *gsum;            // [n_blocks][n_experts], [n_groups][n_experts]
+  int n_blocks;
+  int32_t *hist, *total;           // [n_blocks][n_experts], [n_experts]
 };
 
-__device__ inline float load_logit(const RouteArgs& a, int e, int n) {
-  const int64_t at = (int64_t)e * a.ldl + n;
-  const float l = a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16)
-                         : static_cast<const float*>(a.logits)[at];
-  return l == l ? l : -INFINITY;                 // NaN: not eligible
+// C logits of token n, experts e .. e1 - 1; -inf past e1, for a NaN and where
+// `live` is false.  The loads themselves are unconditional (clamped), so that
+// all of them are in flight at once.
+template <int C>
+__device__ inline void load_logits(const RouteArgs& a, int e, int e1, int n, bool live, float (&l)[C]) {
+  const int nc = live ? n : 0;
+  if (a.bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + nc;
+#pragma unroll
+    for (int u = 0; u < C; ++u) l[u] = __uint_as_float((uint32_t)p[(int64_t)min(e + u, e1 - 1) * a.ldl] << 16);
+  } else {
+    const float* p = static_cast<const float*>(a.logits) + nc;
+#pragma unroll
+    for (int u = 0; u < C; ++u) l[u] = p[(int64_t)min(e + u, e1 - 1) * a.ldl];
+  }
+#pragma unroll
+  for (int u = 0; u < C; ++u) l[u] = live && e + u < e1 && l[u] == l[u] ? l[u] : -INFINITY;
 }
 
 // A list of the K largest logits so far, descending, equal ones in the order
@@ -92,56 +104,68 @@ struct RouteShared {
   int before[HINM_MAX_EXPERTS];                  // counts of earlier blocks, then the block's first column
   int total[HINM_MAX_EXPERTS];
   int start[HINM_MAX_EXPERTS + 1];
-  int part[kRouteThreads];
+  int part[4];                                   // waves' padded counts
 };
 
 // Choices and weights of tokens b * kTok ..; their experts' counts in s.hist.
 // The four waves take a quarter of the experts each, one token a lane, and
 // the first wave merges the four lists (in expert order, so equal logits stay
 // in it).  Each thread ends up with its token's choices in the first wave.
-template <int K>
+// C: logits a thread holds at once (all of its quarter when that is no more).
+template <int K, int C>
 __device__ inline void topk_block(const RouteArgs& a, RouteShared<K>& s, int b, Best<K>& best) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = b * kTok + lane;
   const bool live = n < a.n_tokens;
   const int per = (a.n_experts + 3) / 4;
-  const int e0 = min(wave * per, a.n_experts), e1 = min(e0 + per, a.n_experts);
+  // no tokens: nothing to read (logits may then be NULL); else lanes past the batch read token 0
+  const int e0 = min(wave * per, a.n_experts), e1 = a.n_tokens > 0 ? min(e0 + per, a.n_experts) : e0;
   for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) s.hist[e] = 0;
   best.clear();
-  if (live) {
-    int e = e0;
-    for (; e + 8 <= e1; e += 8) {                // eight loads in flight
-      float l[8];
+  float l[C];
+  for (int e = e0; e < e1; e += C) {
+    load_logits<C>(a, e, e1, n, live, l);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) l[u] = load_logit(a, e + u, n);
+    for (int u = 0; u < C; ++u) best.add(l[u], e + u);
+  }
+  // merge the four lists in two rounds: 1 into 0 and 3 into 2, then 2 into 0
+  // (equal logits stay in expert order)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) best.add(l[u], e + u);
+  for (int d = 1; d <= 2; d *= 2) {
+    if (wave % (2 * d) == d) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        s.v[wave][j][lane] = best.v[j];
+        s.id[wave][j][lane] = best.id[j];
+      }
     }
-    for (; e < e1; ++e) best.add(load_logit(a, e, n), e);
-  }
+    __syncthreads();
+    if (wave % (2 * d) == 0) {
+      float v[K];
+      int id[K];
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    s.v[wave][j][lane] = best.v[j];
-    s.id[wave][j][lane] = best.id[j];
-  }
-  __syncthreads();
-  if (wave == 0) {
-    for (int w = 1; w < 4; ++w)
+      for (int j = 0; j < K; ++j) {
+        v[j] = s.v[wave + d][j][lane];
+        id[j] = s.id[wave + d][j][lane];
+      }
 #pragma unroll
-      for (int j = 0; j < K; ++j) best.add(s.v[w][j][lane], s.id[w][j][lane]);
-    s.top[lane] = best.v[0];
+      for (int j = 0; j < K; ++j) best.add(v[j], id[j]);
+    }
   }
+  if (wave == 0) s.top[lane] = best.v[0];
   __syncthreads();
   // exp(l - m), where l == m gives 1 also for infinities.  The sum over all
   // experts is kept in 64 bits: up to 1024 terms, added one by one.
   const float m = s.top[lane];
-  auto term = [&](float l) { return l == m ? 1.f : expf(l - m); };
+  auto term = [&](float v) { return v == m ? 1.f : expf(v - m); };
   if (!a.renormalize) {
     double sum = 0.0;
-    if (live && m > -INFINITY)
-      for (int e = e0; e < e1; ++e) {
-        const float l = load_logit(a, e, n);
-        if (l > -INFINITY) sum += (double)term(l);
+    if (m > -INFINITY)
+      for (int e = e0; e < e1; e += C) {
+        if (per > C) load_logits<C>(a, e, e1, n, live, l);   // else l still holds them
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+          sum += l[u] > -INFINITY ? (double)term(l[u]) : 0.0;
       }
     s.sum[wave][lane] = sum;
     __syncthreads();
@@ -155,43 +179,45 @@ __device__ inline void topk_block(const RouteArgs& a, RouteShared<K>& s, int b, 
     } else {
       sum = s.sum[0][lane] + s.sum[1][lane] + s.sum[2][lane] + s.sum[3][lane];
     }
+    const double inv = 1.0 / sum;
 #pragma unroll
     for (int j = 0; j < K; ++j)
       if (j < a.top_k) {
         const int e = best.id[j];
         a.ids[(int64_t)n * a.top_k + j] = e;
-        a.weights[(int64_t)n * a.top_k + j] = e >= 0 ? (float)((double)term(best.v[j]) / sum) : 0.f;
+        a.weights[(int64_t)n * a.top_k + j] = e >= 0 ? (float)((double)term(best.v[j]) * inv) : 0.f;
         if (e >= 0) atomicAdd(&s.hist[e], 1);    // whole numbers: the order does not matter
       }
   }
   __syncthreads();
 }
 
-// Every expert's total and first column, and the block's first column of
-// every expert (s.before); `rows` adds the counts to s.before and s.total.
+// First columns: s.start from the totals, and s.before, the counts of earlier
+// blocks, becomes the block's own first column of every expert.
 template <int K>
 __device__ inline void scan_experts(const RouteArgs& a, RouteShared<K>& s) {
   // exclusive prefix sum of the padded totals: each thread a run of experts
   const int per = (a.n_experts + kRouteThreads - 1) / kRouteThreads;
   const int e0 = min((int)threadIdx.x * per, a.n_experts), e1 = min(e0 + per, a.n_experts);
-  const int mask = a.align - 1;
+  const int mask = a.align - 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int run = 0;
   for (int e = e0; e < e1; ++e) run += (s.total[e] + mask) & ~mask;
-  s.part[threadIdx.x] = run;
-  __syncthreads();
-  for (int d = 1; d < kRouteThreads; d *= 2) {
-    const int v = (int)threadIdx.x >= d ? s.part[threadIdx.x - d] : 0;
-    __syncthreads();
-    s.part[threadIdx.x] += v;
-    __syncthreads();
+  int sum = run;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int v = __shfl_up(sum, d);
+    sum += lane >= d ? v : 0;
   }
-  int at = s.part[threadIdx.x] - run;
+  if (lane == 63) s.part[wave] = sum;
+  __syncthreads();
+  int at = sum - run;
+  for (int w = 0; w < wave; ++w) at += s.part[w];
   for (int e = e0; e < e1; ++e) {
     s.start[e] = at;
     s.before[e] += at;
     at += (s.total[e] + mask) & ~mask;
   }
-  if (threadIdx.x == kRouteThreads - 1) s.start[a.n_experts] = s.part[kRouteThreads - 1];
+  if (threadIdx.x == kRouteThreads - 1) s.start[a.n_experts] = at;
   __syncthreads();
 }
 
@@ -237,11 +263,11 @@ __device__ inline void place_block(const RouteArgs& a, RouteShared<K>& s, int b,
     a.src[c] = -1;
 }
 
-template <int K, bool ONE>
+template <int K, int C, bool ONE>
 __global__ __launch_bounds__(kRouteThreads) void topk_kernel(RouteArgs a) {
   __shared__ RouteShared<K> s;
   Best<K> best;
-  topk_block<K>(a, s, blockIdx.x, best);
+  topk_block<K, C>(a, s, blockIdx.x, best);
   if constexpr (ONE) {
     for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) {
       s.total[e] = s.hist[e];
@@ -259,13 +285,39 @@ __global__ __launch_bounds__(kRouteThreads) void topk_kernel(RouteArgs a) {
   }
 }
 
-// Sums of kGroup blocks' counts.
-__global__ __launch_bounds__(kRouteThreads) void sum_kernel(RouteArgs a) {
-  const int b0 = blockIdx.x * kGroup, b1 = min(b0 + kGroup, a.n_blocks);
-  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) {
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += a.hist[(int64_t)b * a.n_experts + e];
-    a.gsum[(int64_t)blockIdx.x * a.n_experts + e] = sum;
+// Counts of every block -> counts of the blocks before it, and the totals: a
+// lane an expert, a wave a run of blocks.
+__global__ __launch_bounds__(kScanParts * 64) void scan_kernel(RouteArgs a) {
+  __shared__ int part[kScanParts][kScanExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * kScanExperts + lane;
+  const int per = (a.n_blocks + kScanParts - 1) / kScanParts;
+  const int b0 = min(wave * per, a.n_blocks), b1 = min(b0 + per, a.n_blocks);
+  const bool live = e < a.n_experts;
+  int32_t* col = a.hist + (live ? e : 0);
+  constexpr int U = 8;                           // loads in flight
+  int sum = 0;
+  for (int b = b0; b < b1; b += U) {
+    int v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = b + u < b1 ? col[(int64_t)(b + u) * a.n_experts] : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) sum += v[u];
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < wave; ++w) at += part[w][lane];
+  if (wave == kScanParts - 1 && live) a.total[e] = at + sum;
+  for (int b = b0; b < b1; b += U) {
+    int v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = b + u < b1 ? col[(int64_t)(b + u) * a.n_experts] : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b + u < b1 && live) col[(int64_t)(b + u) * a.n_experts] = at;
+      at += v[u];
+    }
   }
 }
 
@@ -277,25 +329,9 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a) {
 #pragma unroll
   for (int j = 0; j < K; ++j)
     id[j] = threadIdx.x < 64 && n < a.n_tokens && j < a.top_k ? a.ids[(int64_t)n * a.top_k + j] : -1;
-  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) s.total[e] = s.before[e] = 0;
-  __syncthreads();
-  // rows of counts: [0, mine) precede this block; all of them make the totals
-  auto rows = [&](const int32_t* t, int r0, int r1, int mine, bool total) {
-    const int64_t lo = (int64_t)r0 * a.n_experts, hi = (int64_t)r1 * a.n_experts;
-    for (int64_t q = lo + threadIdx.x; q < hi; q += kRouteThreads) {
-      const int v = t[q], r = (int)(q / a.n_experts), e = (int)(q - (int64_t)r * a.n_experts);
-      if (v) {
-        if (r < mine) atomicAdd(&s.before[e], v);
-        if (total) atomicAdd(&s.total[e], v);
-      }
-    }
-  };
-  if (a.n_groups) {
-    const int g = b / kGroup;
-    rows(a.gsum, 0, a.n_groups, g, true);
-    rows(a.hist, g * kGroup, b, b, false);
-  } else {
-    rows(a.hist, 0, a.n_blocks, b, true);
+  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) {
+    s.total[e] = a.total[e];
+    s.before[e] = a.hist[(int64_t)b * a.n_experts + e];
   }
   __syncthreads();
   scan_experts<K>(a, s);
@@ -420,8 +456,10 @@ __global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(const uint16_t* 
   }
 }
 
-// Four tokens a thread; every token's sum runs over its choices in order.
-template <int G>
+// Four tokens a thread; every token's sum runs over its choices in order.  K:
+// top_k when it is 1 or 2 (a thread's slots and weights then are whole 16-byte
+// words), 0 for any other.
+template <int G, int K>
 __global__ __launch_bounds__(kMoveThreads) void combine_kernel(const uint16_t* __restrict__ ys, int64_t channels,
                                                                int n_cols, int64_t ldys,
                                                                const int32_t* __restrict__ slots,
@@ -438,22 +476,35 @@ __global__ __launch_bounds__(kMoveThreads) void combine_kernel(const uint16_t* _
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int r = 0; r < G; ++r) acc[u][r] = 0.f;
-#pragma unroll 2
-      for (int j = 0; j < top_k; ++j)
+      auto add = [&](int u, int s, float w) {
+        if (s >= 0 && s < n_cols) {
+          const Rows<G> t = buf[s];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t at = (int64_t)min(n + u, n_tokens - 1) * top_k + j;
-          const int s = slots[at];
-          const float w = weights[at];
-          if (s >= 0 && s < n_cols) {
-            const Rows<G> t = buf[s];
-#pragma unroll
-            for (int r = 0; r < G; ++r) {
-              const uint32_t h = t.w[r / 2];
-              acc[u][r] = fmaf(w, __uint_as_float(r & 1 ? h & 0xffff0000u : h << 16), acc[u][r]);
-            }
+          for (int r = 0; r < G; ++r) {
+            const uint32_t h = t.w[r / 2];
+            acc[u][r] = fmaf(w, __uint_as_float(r & 1 ? h & 0xffff0000u : h << 16), acc[u][r]);
           }
         }
+      };
+      if (K > 0 && left >= 4) {
+        typedef u32x4 word_u32x4 __attribute__((aligned(4)));
+        u32x4 s[K ? K : 1], w[K ? K : 1];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          s[k] = *reinterpret_cast<const word_u32x4*>(slots + (int64_t)n * K + 4 * k);
+          w[k] = *reinterpret_cast<const word_u32x4*>(weights + (int64_t)n * K + 4 * k);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            add(u, (int)s[(u * K + j) / 4][(u * K + j) % 4], __uint_as_float(w[(u * K + j) / 4][(u * K + j) % 4]));
+      } else {
+        for (int j = 0; j < top_k; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (u < left) add(u, slots[(int64_t)(n + u) * top_k + j], weights[(int64_t)(n + u) * top_k + j]);
+      }
 #pragma unroll
       for (int r = 0; r < G; ++r)
         if (c0 + r < channels) {
@@ -550,29 +601,35 @@ int64_t route_columns(int64_t n_tokens, int32_t n_experts, int32_t top_k, int32_
   return (used + std::min<int64_t>(n_experts, used) * (align - 1) + align - 1) / align * align;
 }
 
-// [counts of every block][sums of every kGroup blocks]
-void route_shape(int64_t n_tokens, int32_t n_experts, int* n_blocks, int* n_groups, size_t* bytes) {
+// [counts of every block][totals]
+void route_shape(int64_t n_tokens, int32_t n_experts, int* n_blocks, size_t* bytes) {
   *n_blocks = (int)std::max<int64_t>(1, (n_tokens + kTok - 1) / kTok);
-  *n_groups = *n_blocks > kGroup ? (*n_blocks + kGroup - 1) / kGroup : 0;
-  *bytes = *n_blocks == 1 ? 0 : (size_t)(*n_blocks + *n_groups) * n_experts * sizeof(int32_t);
+  *bytes = *n_blocks == 1 ? 0 : (size_t)(*n_blocks + 1) * n_experts * sizeof(int32_t);
 }
 
-template <int K>
+template <int K, int C>
 int launch_route(const RouteArgs& a, hipStream_t stream) {
   if (a.n_blocks == 1) {
-    hipLaunchKernelGGL((topk_kernel<K, true>), dim3(1), dim3(kRouteThreads), 0, stream, a);
+    hipLaunchKernelGGL((topk_kernel<K, C, true>), dim3(1), dim3(kRouteThreads), 0, stream, a);
     return launch_status("route");
   }
-  hipLaunchKernelGGL((topk_kernel<K, false>), dim3(a.n_blocks), dim3(kRouteThreads), 0, stream, a);
+  hipLaunchKernelGGL((topk_kernel<K, C, false>), dim3(a.n_blocks), dim3(kRouteThreads), 0, stream, a);
   int st = launch_status("route");
   if (st) return st;
-  if (a.n_groups) {
-    hipLaunchKernelGGL(sum_kernel, dim3(a.n_groups), dim3(kRouteThreads), 0, stream, a);
-    st = launch_status("route");
-    if (st) return st;
-  }
+  hipLaunchKernelGGL(scan_kernel, dim3((a.n_experts + kScanExperts - 1) / kScanExperts), dim3(kScanParts * 64), 0, stream, a);
+  st = launch_status("route");
+  if (st) return st;
   hipLaunchKernelGGL(place_kernel<K>, dim3(a.n_blocks), dim3(kRouteThreads), 0, stream, a);
   return launch_status("route");
+}
+
+// Logits a thread holds: its quarter of 8, 32 or 128 experts.
+template <int K>
+int launch_route(const RouteArgs& a, hipStream_t stream) {
+  if constexpr (K <= 8)                          // 16 choices need more than 8 experts
+    if (a.n_experts <= 8) return launch_route<K, 2>(a, stream);
+  if (a.n_experts <= 32) return launch_route<K, 8>(a, stream);
+  return launch_route<K, 32>(a, stream);
 }
 
 }  // namespace
@@ -592,8 +649,8 @@ extern "C" int hinm_route_workspace_bytes(int64_t n_tokens, int32_t n_experts, s
   const int st = check_router(n_tokens, n_experts);
   if (st) return st;
   if (!bytes) return fail(HINM_EINVAL, "bytes is NULL");
-  int nb, ng;
-  route_shape(n_tokens, n_experts, &nb, &ng, bytes);
+  int nb;
+  route_shape(n_tokens, n_experts, &nb, bytes);
   return HINM_OK;
 }
 
@@ -619,7 +676,7 @@ extern "C" int hinm_route(const void* logits, int32_t logits_type, int64_t n_tok
     if (!hinm::aligned(p, 4)) return fail(HINM_EALIGN, "the outputs must be 4-byte aligned");
   RouteArgs a;
   size_t bytes;
-  route_shape(n_tokens, n_experts, &a.n_blocks, &a.n_groups, &bytes);
+  route_shape(n_tokens, n_experts, &a.n_blocks, &bytes);
   if (bytes > 0) {
     if (!workspace || workspace_bytes < bytes)
       return fail(HINM_EWORKSPACE, "route workspace of %zu bytes given, %zu needed", workspace_bytes, bytes);
@@ -643,7 +700,7 @@ extern "C" int hinm_route(const void* logits, int32_t logits_type, int64_t n_tok
   a.src = src;
   a.n_cols = n_cols;
   a.hist = static_cast<int32_t*>(workspace);
-  a.gsum = a.hist ? a.hist + (size_t)a.n_blocks * n_experts : nullptr;
+  a.total = a.hist ? a.hist + (size_t)a.n_blocks * n_experts : nullptr;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
   if (top_k == 1) return launch_route<1>(a, stream);
   if (top_k == 2) return launch_route<2>(a, stream);
@@ -713,8 +770,15 @@ extern "C" int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_col
   const int nt = (int)n_tokens, nc = (int)n_cols, g = staged_rows(n_cols);
   if (g) {
     const dim3 grid((unsigned)std::min<int64_t>((channels + g - 1) / g, kMoveWgs)), block(kMoveThreads);
-#define HINM_COMBINE(G_)                                                                                              \
-  hipLaunchKernelGGL(combine_kernel<G_>, grid, block, 0, st_, ys, channels, nc, ldys, slots, weights, nt, top_k, y, ldy)
+#define HINM_COMBINE_K(G_, K_)                                                                                       \
+  hipLaunchKernelGGL((combine_kernel<G_, K_>), grid, block, 0, st_, ys, channels, nc, ldys, slots, weights, nt, top_k, \
+                     y, ldy)
+#define HINM_COMBINE(G_)                                                                                             \
+  do {                                                                                                               \
+    if (top_k == 1) HINM_COMBINE_K(G_, 1);                                                                           \
+    else if (top_k == 2) HINM_COMBINE_K(G_, 2);                                                                      \
+    else HINM_COMBINE_K(G_, 0);                                                                                      \
+  } while (0)
     switch (g) {
       case 8: HINM_COMBINE(8); break;
       case 4: HINM_COMBINE(4); break;
@@ -722,6 +786,7 @@ extern "C" int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_col
       default: HINM_COMBINE(1); break;
     }
 #undef HINM_COMBINE
+#undef HINM_COMBINE_K
   } else {
     const dim3 grid((unsigned)((n_tokens + 255) / 256),
                     (unsigned)std::min<int64_t>((channels + kMoveRows - 1) / kMoveRows, 65535));

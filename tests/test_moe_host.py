@@ -65,7 +65,7 @@ def test_route_columns_refuses(lib, args, status):
 def test_route_refuses(lib):
     cols = hinm.route_columns(100, 8, 2, 8)
     ws = ctypes.c_size_t()
-    assert lib.hinm_route_workspace_bytes(100, 8, ctypes.byref(ws)) == 0 and ws.value == 2 * 8 * 4
+    assert lib.hinm_route_workspace_bytes(100, 8, ctypes.byref(ws)) == 0 and ws.value == (2 + 1) * 8 * 4
 
     def call(**kw):
         a = dict(logits=FAKE, type=1, n=100, ldl=100, e=8, k=2, renorm=1, align=8, ids=FAKE, w=FAKE, slots=FAKE,
