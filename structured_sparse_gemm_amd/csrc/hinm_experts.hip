@@ -17,6 +17,9 @@ using hinm::fail;
 
 namespace {
 
+// Round to nearest even (the conversion instruction; NaN stays NaN).
+__device__ inline uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
 // 16 bytes at any 2-byte aligned address (one access: the device takes them).
 typedef u32x4 any_u32x4 __attribute__((aligned(2)));
 
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(256) void experts_general_kernel(ExpArgs a) {
       }
       if (n0 + i16 < hi)
         for (int k = 0; k < 4; ++k)
-          a.y[((int64_t)t * a.rows + rb * 64 + wave * 16 + 4 * kc + k) * a.ldy + n0 + i16] = bf16_rne(acc[k]);
+          a.y[((int64_t)t * a.rows + rb * 64 + wave * 16 + 4 * kc + k) * a.ldy + n0 + i16] = to_bf16(acc[k]);
     }
     first += nb;
   }
@@ -238,11 +241,11 @@ struct DecA<true> {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <bool MX4, int NT>
-__global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float* __restrict__ part,
+__global__ __launch_bounds__(256, NT == 16 ? 3 : 2) void experts_decode_kernel(ExpArgs a, float* __restrict__ part,
                                                                 unsigned* __restrict__ counters) {
   constexpr int NB = NT / 16;
   constexpr int XL = NT / 8;                       // X loads a lane for 64 positions
-  constexpr int D = NT == 64 ? 2 : NT == 32 && !MX4 ? 3 : 4;   // blocks in flight (registers)
+  constexpr int D = 2;                             // blocks in flight of a wave
   constexpr int kRed = NT + 4;                     // row pitch of the waves' sums (floats)
   __shared__ __attribute__((aligned(16))) union {
     uint16_t xs[4][64 * NT];
@@ -261,6 +264,12 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
   int splits = 1;
   while (items * splits * 2 <= (int)gridDim.x && nblk >= 16 * splits) splits *= 2;
 
+  // A dense block is multiplied as a 2:4 block whose groups keep positions 0
+  // and 1: its column 2 q + u sits at position 4 q + u, and positions 4 q + 2
+  // and 4 q + 3 hold zeros.  Byte offset in its index list by position, and a
+  // mask that makes the index of a position without a column -1:
+  const uint32_t l_dense = (lane & 2) ? 0u : 4u * (2 * (lane >> 2) + (lane & 1));
+  const int no_index = (lane & 2) ? -1 : 0;
   // this lane's share of a block's X rows: position and first token of load j
   int xpos[XL], xtok[XL];
 #pragma unroll
@@ -329,56 +338,54 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
     int I[D];
     uint32_t P[D];                                 // loads that hold the buffer's last element
 
+    // Block i of this worker.  A block's place in the packed bytes is a scalar
+    // offset and the lane's share a constant.  Past the end the last block is
+    // read again (it is in the caches) and its X rows are zeros, so that the
+    // loop below has no conditions: every wait is for a known number of
+    // younger loads, and a remainder needs no second copy of the code.
+    auto block = [&](int i) { return v < nblk ? v + nw * min(i, cnt - 1) : 0; };
     auto load_idx = [&](int i) -> int {
-      const int b = v + nw * i;
+      const int b = block(i);
       const bool dense = b < a.nkb_d;
-      const uint32_t at = dense ? (uint32_t)(t * a.nkb_d + b) * 32u + (lane & 31)
-                                : (uint32_t)(t * a.nkb_s + b - a.nkb_d) * 64u + lane;
-      return (int)__builtin_amdgcn_raw_buffer_load_b32(dense ? rid : ris, i < cnt ? at * 4u : kOob, 0, 0);
+      const uint32_t kb = dense ? (uint32_t)(t * a.nkb_d + b) : (uint32_t)(t * a.nkb_s + b - a.nkb_d);
+      return (int)__builtin_amdgcn_raw_buffer_load_b32(dense ? rid : ris, dense ? l_dense : 4u * lane,
+                                                       kb * (dense ? 128u : 256u), 0);
     };
     auto load_a = [&](int i, DecA<MX4>& A) {
-      const int b = v + nw * i;
+      const int b = block(i);
       const bool dense = b < a.nkb_d;
       const uint32_t kb = dense ? (uint32_t)(t * a.nkb_d + b) : (uint32_t)(t * a.nkb_s + b - a.nkb_d);
       const __amdgpu_buffer_rsrc_t rv = dense ? rvd : rvs;
+      const uint32_t u = kb * (uint32_t)nrb + rb, um = dense ? 0u : u * 512u;   // a dense block's metadata is not used
       if constexpr (MX4) {
-        const uint32_t u = i < cnt ? kb * (uint32_t)nrb + rb : 0u;
-        A.v = __builtin_amdgcn_raw_buffer_load_b128(rv, i < cnt ? u * 1024u + 256u * kc + 16u * i16 : kOob, 0, 0);
-        A.scale = __builtin_amdgcn_raw_buffer_load_b32(dense ? rsd : rss, i < cnt ? u * 64u + 4u * i16 : kOob, 0, 0);
-        const u32x2 m = __builtin_amdgcn_raw_buffer_load_b64(
-            rm, i < cnt && !dense ? u * 512u + 128u * kc + 8u * i16 : kOob, 0, 0);
+        A.v = __builtin_amdgcn_raw_buffer_load_b128(rv, 256u * kc + 16u * i16, u * 1024u, 0);
+        A.scale = __builtin_amdgcn_raw_buffer_load_b32(dense ? rsd : rss, 4u * i16, u * 64u, 0);
+        const u32x2 m = __builtin_amdgcn_raw_buffer_load_b64(rm, 128u * kc + 8u * i16, um, 0);
         A.m[0] = m[0];
         A.m[1] = m[1];
       } else {
-        const uint32_t row = kb * (uint32_t)a.rows + rb * 64u + i16;
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          A.v[f] = __builtin_amdgcn_raw_buffer_load_b128(rv, i < cnt ? (row + 16u * f) * 64u + 16u * kc : kOob, 0, 0);
-          A.m[f] = __builtin_amdgcn_raw_buffer_load_b16(rm, i < cnt && !dense ? (row + 16u * f) * 8u + 2u * kc : kOob,
-                                                        0, 0);
+          A.v[f] = __builtin_amdgcn_raw_buffer_load_b128(rv, 64u * i16 + 16u * kc + 1024u * f, u * 4096u, 0);
+          A.m[f] = __builtin_amdgcn_raw_buffer_load_b16(rm, 8u * i16 + 2u * kc + 128u * f, um, 0);
         }
       }
     };
-    // X rows of block i from its index word; a dense block fills 32 positions
+    // X rows of block i from its index word
     auto load_x = [&](int i, int iw, u32x4 (&x)[XL], uint32_t& p) {
-      const bool dense = v + nw * i < a.nkb_d;
+      iw = i < cnt ? iw | (block(i) < a.nkb_d ? no_index : 0) : -1;
       p = 0;
 #pragma unroll
       for (int j = 0; j < XL; ++j) {
-        if (dense && 2 * j >= XL) break;
         const int c = __shfl(iw, xpos[j]);
-        x[j] = __builtin_amdgcn_raw_buffer_load_b128(
-            rx, i < cnt && c >= 0 ? __umul24((uint32_t)c, ldx_bytes) + xcol[j] : kOob, 0, 0);
+        x[j] = __builtin_amdgcn_raw_buffer_load_b128(rx, c >= 0 ? __umul24((uint32_t)c, ldx_bytes) + xcol[j] : kOob, 0, 0);
         if (touch) p |= c == a.cin - 1 ? lastj & (1u << j) : 0u;
       }
     };
     auto compute = [&](int i, const DecA<MX4>& A, const u32x4 (&x)[XL], uint32_t p) {
-      const bool dense = v + nw * i < a.nkb_d;
+      const bool dense = block(i) < a.nkb_d;
 #pragma unroll
-      for (int j = 0; j < XL; ++j) {
-        if (dense && 2 * j >= XL) break;
-        *reinterpret_cast<u32x4*>(xs + 8 * (64 * j + lane)) = x[j];
-      }
+      for (int j = 0; j < XL; ++j) *reinterpret_cast<u32x4*>(xs + 8 * (64 * j + lane)) = x[j];
       if (touch) {
 #pragma unroll
         for (int j = 0; j < XL; ++j)
@@ -386,30 +393,27 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
       }
       __builtin_amdgcn_wave_barrier();
       bf16x8 av[4];
+      int sidx[4];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        if constexpr (MX4) av[f] = mx4_expand(A.v[f], mx4_scale((A.scale >> (8 * f)) & 255u));
-        else av[f] = __builtin_bit_cast(bf16x8, A.v[f]);
+        if constexpr (MX4) {
+          av[f] = mx4_expand(A.v[f], mx4_scale((A.scale >> (8 * f)) & 255u));
+          sidx[f] = (int)((A.m[f >> 1] >> (16 * (f & 1))) & 0xffffu);
+        } else {
+          av[f] = __builtin_bit_cast(bf16x8, A.v[f]);
+          sidx[f] = (int)A.m[f];
+        }
+        sidx[f] = dense ? 0x4444 : sidx[f];
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const v4i16 b0 = tr_read(xs + ro[0][nb]), b1 = tr_read(xs + ro[1][nb]);
+        const v4i16 b2 = tr_read(xs + ro[2][nb]), b3 = tr_read(xs + ro[3][nb]);
         const bf16x8 lo8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
-        if (dense) {
+        const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b2, b3, 0, 1, 2, 3, 4, 5, 6, 7));
+        const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
 #pragma unroll
-          for (int f = 0; f < 4; ++f) acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[f], lo8, acc[f][nb], 0, 0, 0);
-        } else {
-          const v4i16 b2 = tr_read(xs + ro[2][nb]), b3 = tr_read(xs + ro[3][nb]);
-          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b2, b3, 0, 1, 2, 3, 4, 5, 6, 7));
-          const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            int sidx;
-            if constexpr (MX4) sidx = (int)((A.m[f >> 1] >> (16 * (f & 1))) & 0xffffu);
-            else sidx = (int)A.m[f];
-            acc[f][nb] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[f], bv, acc[f][nb], sidx, 0, 0);
-          }
-        }
+        for (int f = 0; f < 4; ++f) acc[f][nb] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[f], bv, acc[f][nb], sidx[f], 0, 0);
       }
       __builtin_amdgcn_wave_barrier();
     };
@@ -426,12 +430,10 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
     for (int i = 0; i < cnt; i += D) {
 #pragma unroll
       for (int k = 0; k < D; ++k) {
-        if (i + k < cnt) {
-          compute(i + k, A[k], X[k], P[k]);
-          load_a(i + k + D, A[k]);
-          load_x(i + k + D, I[k], X[k], P[k]);
-          I[k] = load_idx(i + k + 2 * D);
-        }
+        compute(i + k, A[k], X[k], P[k]);
+        load_a(i + k + D, A[k]);
+        load_x(i + k + D, I[k], X[k], P[k]);
+        I[k] = load_idx(i + k + 2 * D);
       }
     }
 
@@ -456,7 +458,7 @@ __global__ __launch_bounds__(256, 2) void experts_decode_kernel(ExpArgs a, float
       uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + row) * a.ldy + n0 + col;
 #pragma unroll
       for (int q = 0; q < OUT; ++q)
-        if (n0 + col + q < hi) dst[q] = bf16_rne(sum[q]);
+        if (n0 + col + q < hi) dst[q] = to_bf16(sum[q]);
     }
     __syncthreads();                               // the sums share LDS with the next item's X rows
   }
@@ -774,7 +776,7 @@ __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, floa
       for (int j = 0; j < C::NTB; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          (r ? yb : ya)[(8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * PITCH + tok_w + 32 * j + (lane & 31)] = bf16_rne(acc[r][j][q]);
+          (r ? yb : ya)[(8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * PITCH + tok_w + 32 * j + (lane & 31)] = to_bf16(acc[r][j][q]);
     __syncthreads();
     // 16-byte stores at 16-byte aligned addresses whatever the row's alignment: piece 0 of a row is what precedes
     // its first aligned address (unaligned stores made 11008 rows of 2047 tokens 14 us slower)
@@ -928,7 +930,7 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
     float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (w.split ? hinm::kWsCounterBytes : 0));
     const dim3 grid(kMaxWgs), block(256);
     switch (token_block(n_experts, n_cols)) {
-      case 16: hipLaunchKernelGGL((experts_decode_kernel<MX4, 16>), grid, block, 0, stream, a, part, ctr); break;
+      case 16: hipLaunchKernelGGL((experts_decode_kernel<MX4, 16>), dim3(768), block, 0, stream, a, part, ctr); break;
       case 32: hipLaunchKernelGGL((experts_decode_kernel<MX4, 32>), grid, block, 0, stream, a, part, ctr); break;
       case 64: hipLaunchKernelGGL((experts_decode_kernel<MX4, 64>), grid, block, 0, stream, a, part, ctr); break;
       case 128: hipLaunchKernelGGL((experts_prefill_kernel<MX4, 128>), grid, block, 0, stream, a, part, ctr); break;

@@ -482,3 +482,61 @@ def test_layer_on_two_streams():
     for i in range(2):
         for y in got[i]:
             assert torch.equal(y.view(torch.int16), want[i].view(torch.int16))
+
+
+# --------------------------------------------------------------------------- X held in LDS
+
+@pytest.mark.parametrize("batch", [1, 2, 3, 4, 5, 8, 9, 15, 16])
+@pytest.mark.parametrize("cout,cin,t,v", [(1024, 4100, 0.6, 0.38), (12800, 260, 0.75, 0.55), (4096, 1028, 0.5, 0.25)])
+def test_product_of_few_tokens(cout, cin, t, v, batch):
+    """Shapes on which the rows of X are held in LDS: row blocks cut between waves and between workgroups, and many
+    row blocks a wave; contiguous X, and a slice whose rows are not aligned and whose buffer ends with an odd
+    element."""
+    print(f"[mx4 spmm] {cout}x{cin} batch={batch}", flush=True)
+    q = hinm.quantize_mx4(_pack(cout, cin, 64, t, v, seed=cin))
+    w = _dense(q.dequantize())
+    g = torch.Generator().manual_seed(batch)
+    for ld, first in ((batch, 0), (batch + 1 + batch % 2, 1)):
+        store = torch.randn(cin * ld, generator=g).bfloat16().to(DEV)
+        x = store.view(cin, ld)[:, ld - batch:]                 # the last row's last element ends the buffer
+        y = hinm.spmm(q, x)
+        y2 = hinm.spmm(q, x)
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+        _check_product(y, w, x, cin - q.plan.z, f"batch {batch} ld {ld}")
+
+
+@pytest.mark.parametrize("counts,align", [([2, 0, 16, 1, 5, 9, 0, 3], 8), ([0, 0, 0, 1, 0, 0, 0, 0], 8),
+                                          ([7, 7, 7, 7, 7, 7, 7, 7], 1), ([40, 0, 0, 3, 0, 17, 0, 0], 8),
+                                          ([0, 3, 0, 0, 0, 0, 0, 0], 1)])
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("odd", [False, True])
+def test_expert_products_of_few_tokens(counts, align, mx4, odd):
+    cout, cin, t, v = 6400, 260, 0.75, 0.55
+    print(f"[experts] few tokens counts={counts} align={align} mx4={mx4} odd={odd}", flush=True)
+    pk = [_pack(cout, cin, 64, t, v, seed=80 + i) for i in range(8)]
+    st = hinm.Experts.stack(pk)
+    if mx4:
+        st = hinm.quantize_mx4(st)
+        pk = [hinm.quantize_mx4(p).dequantize() for p in pk]
+    starts, cols = _ranges(counts, align, 3 if odd else 0, 1 if odd else 0)
+    ld = cols + (cols + 1) % 2 if odd else -(-cols // 8) * 8
+    g = torch.Generator().manual_seed(sum(counts))
+    x = torch.randn(cin, ld, generator=g).bfloat16().to(DEV)[:, ld - cols:]
+    i32 = lambda q: torch.tensor(q, dtype=torch.int32, device=DEV)
+    r = hinm.Routing(i32([[0]]), torch.ones(1, 1, device=DEV), i32([[0]]), i32(starts + [cols]), i32(counts),
+                     i32([0] * cols))
+    mine = torch.zeros(cols, dtype=torch.bool)
+    for s, c in zip(starts, counts):
+        mine[s:s + c] = True
+    x[:, ~mine.to(DEV)] = float("nan")
+    y = torch.full((cout, cols), 7.0, dtype=torch.bfloat16, device=DEV)
+    hinm.spmm_experts(st, x, r, out=y)
+    first = y.clone()
+    hinm.spmm_experts(st, x, r, out=y)
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.int16), y.view(torch.int16))
+    assert bool((y[:, ~mine.to(DEV)] == 7).all())
+    for e, (s, c) in enumerate(zip(starts, counts)):
+        if c:
+            _check_product(y[:, s:s + c], _dense(pk[e]), x[:, s:s + c], cin - pk[e].plan.z, f"expert {e}")
