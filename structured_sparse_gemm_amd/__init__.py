@@ -14,7 +14,7 @@ import ctypes
 import dataclasses
 import functools
 import os
-from typing import Optional
+from typing import Optional, Tuple
 
 import numpy as np
 import torch
@@ -811,15 +811,25 @@ def _call(dev: torch.device, fn, *args) -> None:
             _check(fn(*args))
 
 
-def _split_workspace(dev: torch.device, stream: int, nbytes: int) -> Optional[torch.Tensor]:
-    """The default workspace of an expert or 4-bit product: the stream's own, as for spmm; while a graph is
-    captured, a new one out of the graph's memory, its arrival counters cleared by a node of the graph, so that graphs
-    captured on one stream and replayed on several never share one."""
-    if nbytes and torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        ws[:65536].zero_()
+def _split_workspace(dev: torch.device, stream: int, need: Tuple[int, int]) -> Optional[torch.Tensor]:
+    """The default workspace of an expert or 4-bit product that needs (bytes, bytes without the copy of X).
+
+    The stream's own, as for spmm.  A new one where the workspace holds a copy of X, so that no stream keeps the
+    largest X it has seen, and while a graph is captured, out of the graph's memory, so that graphs captured on one
+    stream and replayed on several never share one; its arrival counters are cleared on the stream (by a node of the
+    graph) where the product may split."""
+    total, split = need
+    if total and (total > split or torch.cuda.is_current_stream_capturing()):
+        ws = torch.empty(total, dtype=torch.uint8, device=dev)
+        if split:
+            ws[:65536].zero_()
         return ws
-    return _workspace(dev, stream, nbytes)
+    return _workspace(dev, stream, total)
+
+
+def _split_need(p: Plan, n_experts: int, n_cols: int, x_aligned: bool) -> Tuple[int, int]:
+    total = spmm_experts_workspace_bytes(p, n_experts, n_cols, x_aligned)
+    return total, total if x_aligned else spmm_experts_workspace_bytes(p, n_experts, n_cols)
 
 
 @dataclasses.dataclass
@@ -1088,9 +1098,7 @@ def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
     key = (batch, ldx % 8 == 0 and x.data_ptr() % 16 == 0)
     need = needs.get(key)
     if need is None:
-        n = ctypes.c_size_t()
-        _check(lib.hinm_spmm_mx4_workspace_bytes(ctypes.byref(p.raw), batch, key[1], ctypes.byref(n)))
-        need = needs[key] = n.value
+        need = needs[key] = _split_need(p, 1, *key)
     stream = _stream_ptr(dev)
     if workspace is None:
         workspace = _split_workspace(dev, stream, need)
@@ -1132,7 +1140,7 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     key = (cols, ldx % 8 == 0 and x.data_ptr() % 16 == 0)
     need = needs.get(key)
     if need is None:
-        need = needs[key] = spmm_experts_workspace_bytes(p, e, *key)
+        need = needs[key] = _split_need(p, e, *key)
     stream = _stream_ptr(dev)
     if workspace is None:
         workspace = _split_workspace(dev, stream, need)

@@ -129,7 +129,8 @@ __global__ __launch_bounds__(256) void experts_general_kernel(ExpArgs a) {
 // 64-row block.  When the items leave workgroups idle, each item's K-blocks
 // are dealt to `splits` workgroups and the partial sums meet in the workspace.
 // ---------------------------------------------------------------------------
-constexpr int kMaxWgs = 512;         // workgroups of a launch: two a compute unit
+constexpr int kCus = 256;            // compute units
+constexpr int kMaxWgs = 512;         // workgroups of a prefill launch: two a compute unit
 
 __device__ inline int plan_blocks(const ExpArgs& a, int nt, int* pre) {
   if (!a.starts) return (a.n_cols + nt - 1) / nt;
@@ -212,18 +213,28 @@ __device__ inline bool join_splits(float (&v)[N], float* part, unsigned* counter
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens an expert: bound by the packed bytes.  Workgroup = 64 rows x NT
-// tokens; its four waves deal the K-blocks among themselves and each works
-// alone - 64 rows x NT tokens of its blocks - so the main loop has no barrier
-// and every load is some blocks ahead: index words 2 D blocks, X rows, values
-// and metadata D blocks.  X rows pass through the wave's own LDS slot for the
-// transposed reads.  At the end the waves' sums meet in LDS, in wave order.
+// Few tokens an expert.  Workgroup = 64 rows x NT tokens; its four waves deal
+// the K-blocks among themselves and each works alone - 64 rows x NT tokens of
+// its blocks - so the main loop has no barrier: index words are loaded two
+// blocks ahead, X rows, values and metadata one block ahead, and X rows pass
+// through the wave's own LDS slot for the transposed reads.  At the end the
+// waves' sums meet in LDS, in wave order.
+//
+// What hides the latency of the index -> X row chain is other waves: five
+// workgroups a compute unit at 16 tokens (88 VGPRs), four at 32.  With two and
+// four blocks in flight and fewer workgroups the same loop was slower (8
+// experts of 11008x4096, 4-bit: 34 and 39 us against 32).  At 16 tokens a
+// gathered X row is 32 bytes that take a 128-byte line of the load path, 64 of
+// the 80 lines of a 4-bit 2:4 block: that path, not memory, bounds the 4-bit
+// product; with bf16 values it is the packed bytes (42 us, 4.9 TB/s).  X held
+// whole in LDS removes those lines but leaves one workgroup a unit: 40 us.
 // ---------------------------------------------------------------------------
+constexpr int decode_wgs(int nt) { return nt == 16 ? 5 : 4; }   // workgroups a compute unit
+
 template <int NT>
 __device__ inline int x_granule(int p, int g) {     // 32-byte granule of position p, 16 tokens g; conflict-free
   if constexpr (NT == 16) return p ^ (((p >> 3) & 1) << 2);
-  else if constexpr (NT == 32) return 2 * p + (g ^ ((p >> 3) & 1));
-  else return 4 * p + (g ^ (((p >> 1) & 1) | (((p >> 3) & 1) << 1)));
+  else return 2 * p + (g ^ ((p >> 3) & 1));
 }
 
 // One block's values and metadata of one lane: 64 rows' fragments f = 0..3.
@@ -241,12 +252,11 @@ struct DecA<true> {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <bool MX4, int NT>
-__global__ __launch_bounds__(256, NT == 16 ? 3 : 2) void experts_decode_kernel(ExpArgs a, float* __restrict__ part,
+__global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(ExpArgs a, float* __restrict__ part,
                                                                 unsigned* __restrict__ counters) {
   constexpr int NB = NT / 16;
   constexpr int XL = NT / 8;                       // X loads a lane for 64 positions
-  constexpr int D = 2;                             // blocks in flight of a wave
-  constexpr int kRed = NT + 4;                     // row pitch of the waves' sums (floats)
+  constexpr int kRed = NT == 16 ? 20 : 34;         // row pitch of the waves' sums (floats); 34: 40 KB of LDS in all
   __shared__ __attribute__((aligned(16))) union {
     uint16_t xs[4][64 * NT];
     float red[4][64 * kRed];
@@ -260,9 +270,13 @@ __global__ __launch_bounds__(256, NT == 16 ? 3 : 2) void experts_decode_kernel(E
   uint16_t* const xs = sh.xs[wave];
 
   const int items = plan_blocks(a, NT, pre) * n_rb;
-  // every wave keeps at least two blocks
+  // A split costs its row blocks a round trip through the workspace (about 3
+  // us), so one is made only where compute units would have no item, and for
+  // at least four K-blocks a wave (4096x11008 at 1 token, 4-bit: 11.0 us with
+  // four splits of its 64 row blocks, 12.8 with two or eight; 11008x4096's 172
+  // row blocks: 10.1 us whole, 10.7 in two).
   int splits = 1;
-  while (items * splits * 2 <= (int)gridDim.x && nblk >= 16 * splits) splits *= 2;
+  while (items * splits * 2 <= kCus && nblk >= 32 * splits) splits *= 2;
 
   // A dense block is multiplied as a 2:4 block whose groups keep positions 0
   // and 1: its column 2 q + u sits at position 4 q + u, and positions 4 q + 2
@@ -277,8 +291,7 @@ __global__ __launch_bounds__(256, NT == 16 ? 3 : 2) void experts_decode_kernel(E
     const int chunk = 64 * j + lane, s = chunk >> 1;
     int p, g;
     if constexpr (NT == 16) p = s ^ (((s >> 3) & 1) << 2), g = 0;
-    else if constexpr (NT == 32) p = s >> 1, g = (s & 1) ^ ((p >> 3) & 1);
-    else p = s >> 2, g = (s & 3) ^ (((p >> 1) & 1) | (((p >> 3) & 1) << 1));
+    else p = s >> 1, g = (s & 1) ^ ((p >> 3) & 1);
     xpos[j] = p;
     xtok[j] = 16 * g + 8 * (chunk & 1);
   }
@@ -333,10 +346,13 @@ __global__ __launch_bounds__(256, NT == 16 ? 3 : 2) void experts_decode_kernel(E
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) acc[f][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // D blocks are in flight; the loops over them stay loops until late in the compiler, which otherwise peels the
+    // first block's work into a copy of its own (0.7 us an item)
+    constexpr int D = 1;
     DecA<MX4> A[D];
     u32x4 X[D][XL];
     int I[D];
-    uint32_t P[D];                                 // loads that hold the buffer's last element
+    uint32_t P[D];                                    // loads that hold the buffer's last element
 
     // Block i of this worker.  A block's place in the packed bytes is a scalar
     // offset and the lane's share a constant.  Past the end the last block is
@@ -849,27 +865,45 @@ int check_bufs(const Buf* b, int n) {
   return HINM_OK;
 }
 
-// Tokens a workgroup takes: from the columns an expert has on average, so that
-// most experts fit one block while few lanes stay empty.
-int token_block(int32_t n_experts, int64_t n_cols) {
+// Tokens a workgroup takes, from the columns an expert has on average (the
+// counts themselves are on the device): 16 or 32 in the decode kernel, 128 or
+// 256 in the prefill kernel.  The decode kernel is the better one for few
+// columns, and for more of them while its items still run at once, three on a
+// compute unit (us, decode 32 against prefill 128, 4-bit: 11008x4096 at 128
+// tokens, 688 items, 18 against 23; at 200, 1204 items, 30 against 28; 8
+// experts of 4096x4096, 39 columns on average, 21 against 32; 55, 30 against
+// 32).  Of the prefill's blocks, 256 halves the bytes of packed values, but an
+// expert a little above 256 then takes two (8 experts of 4096x4096, 128
+// against 256: 64 columns 48 against 42, 135 46 against 62, 199 69 against
+// 64; one weight of 11008x4096: 200 tokens 28 against 32, 400 44 against 40;
+// of 2048x2048: 2048 tokens 19 against 29).
+int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
-  return avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : avg < 256 ? 128 : 256;
+  if (avg <= (n_experts == 1 ? 16 : 20)) return 16;
+  const int64_t some = n_experts > 1 ? std::min<int64_t>(n_experts, n_cols) / 4 : 0;   // blocks that are not full
+  if ((n_experts > 1 && avg <= 48) || (p.cout / 64) * ((n_cols + 31) / 32 + some) <= 3 * kCus) return 32;
+  if (n_experts == 1) return (p.cout / 64) * ((n_cols + 255) / 256) <= kCus ? 128 : 256;
+  return avg <= 64 || (avg > 110 && avg <= 170) ? 128 : 256;
 }
 
 // Workspace: arrival counters and the partial sums of at most kMaxWgs
 // workgroups, where a launch may split; behind them, for the kernel of many
 // tokens and rows that are not 16-byte aligned, a copy of X with aligned rows:
 // gathering unaligned rows made the 11008x4096 product over 2047 tokens 171 us
-// where aligned ones take 111, and the copy takes 10.
+// where aligned ones take 111, and the copy takes 10.  The counters' place is
+// kept free also where nothing splits: the next call with the same workspace
+// may split, and counts on zeros there.
 struct Workspace {
-  int64_t split, copy, ld;
+  int64_t split, copy, ld;           // bytes of counters and sums, bytes of the copy, the copy's row pitch (elements)
+  int64_t copy_at() const { return std::max(split, hinm::kWsCounterBytes); }
+  int64_t bytes() const { return copy ? copy_at() + copy : split; }
 };
 Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols, bool x_aligned) {
   Workspace w{0, 0, 0};
   if (n_cols == 0) return w;
-  const int nt = token_block(n_experts, n_cols);
+  const int nt = token_block(p, n_experts, n_cols);
   const int64_t fewest = (p.cout / 64) * (n_experts == 1 ? (n_cols + nt - 1) / nt : 1);   // items, if any
-  if (fewest * 2 <= kMaxWgs) w.split = hinm::kWsCounterBytes + (int64_t)kMaxWgs * nt * 64 * 4;
+  if (fewest * 2 <= (nt <= 32 ? kCus : kMaxWgs)) w.split = hinm::kWsCounterBytes + (int64_t)kMaxWgs * nt * 64 * 4;
   if (nt >= 128 && !x_aligned) {
     w.ld = (n_cols + 7) / 8 * 8;
     w.copy = (p.cin * w.ld * 2 + 255) / 256 * 256;
@@ -884,7 +918,7 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
            void* stream_) {
   const bool x_aligned = hinm::aligned(x, 16) && ldx % 8 == 0;
   const Workspace w = workspace_of(p, n_experts, n_cols, x_aligned);
-  const int64_t need = w.split + w.copy;
+  const int64_t need = w.bytes();
   if (need > 0) {
     if (!workspace || workspace_bytes < (size_t)need)
       return fail(HINM_EWORKSPACE, "workspace of %zu bytes given, %lld needed", workspace_bytes, (long long)need);
@@ -909,7 +943,7 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
   a.x_end = 1;
   if (w.copy) {
-    uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w.split);
+    uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w.copy_at());
     const dim3 grid((unsigned)((w.ld + 2047) / 2048), (unsigned)std::min(p.cin, 4096));
     hipLaunchKernelGGL(align_kernel, grid, dim3(256), 0, stream, a.x, ldx, a.n_cols, copy, w.ld, p.cin);
     const hipError_t e = hipGetLastError();
@@ -929,10 +963,9 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
     unsigned* ctr = static_cast<unsigned*>(workspace);
     float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + (w.split ? hinm::kWsCounterBytes : 0));
     const dim3 grid(kMaxWgs), block(256);
-    switch (token_block(n_experts, n_cols)) {
-      case 16: hipLaunchKernelGGL((experts_decode_kernel<MX4, 16>), dim3(768), block, 0, stream, a, part, ctr); break;
-      case 32: hipLaunchKernelGGL((experts_decode_kernel<MX4, 32>), grid, block, 0, stream, a, part, ctr); break;
-      case 64: hipLaunchKernelGGL((experts_decode_kernel<MX4, 64>), grid, block, 0, stream, a, part, ctr); break;
+    switch (token_block(p, n_experts, n_cols)) {
+      case 16: hipLaunchKernelGGL((experts_decode_kernel<MX4, 16>), dim3(kCus * decode_wgs(16)), block, 0, stream, a, part, ctr); break;
+      case 32: hipLaunchKernelGGL((experts_decode_kernel<MX4, 32>), dim3(kCus * decode_wgs(32)), block, 0, stream, a, part, ctr); break;
       case 128: hipLaunchKernelGGL((experts_prefill_kernel<MX4, 128>), grid, block, 0, stream, a, part, ctr); break;
       default: hipLaunchKernelGGL((experts_prefill_kernel<MX4, 256>), grid, block, 0, stream, a, part, ctr); break;
     }
@@ -988,7 +1021,7 @@ extern "C" int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_
   if (!bytes) return fail(HINM_EINVAL, "bytes is NULL");
   if (n_cols < 0) return fail(HINM_ESHAPE, "%lld columns", (long long)n_cols);
   const Workspace w = workspace_of(*plan, n_experts, n_cols, x_aligned != 0);
-  *bytes = (size_t)(w.split + w.copy);
+  *bytes = (size_t)w.bytes();
   return HINM_OK;
 }
 

@@ -540,3 +540,48 @@ def test_expert_products_of_few_tokens(counts, align, mx4, odd):
     for e, (s, c) in enumerate(zip(starts, counts)):
         if c:
             _check_product(y[:, s:s + c], _dense(pk[e]), x[:, s:s + c], cin - pk[e].plan.z, f"expert {e}")
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+def test_expert_products_past_32_bit_offsets(mx4):
+    """Rows 2^24 bytes apart and more, the last of them past 2^32 bytes from the first, and a result as far apart."""
+    cout, cin, ld, counts = 64, 264, (1 << 23) + 8, [5, 0, 33]
+    pk = [_pack(cout, cin, 64, 0.5, 0.25, seed=90 + i) for i in range(3)]
+    st = hinm.Experts.stack(pk)
+    if mx4:
+        st = hinm.quantize_mx4(st)
+        pk = [hinm.quantize_mx4(p).dequantize() for p in pk]
+    starts, cols = _ranges(counts, 8)
+    x = torch.empty(cin * ld, dtype=torch.bfloat16, device=DEV).view(cin, ld)[:, :cols]
+    y = torch.empty(cout * ld, dtype=torch.bfloat16, device=DEV).view(cout, ld)[:, :cols]
+    x.copy_(torch.randn(cin, cols, generator=torch.Generator().manual_seed(4)).bfloat16())
+    y.fill_(7.0)
+    i32 = lambda q: torch.tensor(q, dtype=torch.int32, device=DEV)
+    r = hinm.Routing(i32([[0]]), torch.ones(1, 1, device=DEV), i32([[0]]), i32(starts + [cols]), i32(counts),
+                     i32([0] * cols))
+    hinm.spmm_experts(st, x, r, out=y)
+    for e, (s, c) in enumerate(zip(starts, counts)):
+        if c:
+            _check_product(y[:, s:s + c], _dense(pk[e]), x[:, s:s + c], cin - pk[e].plan.z, f"expert {e}")
+        assert bool((y[:, s + c:starts[e + 1] if e < 2 else cols] == 7).all())
+    if mx4:
+        one = hinm.spmm(hinm.quantize_mx4(_pack(cout, cin, 64, 0.5, 0.25, seed=90)), x[:, :5], out=y[:, 8:13])
+        assert torch.equal(one.view(torch.int16), y[:, :5].view(torch.int16))
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_products_of_one_workspace(given):
+    """A product that copies X into the workspace, then one that counts arrivals there, each several times; the
+    first is long enough that it does not split."""
+    cout, cin, n = 2048, 1028, 3 * 2048 + 1
+    q = hinm.quantize_mx4(_pack(cout, cin, 64, 0.5, 0.25, seed=5))
+    gen = torch.Generator().manual_seed(6)
+    xs = [torch.randn(cin, b, generator=gen).bfloat16().to(DEV) for b in (n, 1, 33, 300)]
+    need = max(hinm.spmm_experts_workspace_bytes(q.plan, 1, x.shape[1], x.shape[1] % 8 == 0) for x in xs)
+    want = [hinm.spmm(q, x, workspace=torch.zeros(need, dtype=torch.uint8, device=DEV)) for x in xs]
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV) if given else None
+    for _ in range(3):
+        for x, w in zip(xs, want):
+            assert torch.equal(hinm.spmm(q, x, workspace=ws).view(torch.int16), w.view(torch.int16))
+    if given:
+        assert not bool(ws[:65536].any())

@@ -119,8 +119,12 @@ def test_experts_refuse(lib, mx4):
     if need:
         assert call(ws=None) == 6 and call(wsn=need - 1) == 6 and call(ws=FAKE + 16) == 5
     # many tokens, unaligned rows: the workspace also holds a copy of X with aligned rows
-    many = hinm.spmm_experts_workspace_bytes(p, 1, 1001)
-    assert hinm.spmm_experts_workspace_bytes(p, 1, 1001, x_aligned=False) == many + 256 * 1008 * 2
+    many = hinm.spmm_experts_workspace_bytes(p, 1, 30001)
+    assert hinm.spmm_experts_workspace_bytes(p, 1, 30001, x_aligned=False) == max(many, 65536) + 256 * 30008 * 2
+    # without splits too the counters' 64 KiB are kept free for other calls with the same workspace
+    none = 256 * 64 * 2 * 256
+    assert hinm.spmm_experts_workspace_bytes(p, 1, none) == 0
+    assert hinm.spmm_experts_workspace_bytes(p, 1, none, x_aligned=False) == 65536 + 256 * none * 2
     assert call(e=1, cols=1001, ldx=1001, ldy=1001, wsn=many) == 6
     q = hinm.plan(96, 256, 32, 0.75, 0.55)                       # tile_rows 32
     assert call(k=make(q)) == 2 and "tile_rows" in _err(lib)
