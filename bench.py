@@ -66,7 +66,8 @@ def parse():
 
 CALIB_BYTES = 256 << 20        # size of the plain copy used to scale the HBM byte counters
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_down_proj_4096x11008.md")
-KERNEL_SOURCES = ("structured_sparse_gemm_amd/csrc/hinm_spmm.hip", "structured_sparse_gemm_amd/csrc/hinm_plan.cpp")
+KERNEL_SOURCES = ("structured_sparse_gemm_amd/csrc/hinm_spmm.hip", "structured_sparse_gemm_amd/csrc/hinm_device.h",
+                  "structured_sparse_gemm_amd/csrc/hinm_plan.cpp")
 
 
 def kernel_source_hash() -> str:

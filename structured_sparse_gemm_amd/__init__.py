@@ -782,8 +782,14 @@ def boundary_search_tiles(importance: torch.Tensor, perm: Optional[torch.Tensor]
 # Mixture-of-experts layers and 4-bit microscaled values.
 # ---------------------------------------------------------------------------
 
+def _on_gpu(dev: torch.device) -> None:
+    if dev.type != "cuda":
+        raise ValueError(f"the weights and the routing must be on a GPU, not on {dev}")
+
+
 def _matrix(t: torch.Tensor, rows: Optional[int], cols: Optional[int], dev: torch.device, what: str) -> int:
     """Checks a bf16 matrix and returns its row stride in elements."""
+    _on_gpu(dev)
     if (t.dtype != torch.bfloat16 or t.dim() != 2 or t.device != dev or (rows is not None and t.shape[0] != rows)
             or (cols is not None and t.shape[1] != cols)):
         raise ValueError(f"{what} must be bf16 [{'channels' if rows is None else rows}, "
@@ -1043,6 +1049,7 @@ class HinmMx4:
 
     def dequantize(self):
         """The bf16 packed weight (or Experts stack) of the same values, exact (hinm_mx4_dequantize)."""
+        _on_gpu(self.device)
         lead = () if self.n_experts is None else (self.n_experts,)
         bufs = {k: _empty((*lead, *s), t, self.device) for k, (s, t) in _packed_shapes(self.plan).items()}
         out = (HinmPacked if self.n_experts is None else Experts)(self.plan, **bufs)
@@ -1078,6 +1085,7 @@ def quantize_mx4(packed) -> HinmMx4:
     p, n = packed.plan, packed.n_experts if isinstance(packed, Experts) else None
     lead = () if n is None else (n,)
     dev = packed.device
+    _on_gpu(dev)
     out = HinmMx4(p, **{k: _empty((*lead, *s), t, dev) for k, (s, t) in _mx4_shapes(p).items()}, n_experts=n)
     _call(dev, library().hinm_mx4_quantize, ctypes.byref(packed.struct()), n or 1, ctypes.byref(out.struct()),
           _stream_ptr(dev))
@@ -1102,6 +1110,8 @@ def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
     stream = _stream_ptr(dev)
     if workspace is None:
         workspace = _split_workspace(dev, stream, need)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     _call(dev, lib.hinm_spmm_mx4, ctypes.byref(st), x.data_ptr(), batch, ldx, out.data_ptr(), ldy,
           workspace.data_ptr() if workspace is not None else None, workspace.numel() if workspace is not None else 0,
           stream)
@@ -1144,6 +1154,8 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     stream = _stream_ptr(dev)
     if workspace is None:
         workspace = _split_workspace(dev, stream, need)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     lib = library()
     _call(dev, lib.hinm_spmm_experts_mx4 if mx4 else lib.hinm_spmm_experts, ctypes.byref(experts.struct()), e,
           x.data_ptr(), cols, ldx, routing.starts.data_ptr(), routing.counts.data_ptr(), out.data_ptr(), ldy,

@@ -585,3 +585,20 @@ def test_products_of_one_workspace(given):
             assert torch.equal(hinm.spmm(q, x, workspace=ws).view(torch.int16), w.view(torch.int16))
     if given:
         assert not bool(ws[:65536].any())
+
+
+def test_workspaces_are_checked():
+    q = hinm.quantize_mx4(_pack(64, 68, 64, 0.5, 0.25, seed=1))
+    st = hinm.Experts.stack([_pack(64, 68, 64, 0.5, 0.25, seed=2)])
+    x = torch.zeros(68, 8, dtype=torch.bfloat16, device=DEV)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    r = hinm.Routing(i32([[0]]), torch.ones(1, 1, device=DEV), i32([[0]]), i32([0, 8]), i32([8]), i32([0] * 8))
+    for bad in (torch.zeros(1 << 24, dtype=torch.uint8), torch.zeros(1 << 24, dtype=torch.float32, device=DEV),
+                torch.zeros(1 << 24, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            hinm.spmm(q, x, workspace=bad)
+        with pytest.raises(ValueError):
+            hinm.spmm_experts(st, x, r, workspace=bad)
+    for small in (0, 65536):
+        with pytest.raises(hinm.HinmError):
+            hinm.spmm_experts(st, x, r, workspace=torch.zeros(small, dtype=torch.uint8, device=DEV))

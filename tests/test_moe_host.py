@@ -239,3 +239,19 @@ def test_plain_four_bit_rule():
     assert mx4_block(np.zeros(32))[0] == 0
     assert mx4_block(np.full(32, 2.0 ** -130))[0] == 0 and mx4_block(np.full(32, np.inf))[0] == 255
     assert set(GRID) == {0, .5, 1, 1.5, 2, 3, 4, 6}
+
+
+def test_binding_refuses_weights_on_the_host():
+    """Everything else about these calls is right: only the place of the tensors is refused."""
+    p = hinm.plan(128, 256, 64, 0.75, 0.55)
+    st = hinm.Experts.stack([hinm.alloc_packed(p, "cpu") for _ in range(4)])
+    q = hinm.HinmMx4(p, **{k: torch.zeros(s, dtype=t) for k, (s, t) in hinm._mx4_shapes(p).items()})
+    r, b = _routing(), torch.bfloat16
+    for call in (lambda: hinm.dispatch(torch.zeros(16, 6, dtype=b), r),
+                 lambda: hinm.combine(torch.zeros(16, 40, dtype=b), r),
+                 lambda: hinm.spmm_experts(st, torch.zeros(256, 40, dtype=b), r),
+                 lambda: hinm.spmm(q, torch.zeros(256, 3, dtype=b)),
+                 lambda: hinm.quantize_mx4(st), lambda: hinm.quantize_mx4(hinm.alloc_packed(p, "cpu")),
+                 q.dequantize):
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()
