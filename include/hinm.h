@@ -573,8 +573,8 @@ int hinm_route(const void* logits, int32_t logits_type, int64_t n_tokens, int64_
  * X (device) bf16 [channels][ldx], ldx >= n_tokens; XS (device) bf16
  * [channels][ldxs], ldxs >= n_cols, every element of XS[:, 0:n_cols] is
  * written and nothing else.  The bits of X are copied.  X and XS must be
- * 2-byte aligned and must not overlap.  channels == 0 or n_cols == 0 is a
- * no-op.  Asynchronous on `stream`.  Errors: HINM_EINVAL, HINM_ESHAPE,
+ * 2-byte aligned and must not overlap.  n_tokens and n_cols are at most 2^30,
+ * channels below 2^31.  channels == 0 or n_cols == 0 is a no-op.  Asynchronous on `stream`.  Errors: HINM_EINVAL, HINM_ESHAPE,
  * HINM_EALIGN, HINM_EHIP, HINM_EDEVICE. */
 int hinm_dispatch(const void* x_bf16, int64_t channels, int64_t n_tokens, int64_t ldx, const int32_t* src,
                   int64_t n_cols, void* xs_bf16, int64_t ldxs, void* stream);

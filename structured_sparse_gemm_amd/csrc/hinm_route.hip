@@ -356,6 +356,7 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteArgs a) {
 constexpr int kMoveThreads = 512;
 constexpr int kMoveLds = 80 * 1024;
 constexpr int64_t kMoveWgs = 1024;
+constexpr int64_t kMoveMax = 1 << 30;  // columns and tokens: a thread's next one still fits an int
 constexpr int kMoveRows = 16;      // channels a workgroup of the direct kernels walks
 
 typedef u32x4 any_u32x4 __attribute__((aligned(2)));   // 16 bytes at any 2-byte aligned address
@@ -720,8 +721,8 @@ extern "C" int hinm_dispatch(const void* x_bf16, int64_t channels, int64_t n_tok
   hinm::clear_error();
   if (channels < 0 || n_tokens < 0 || n_cols < 0)
     return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must not be negative");
-  if (channels > INT32_MAX || n_tokens > INT32_MAX || n_cols > INT32_MAX)
-    return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must fit in int32");
+  if (channels > INT32_MAX || n_tokens > kMoveMax || n_cols > kMoveMax)
+    return fail(HINM_ESHAPE, "channels must be below 2^31, n_tokens and n_cols at most 2^30");
   if (ldx < n_tokens || ldxs < n_cols)
     return fail(HINM_ESHAPE, "ldx=%lld must be >= n_tokens=%lld and ldxs=%lld >= n_cols=%lld", (long long)ldx,
                 (long long)n_tokens, (long long)ldxs, (long long)n_cols);
@@ -757,8 +758,8 @@ extern "C" int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_col
   hinm::clear_error();
   if (channels < 0 || n_tokens < 0 || n_cols < 0)
     return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must not be negative");
-  if (channels > INT32_MAX || n_tokens > INT32_MAX || n_cols > INT32_MAX)
-    return fail(HINM_ESHAPE, "channels, n_tokens and n_cols must fit in int32");
+  if (channels > INT32_MAX || n_tokens > kMoveMax || n_cols > kMoveMax)
+    return fail(HINM_ESHAPE, "channels must be below 2^31, n_tokens and n_cols at most 2^30");
   if (top_k < 1 || top_k > HINM_MAX_TOP_K) return fail(HINM_ESHAPE, "top_k=%d; 1 to %d are supported", top_k, HINM_MAX_TOP_K);
   if (ldy < n_tokens || ldys < n_cols)
     return fail(HINM_ESHAPE, "ldy=%lld must be >= n_tokens=%lld and ldys=%lld >= n_cols=%lld", (long long)ldy,

@@ -602,3 +602,68 @@ def test_workspaces_are_checked():
     for small in (0, 65536):
         with pytest.raises(hinm.HinmError):
             hinm.spmm_experts(st, x, r, workspace=torch.zeros(small, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+def test_layer_without_tokens(mx4):
+    st = hinm.Experts.stack([_pack(128, 68, 64, 0.5, 0.25, seed=i) for i in range(3)])
+    st = hinm.quantize_mx4(st) if mx4 else st
+    r = hinm.route(torch.zeros(3, 0, dtype=torch.bfloat16, device=DEV), 2)
+    xs = hinm.dispatch(torch.zeros(68, 0, dtype=torch.bfloat16, device=DEV), r)
+    ys = hinm.spmm_experts(st, xs, r)
+    y = hinm.combine(ys, r)
+    torch.cuda.synchronize()
+    assert r.counts.tolist() == [0, 0, 0] and y.shape == (128, 0)
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("e,most", [(300, 3), (1024, 1), (65, 90)])
+def test_many_experts(e, most, mx4):
+    """More experts than a wave has lanes, most of them with few columns or none, in both kernels."""
+    pk = [_pack(64, 36, 64, 0.5, 0.25, seed=i) for i in range(5)]
+    st = hinm.Experts.stack([pk[i % 5] for i in range(e)])
+    if mx4:
+        st = hinm.quantize_mx4(st)
+        pk = [hinm.quantize_mx4(p).dequantize() for p in pk]
+    g = torch.Generator().manual_seed(e)
+    counts = torch.randint(0, most + 1, (e,), generator=g).tolist()
+    starts, cols = _ranges(counts, 1, lead=2)
+    x = torch.randn(36, cols, generator=g).bfloat16().to(DEV)
+    i32 = lambda q: torch.tensor(q, dtype=torch.int32, device=DEV)
+    r = hinm.Routing(i32([[0]]), torch.ones(1, 1, device=DEV), i32([[0]]), i32(starts + [cols]), i32(counts),
+                     i32([0] * cols))
+    y = hinm.spmm_experts(st, x, r)
+    w = [_dense(p) for p in pk]
+    for i, (s, c) in enumerate(zip(starts, counts)):
+        if c:
+            _check_product(y[:, s:s + c], w[i % 5], x[:, s:s + c], 36 - pk[0].plan.z, f"expert {i}")
+
+
+def test_products_that_copy_x_in_graphs_on_two_streams():
+    """Two graphs of a long product with unaligned rows and a split one, replayed together several times with eager
+    work between."""
+    q = hinm.quantize_mx4(_pack(2048, 1028, 64, 0.5, 0.25, seed=5))
+    gen = torch.Generator().manual_seed(7)
+    streams, graphs, outs, want = [torch.cuda.Stream() for _ in range(2)], [], [], []
+    for s in streams:
+        xs = [torch.randn(1028, b, generator=gen).bfloat16().to(DEV) for b in (6145, 1, 301)]
+        want.append([hinm.spmm(q, x) for x in xs])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append([hinm.spmm(q, x) for x in xs])
+        graphs.append((g, xs))
+    for _ in range(4):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for (g, xs), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = hinm.spmm(q, graphs[0][1][1])
+        torch.cuda.synchronize()
+        assert torch.equal(eager.view(torch.int16), want[0][1].view(torch.int16))
+        for o, w in zip(outs, want):
+            for a, b in zip(o, w):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16))

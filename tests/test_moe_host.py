@@ -89,10 +89,13 @@ def test_dispatch_and_combine_refuse(lib):
     assert dispatch(x=None) == 1 and dispatch(src=None) == 1 and dispatch(xs=None) == 1
     assert dispatch(x=FAKE + 1) == 5 and dispatch(src=FAKE + 2) == 5
     assert dispatch(c=0) == 0 and dispatch(cols=0) == 0
+    big = (1 << 30) + 1
+    assert dispatch(cols=big, ldxs=big) == 2 and dispatch(n=big, ldx=big) == 2
 
     def combine(ys=FAKE, c=4, cols=16, ldys=16, slots=FAKE, w=FAKE, n=8, k=2, y=FAKE, ldy=8):
         return lib.hinm_combine(ys, c, cols, ldys, slots, w, n, k, y, ldy, None)
 
+    assert combine(cols=big, ldys=big) == 2 and combine(n=big, ldy=big) == 2
     assert combine(ldys=15) == 2 and combine(ldy=7) == 2 and combine(k=0) == 2 and combine(k=17) == 2
     assert combine(ys=None) == 1 and combine(slots=None) == 1 and combine(w=None) == 1 and combine(y=None) == 1
     assert combine(y=FAKE + 1) == 5 and combine(w=FAKE + 2) == 5
