@@ -201,13 +201,19 @@ __device__ inline bool join_splits(float (&v)[N], float* part, unsigned* counter
   const float* p0 = part + (int64_t)item * splits * N * 256 + threadIdx.x;
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    float t[N];
+  constexpr int U = N <= 8 ? 4 : 1;                // splits whose loads are in flight at once (one by one: +0.5 us)
+  for (int s = 0; s < splits; s += U) {
+    float t[U][N];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      t[k] = __hip_atomic_load(p0 + (int64_t)s * N * 256 + k * 256, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += t[k];
+      for (int k = 0; k < N; ++k)
+        t[u][k] = __hip_atomic_load(p0 + (int64_t)min(s + u, splits - 1) * N * 256 + k * 256, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += s + u < splits ? t[u][k] : 0.f;
   }
   return true;
 }
@@ -226,8 +232,9 @@ __device__ inline bool join_splits(float (&v)[N], float* part, unsigned* counter
 // experts of 11008x4096, 4-bit: 34 and 39 us against 32).  At 16 tokens a
 // gathered X row is 32 bytes that take a 128-byte line of the load path, 64 of
 // the 80 lines of a 4-bit 2:4 block: that path, not memory, bounds the 4-bit
-// product; with bf16 values it is the packed bytes (42 us, 4.9 TB/s).  X held
-// whole in LDS removes those lines but leaves one workgroup a unit: 40 us.
+// product (29 us); with bf16 values it is the packed bytes (209 MB in 52 us, 4.0
+// TB/s from memory, in 40 partly from the last-level cache).  X held whole in
+// LDS removes those lines but leaves one workgroup a unit: 41 us.
 // ---------------------------------------------------------------------------
 constexpr int decode_wgs(int nt) { return nt == 16 ? 5 : 4; }   // workgroups a compute unit
 
@@ -252,8 +259,9 @@ struct DecA<true> {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <bool MX4, int NT>
-__global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(ExpArgs a, float* __restrict__ part,
-                                                                unsigned* __restrict__ counters) {
+__global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(ExpArgs a,
+                                                                                   float* __restrict__ part,
+                                                                                   unsigned* __restrict__ counters) {
   constexpr int NB = NT / 16;
   constexpr int XL = NT / 8;                       // X loads a lane for 64 positions
   constexpr int kRed = NT == 16 ? 20 : 34;         // row pitch of the waves' sums (floats); 34: 40 KB of LDS in all
@@ -270,11 +278,11 @@ __global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(Exp
   uint16_t* const xs = sh.xs[wave];
 
   const int items = plan_blocks(a, NT, pre) * n_rb;
-  // A split costs its row blocks a round trip through the workspace (about 3
+  // A split costs its row blocks a round trip through the workspace (about 2.5
   // us), so one is made only where compute units would have no item, and for
-  // at least four K-blocks a wave (4096x11008 at 1 token, 4-bit: 11.0 us with
-  // four splits of its 64 row blocks, 12.8 with two or eight; 11008x4096's 172
-  // row blocks: 10.1 us whole, 10.7 in two).
+  // at least four K-blocks a wave (4-bit, 1 token: 4096x11008 10.4
+  // us with four splits of its 64 row blocks, 11.2 with eight; 11008x4096's
+  // 172 row blocks 8.3 us whole, 10.6 in two).
   int splits = 1;
   while (items * splits * 2 <= kCus && nblk >= 32 * splits) splits *= 2;
 
