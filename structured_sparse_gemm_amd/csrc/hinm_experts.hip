@@ -36,6 +36,7 @@ struct ExpArgs {
   int x_end;                         // 1: the buffer of X ends with row cin - 1's last column (0: its rows are padded)
   const int32_t *starts, *counts;    // NULL: one range, all columns
   int n_experts, n_cols;
+  int may_split;                     // the workspace has room for arrival counters and partial sums
   int cin, cout, rows, n_tiles, nkb_d, nkb_s;
 };
 
@@ -127,7 +128,9 @@ __global__ __launch_bounds__(256) void experts_general_kernel(ExpArgs a) {
 // cut into ceil(n_e / NT) token blocks, numbered through all experts
 // (pre[e] = blocks before expert e), and an item is one token block times one
 // 64-row block.  When the items leave workgroups idle, each item's K-blocks
-// are dealt to `splits` workgroups and the partial sums meet in the workspace.
+// are dealt to `splits` workgroups and the partial sums meet in the workspace;
+// never where the host, which does not know the ranges, gave it no room for
+// them (may_split).
 // ---------------------------------------------------------------------------
 constexpr int kCus = 256;            // compute units
 constexpr int kMaxWgs = 512;         // workgroups of a prefill launch: two a compute unit
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(Exp
   // us with four splits of its 64 row blocks, 11.2 with eight; 11008x4096's
   // 172 row blocks 8.3 us whole, 10.6 in two).
   int splits = 1;
-  while (items * splits * 2 <= kCus && nblk >= 32 * splits) splits *= 2;
+  while (a.may_split && items * splits * 2 <= kCus && nblk >= 32 * splits) splits *= 2;
 
   // A dense block is multiplied as a 2:4 block whose groups keep positions 0
   // and 1: its column 2 q + u sits at position 4 q + u, and positions 4 q + 2
@@ -726,7 +729,8 @@ __global__ __launch_bounds__(256, 2) void experts_prefill_kernel(ExpArgs a, floa
 
   const int items = plan_blocks(a, NT, pre) * n_rb;
   int splits = 1;
-  while (splits < 4 && items * splits * 2 <= (int)gridDim.x && a.nkb_d + 2 * a.nkb_s >= 16 * splits) splits *= 2;
+  while (a.may_split && splits < 4 && items * splits * 2 <= (int)gridDim.x && a.nkb_d + 2 * a.nkb_s >= 16 * splits)
+    splits *= 2;
   const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8, per_xcd = gridDim.x / 8;
   const int w_lo = (int)((int64_t)xcd * items * splits / 8), w_hi = (int)((int64_t)(xcd + 1) * items * splits / 8);
   __amdgpu_buffer_rsrc_t rx;
@@ -901,7 +905,11 @@ int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
 }
 
 // Workspace: arrival counters and the partial sums of at most kMaxWgs
-// workgroups, where a launch may split; behind them, for the kernel of many
+// workgroups, where a launch may split: with several experts when one token
+// block would leave workgroups idle, with one expert when all columns would.
+// A lone range shorter than the columns may leave them idle all the same; it
+// then runs unsplit (may_split), so that what the product needs and its bits
+// depend on what the host knows.  Behind them, for the kernel of many
 // tokens and rows that are not 16-byte aligned, a copy of X with aligned rows:
 // gathering unaligned rows made the 11008x4096 product over 2047 tokens 171 us
 // where aligned ones take 111, and the copy takes 10.  The counters' place is
@@ -948,6 +956,7 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
   a.counts = counts;
   a.n_experts = n_experts;
   a.n_cols = (int)n_cols;
+  a.may_split = w.split > 0;
   a.cin = p.cin;
   a.cout = p.cout;
   a.rows = p.tile_rows;
