@@ -973,7 +973,7 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
     if (e != hipSuccess) return fail(HINM_EHIP, "experts launch: %s", hipGetErrorString(e));
     a.x = copy;
     a.ldx = ldx = w.ld;
-    a.x_end = 0;
+    a.x_end = w.ld == n_cols;            // a multiple of 8 columns leaves the copy's rows no pad
   }
   // The fast kernels address X with 32-bit buffer offsets and 24-bit
   // multiplies (row number, row pitch in bytes).

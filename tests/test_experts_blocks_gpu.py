@@ -86,3 +86,29 @@ def test_one_expert_with_fewer_columns_than_the_buffer(cout, cin, t, v, cols, st
     torch.cuda.synchronize()
     _check(y[:, start:start + count], w, x[:, start:start + count], cin - st.plan.z, "one expert")
     assert bool((y[:, :start] == 7).all()) and bool((y[:, start + count:] == 7).all())
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("cout,block,counts", [(4096, 128, [150, 100, 147]), (4096, 256, [300, 211, 401])])
+def test_last_column_of_a_copied_x(cout, block, counts, mx4):
+    """X rows that are not aligned are copied.  With a multiple of 8 columns the copy's rows have no pad, and a range
+    that starts at an odd column and ends with the buffer has the last element of X in a word that crosses its end:
+    the last column takes it all the same."""
+    cin, t, v = 516, 0.5, 0.25
+    st, ws = _stack(cout, cin, t, v, 3, mx4)
+    cols = -(-(sum(counts) + 3) // 8) * 8                     # leading columns that belong to nobody
+    starts = [cols - sum(counts[i:]) for i in range(3)]
+    assert starts[2] % 2 == 1
+    room = hinm.spmm_experts_workspace_bytes(st.plan, 3, cols)
+    assert room == 65536 + 512 * 64 * block * 4
+    assert hinm.spmm_experts_workspace_bytes(st.plan, 3, cols, x_aligned=False) == room + -(-cin * cols * 2 // 256) * 256
+    x = torch.randn(cin, cols + 1, generator=torch.Generator().manual_seed(block)).bfloat16().to(DEV)[:, 1:]
+    x[-1] = 64.0                                              # a lost element shows in every row that keeps it
+    y = torch.full((cout, cols), 7.0, dtype=torch.bfloat16, device=DEV)
+    print(f"[experts] copied X, {cout} rows, {cols} columns from {starts[2]}, mx4={mx4}", flush=True)
+    hinm.spmm_experts(st, x, _routing(starts, counts, cols), out=y)
+    torch.cuda.synchronize()
+    assert any(bool(w[:, -1].any()) for w in ws)
+    for w, s, c in zip(ws, starts, counts):
+        _check(y[:, s:s + c], w, x[:, s:s + c], cin - st.plan.z, f"columns from {s}")
+    assert bool((y[:, :starts[0]] == 7).all())
