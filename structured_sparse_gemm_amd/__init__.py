@@ -481,6 +481,19 @@ def spmm_workspace_bytes(p: Plan, batch: int) -> int:
     return n.value
 
 
+def _one_weight(packed, what: str) -> None:
+    """Refuses what is not a single uniform bf16 weight: the C calls read its buffers as such."""
+    if isinstance(packed, HinmPacked):
+        return
+    if isinstance(packed, Experts) or (isinstance(packed, HinmMx4) and packed.n_experts is not None):
+        raise ValueError(f"{what} takes one weight; a stack of experts is multiplied by spmm_experts")
+    if isinstance(packed, HinmMx4):
+        raise ValueError(f"{what} takes bf16 values; 4-bit weights are multiplied one at a time by spmm")
+    if isinstance(packed, HinmTPacked):
+        raise ValueError(f"{what} takes uniform packed weights (pack, not pack_tiles)")
+    raise ValueError(f"{what} takes a packed weight, not a {type(packed).__name__}")
+
+
 _ws_cache = {}
 _ws_retired = []
 _opt_gen = 0
@@ -558,9 +571,11 @@ def spmm(packed: HinmPacked, x: torch.Tensor, out: Optional[torch.Tensor] = None
         if out_rows is not None:
             raise ValueError("out_rows is not supported with 4-bit values")
         return _spmm_mx4(packed, x, out, workspace)
+    tiled = isinstance(packed, HinmTPacked)
+    if not tiled and not isinstance(packed, HinmPacked):
+        _one_weight(packed, "spmm")
     p = packed.plan
     dev = x.device
-    tiled = isinstance(packed, HinmTPacked)
     if tiled and out_rows is not None:
         raise ValueError("out_rows is not supported with per-tile counts")
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[0] != p.cin or dev != packed.idx_24.device:
@@ -608,14 +623,15 @@ def spmm(packed: HinmPacked, x: torch.Tensor, out: Optional[torch.Tensor] = None
 
 class Group:
     """Several packed weights that multiply the same activations (hinm_spmm_group), e.g. the q, k and v
-    projections of a layer.  Holds the C array of weight pointers; the weights must stay alive."""
+    projections of a layer.  Takes bf16 weights from pack.  Holds the C array of weight pointers; the weights must
+    stay alive."""
 
     def __init__(self, packed):
         self.packed = list(packed)
         if not 1 <= len(self.packed) <= 8:
             raise ValueError("a group holds 1 to 8 packed weights")
-        if any(isinstance(p, HinmTPacked) for p in self.packed):
-            raise ValueError("groups take uniform packed weights (pack, not pack_tiles)")
+        for p in self.packed:
+            _one_weight(p, "a group")
         self.structs = [p.struct() for p in self.packed]
         self.ptrs = (ctypes.c_void_p * len(self.structs))(*[ctypes.addressof(st) for st in self.structs])
         self._need = {}
@@ -664,6 +680,7 @@ def spmm_noalloc(packed: HinmPacked, x: torch.Tensor, out: torch.Tensor) -> torc
     scratch is the library's own device array, shared by every call on the device, so calls on different
     streams of one device must not overlap).  x bf16 [cin, batch], out bf16 [cout, batch], both with unit
     column stride.  Asynchronous on the current stream."""
+    _one_weight(packed, "spmm_noalloc")
     p = packed.plan
     dev = x.device
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[0] != p.cin or dev != packed.device or x.stride(1) != 1:
@@ -682,6 +699,7 @@ def spmm_noalloc(packed: HinmPacked, x: torch.Tensor, out: torch.Tensor) -> torc
 def translate_indices(packed: HinmPacked, mapping: torch.Tensor) -> HinmPacked:
     """Rewrites the packed index lists in place through ``mapping`` (int32 [cin] permutation on the device):
     index i becomes mapping[i], pads stay -1 (hinm_translate_indices).  Synchronous; returns ``packed``."""
+    _one_weight(packed, "translate_indices")
     p = packed.plan
     dev = packed.idx_24.device
     if mapping.dtype != torch.int32 or mapping.shape != (p.cin,) or not mapping.is_contiguous() or mapping.device != dev:
