@@ -807,7 +807,6 @@ def _on_gpu(dev: torch.device) -> None:
 
 def _matrix(t: torch.Tensor, rows: Optional[int], cols: Optional[int], dev: torch.device, what: str) -> int:
     """Checks a bf16 matrix and returns its row stride in elements."""
-    _on_gpu(dev)
     if (t.dtype != torch.bfloat16 or t.dim() != 2 or t.device != dev or (rows is not None and t.shape[0] != rows)
             or (cols is not None and t.shape[1] != cols)):
         raise ValueError(f"{what} must be bf16 [{'channels' if rows is None else rows}, "
@@ -931,6 +930,7 @@ def dispatch(x: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = No
     dev = routing.src.device
     ldx = _matrix(x, None, routing.n_tokens, dev, "x")
     _index(routing.src, (routing.n_cols,), dev, "routing.src")
+    _on_gpu(dev)
     c, cols = x.shape[0], routing.n_cols
     if out is None:
         out = torch.empty((c, cols), dtype=torch.bfloat16, device=dev)
@@ -948,6 +948,7 @@ def combine(y: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = Non
     n, k, c = routing.n_tokens, routing.top_k, y.shape[0]
     _index(routing.slots, (n, k), dev, "routing.slots")
     _index(routing.weights, (n, k), dev, "routing.weights", torch.float32)
+    _on_gpu(dev)
     if out is None:
         out = torch.empty((c, n), dtype=torch.bfloat16, device=dev)
     ldo = _matrix(out, c, n, dev, "out")
@@ -1115,6 +1116,7 @@ def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
         raise ValueError("spmm takes one weight; multiply a stack with spmm_experts")
     p, dev = packed.plan, packed.idx_24.device
     ldx = _matrix(x, p.cin, None, dev, "x")
+    _on_gpu(dev)
     batch = x.shape[1]
     if out is None:
         out = torch.empty((p.cout, batch), dtype=torch.bfloat16, device=dev)
@@ -1161,6 +1163,7 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
         raise ValueError(f"the routing has {routing.counts.shape[0]} experts, the stack {e}")
     _index(routing.starts, (e + 1,), dev, "routing.starts")
     _index(routing.counts, (e,), dev, "routing.counts")
+    _on_gpu(dev)
     if out is None:
         out = torch.empty((p.cout, cols), dtype=torch.bfloat16, device=dev)
     ldy = _matrix(out, p.cout, cols, dev, "out")
