@@ -1148,7 +1148,7 @@ def spmm_experts_workspace_bytes(p: Plan, n_experts: int, n_cols: int, x_aligned
 def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Every expert's product over its own columns (hinm_spmm_experts, or hinm_spmm_experts_mx4 for a quantised
-    stack): x bf16 [cin, columns] in the routing's order -> bf16 [cout, columns].
+    stack): x bf16 [cin, columns] in the routing's order, as many as it has -> bf16 [cout, columns].
 
     Columns that belong to no expert are left as they were in ``out`` (unspecified in a new one).  The ranges are
     read on the device: no host synchronisation.  Asynchronous on the current stream; workspace as in spmm, but
@@ -1161,6 +1161,8 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     cols = x.shape[1]
     if routing.counts.shape[0] != e:
         raise ValueError(f"the routing has {routing.counts.shape[0]} experts, the stack {e}")
+    if cols != routing.n_cols:
+        raise ValueError(f"x has {cols} columns, the routing {routing.n_cols}")
     _index(routing.starts, (e + 1,), dev, "routing.starts")
     _index(routing.counts, (e,), dev, "routing.counts")
     _on_gpu(dev)

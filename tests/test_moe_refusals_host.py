@@ -68,3 +68,11 @@ def test_spmm_of_a_four_bit_weight(x, message):
     q = hinm.HinmMx4(p, **{k: torch.zeros(s, dtype=t) for k, (s, t) in hinm._mx4_shapes(p).items()})
     with pytest.raises(ValueError, match=message):
         hinm.spmm(q, x)
+
+
+@pytest.mark.parametrize("four_bit", [False, True])
+@pytest.mark.parametrize("cols", [0, 6, 39, 41])
+def test_spmm_experts_of_another_routing(cols, four_bit):
+    """X before dispatch (6 tokens) or in the order of another routing: its ranges would be cut silently."""
+    with pytest.raises(ValueError, match=f"x has {cols} columns, the routing 40"):
+        hinm.spmm_experts(_stack(four_bit=four_bit), torch.zeros(256, cols, dtype=BF16), _routing())
