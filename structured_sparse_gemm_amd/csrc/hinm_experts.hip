@@ -849,13 +849,19 @@ __global__ __launch_bounds__(256) void align_kernel(const uint16_t* __restrict__
     }
 }
 
+int check_cols(int64_t n_cols) {
+  if (n_cols < 0) return fail(HINM_ESHAPE, "%lld columns", (long long)n_cols);
+  if (n_cols > (1 << 24)) return fail(HINM_ESHAPE, "%lld columns exceed 2^24", (long long)n_cols);
+  return HINM_OK;
+}
+
 int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n_cols, int64_t ldx, const void* y,
                int64_t ldy) {
   if (p.tile_rows % 64 != 0) return fail(HINM_ESHAPE, "tile_rows=%d is not a multiple of 64", p.tile_rows);
   if (n_experts < 1 || n_experts > HINM_MAX_EXPERTS)
     return fail(HINM_ESHAPE, "n_experts=%d; 1 to %d are supported", n_experts, HINM_MAX_EXPERTS);
-  if (n_cols < 0) return fail(HINM_ESHAPE, "%lld columns", (long long)n_cols);
-  if (n_cols > (1 << 24)) return fail(HINM_ESHAPE, "%lld columns exceed 2^24", (long long)n_cols);
+  const int st = check_cols(n_cols);
+  if (st) return st;
   if (ldx < n_cols || ldy < n_cols)
     return fail(HINM_ESHAPE, "ldx=%lld and ldy=%lld must be >= the %lld columns", (long long)ldx, (long long)ldy,
                 (long long)n_cols);
@@ -1042,7 +1048,8 @@ extern "C" int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_
   st = check_args(*plan, n_experts, nullptr, 0, 0, nullptr, 0);
   if (st) return st;
   if (!bytes) return fail(HINM_EINVAL, "bytes is NULL");
-  if (n_cols < 0) return fail(HINM_ESHAPE, "%lld columns", (long long)n_cols);
+  st = check_cols(n_cols);
+  if (st) return st;
   const Workspace w = workspace_of(*plan, n_experts, n_cols, x_aligned != 0);
   *bytes = (size_t)w.bytes();
   return HINM_OK;

@@ -1,5 +1,7 @@
 """Each refusal of the mixture-of-experts calls for its own reason, told from the message (CPU only: tensors in host
 memory are refused last, so every other check is reached)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -76,3 +78,15 @@ def test_spmm_experts_of_another_routing(cols, four_bit):
     """X before dispatch (6 tokens) or in the order of another routing: its ranges would be cut silently."""
     with pytest.raises(ValueError, match=f"x has {cols} columns, the routing 40"):
         hinm.spmm_experts(_stack(four_bit=four_bit), torch.zeros(256, cols, dtype=BF16), _routing())
+
+
+@pytest.mark.parametrize("cols", [(1 << 24) + 1, 1 << 62])
+def test_workspace_queries_refuse_what_the_products_refuse(cols):
+    """More than 2^24 columns: the bytes of a copy of X would pass 63 bits."""
+    p = hinm.plan(128, 256, 64, 0.75, 0.55)
+    for aligned in (True, False):
+        assert hinm.spmm_experts_workspace_bytes(p, 4, 1 << 24, aligned) >= 0
+        with pytest.raises(hinm.HinmError, match="exceed 2"):
+            hinm.spmm_experts_workspace_bytes(p, 4, cols, aligned)
+        n = ctypes.c_size_t()
+        assert hinm.library().hinm_spmm_mx4_workspace_bytes(ctypes.byref(p.raw), cols, int(aligned), ctypes.byref(n)) == 2
