@@ -1051,6 +1051,7 @@ class HinmMx4:
     meta_24: torch.Tensor      # int16 bits of uint16
     idx_24: torch.Tensor
     n_experts: Optional[int] = None   # None: one weight
+    flags: int = 0                    # of the one weight it was made from, for dequantize
 
     @property
     def device(self) -> torch.device:
@@ -1067,13 +1068,16 @@ class HinmMx4:
         return st
 
     def dequantize(self):
-        """The bf16 packed weight (or Experts stack) of the same values, exact (hinm_mx4_dequantize)."""
+        """The bf16 packed weight (or Experts stack) of the same values, exact (hinm_mx4_dequantize).  One weight
+        keeps the flags of the weight it was made from: they describe the index lists, which are copied."""
         _on_gpu(self.device)
         lead = () if self.n_experts is None else (self.n_experts,)
         bufs = {k: _empty((*lead, *s), t, self.device) for k, (s, t) in _packed_shapes(self.plan).items()}
         out = (HinmPacked if self.n_experts is None else Experts)(self.plan, **bufs)
         _call(self.device, library().hinm_mx4_dequantize, ctypes.byref(self.struct()), self.n_experts or 1,
               ctypes.byref(out.struct()), _stream_ptr(self.device))
+        if self.n_experts is None:
+            out.flags = out.struct().flags = int(self.flags)
         return out
 
     def state_dict(self) -> dict:
@@ -1081,7 +1085,7 @@ class HinmMx4:
         p = self.plan
         return {"format": "hinm-mx4", "format_version": HINM_MX4_FORMAT_VERSION, "n_experts": self.n_experts or 0,
                 "cout": p.cout, "cin": p.cin, "tile_rows": p.tile_rows, "t_s": p.t_s, "v_s": p.v_s,
-                **{k: getattr(self, k) for k in _MX4_BUFFERS}}
+                "flags": int(self.flags), **{k: getattr(self, k) for k in _MX4_BUFFERS}}
 
     @classmethod
     def from_state_dict(cls, sd: dict, device=None) -> "HinmMx4":
@@ -1092,7 +1096,7 @@ class HinmMx4:
             raise ValueError("a stored 4-bit weight needs tile_rows % 64 == 0 and n_experts >= 0")
         lead = (n,) if n else ()
         want = {k: ((*lead, *s), t) for k, (s, t) in _mx4_shapes(p).items()}
-        return cls(p, **_checked_buffers(sd, want, device), n_experts=n or None)
+        return cls(p, **_checked_buffers(sd, want, device), n_experts=n or None, flags=int(sd.get("flags", 0)))
 
 
 def quantize_mx4(packed) -> HinmMx4:
@@ -1105,7 +1109,8 @@ def quantize_mx4(packed) -> HinmMx4:
     lead = () if n is None else (n,)
     dev = packed.device
     _on_gpu(dev)
-    out = HinmMx4(p, **{k: _empty((*lead, *s), t, dev) for k, (s, t) in _mx4_shapes(p).items()}, n_experts=n)
+    out = HinmMx4(p, **{k: _empty((*lead, *s), t, dev) for k, (s, t) in _mx4_shapes(p).items()}, n_experts=n,
+                  flags=packed.flags if n is None else 0)
     _call(dev, library().hinm_mx4_quantize, ctypes.byref(packed.struct()), n or 1, ctypes.byref(out.struct()),
           _stream_ptr(dev))
     return out
