@@ -112,3 +112,149 @@ def test_last_column_of_a_copied_x(cout, block, counts, mx4):
     for w, s, c in zip(ws, starts, counts):
         _check(y[:, s:s + c], w, x[:, s:s + c], cin - st.plan.z, f"columns from {s}")
     assert bool((y[:, :starts[0]] == 7).all())
+
+
+# --------------------------------------------------------------------------- blocks of 128 and 256 tokens
+
+def _block_of(plan, e, cols):
+    """Tokens a workgroup takes, read from the room for the sums of split items; None without such room."""
+    n = hinm.spmm_experts_workspace_bytes(plan, e, cols)
+    return (n - 65536) // (512 * 64 * 4) if n else None
+
+
+def _layout(counts, how):
+    """Starts and columns of ranges: "aligned" as the router makes them; "gaps" at odd columns with others' between
+    them; "end" one behind another from column 1, the last one ending with the buffer."""
+    if how == "end":
+        return [1 + sum(counts[:i]) for i in range(len(counts))], 1 + sum(counts)
+    starts, at = [], 0 if how == "aligned" else 1
+    for c in counts:
+        starts.append(at)
+        at += -(-c // 8) * 8 if how == "aligned" else c + 3
+    return starts, at
+
+
+def _matrices(cin, cout, cols, how, seed):
+    """X and Y: rows of whole 16 bytes, or (with "gaps") both an odd number of elements apart from an odd place."""
+    off, ld = (1, cols + 1 + cols % 2) if how == "gaps" else (0, -(-cols // 8) * 8)
+    x = torch.randn(off + cin * ld, generator=torch.Generator().manual_seed(seed)).bfloat16().to(DEV)
+    y = torch.full((off + cout * ld,), 7.0, dtype=torch.bfloat16, device=DEV)
+    return x[off:].view(cin, ld)[:, :cols], y, y[off:].view(cout, ld)[:, :cols]
+
+
+def _run(st, ws, counts, how, seed):
+    """Two calls against the 64-bit products; other columns' X is NaN, and their Y has to stay."""
+    starts, cols = _layout(counts, how)
+    p = st.plan
+    x, store, y = _matrices(p.cin, p.cout, cols, how, seed)
+    mine = torch.zeros(cols, dtype=torch.bool)
+    for s, c in zip(starts, counts):
+        mine[s:s + c] = True
+    x[:, ~mine.to(DEV)] = float("nan")
+    r = _routing(starts, counts, cols)
+    hinm.spmm_experts(st, x, r, out=y)
+    first = store.clone()
+    hinm.spmm_experts(st, x, r, out=y)
+    torch.cuda.synchronize()
+    assert torch.equal(first.view(torch.int16), store.view(torch.int16))   # the same bits on every call
+    for e, (s, c) in enumerate(zip(starts, counts)):
+        if c:
+            _check(y[:, s:s + c], ws[e], x[:, s:s + c], p.cin - p.z, f"expert {e}")
+    y[:, mine.to(DEV)] = 7.0
+    assert bool((store == 7).all())                                        # everything else as it was
+
+
+@pytest.mark.parametrize("how", ["aligned", "gaps", "end"])
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("cout,cin,t,v,block,counts", [
+    (4096, 516, 0.5, 0.25, 128, [130, 128, 129]),            # items enough: no split
+    (4096, 516, 0.75, 0.55, 128, [1, 385, 7]),
+    (4096, 260, 0.0, 0.0, 256, [257, 300, 511]),             # dense blocks alone
+    (4096, 516, 0.5, 0.25, 256, [700, 0, 255]),
+    (1536, 1028, 0.5, 0.25, 128, [0] * 5 + [461, 0, 300, 0, 0, 155] + [0] * 4 + [1]),   # 16 experts: split in two
+    (1024, 1028, 0.5, 0.25, 256, [555, 1, 777, 299]),        # split in two
+    (1024, 2052, 0.5, 0.25, 256, [0, 1509, 0, 1]),           # split in four
+    (512, 2052, 0.5, 0.25, 256, [5, 3001, 0, 129]),          # few tiles, split in four
+])
+def test_long_ranges(cout, cin, t, v, block, counts, mx4, how):
+    st, ws = _stack(cout, cin, t, v, len(counts), mx4, seed=cin)
+    cols = _layout(counts, how)[1]
+    if len(counts) == 16:                                    # 49 to 64 columns an expert on average
+        assert 16 * 48 < cols <= 16 * 64
+    print(f"[experts] {cout}x{cin} counts={counts} mx4={mx4} {how}", flush=True)
+    assert _block_of(st.plan, len(counts), cols) == block
+    _run(st, ws, counts, how, seed=cout + cols)
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+def test_long_ranges_of_large_weights(mx4):
+    """Two experts of 11008x4096 over 2047 tokens."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    pk = []
+    for _ in range(2):
+        w = torch.randn(11008, 4096, generator=g, device=DEV).bfloat16()
+        perm = torch.rand(172, 4096, generator=g, device=DEV).argsort(1).int()
+        pk.append(hinm.pack(w, w.float().abs(), 64, 0.75, 0.55, perm))
+    st = hinm.Experts.stack(pk)
+    if mx4:
+        st = hinm.quantize_mx4(st)
+        pk = [hinm.quantize_mx4(p).dequantize() for p in pk]
+    ws = [_weight(p) for p in pk]
+    for how in ("aligned", "end"):
+        print(f"[experts] 11008x4096, mx4={mx4} {how}", flush=True)
+        assert _block_of(st.plan, 2, _layout([1500, 547], how)[1]) == 256
+        _run(st, ws, [1500, 547], how, seed=5)
+
+
+@pytest.mark.parametrize("cout,cin,batch,room", [
+    (4096, 516, 1000, 0), (4096, 516, 999, 0),               # 128 tokens, 512 items
+    (2048, 1028, 1000, 128), (2048, 1028, 1001, 128),        # 128 tokens, split in two
+    (4096, 516, 1100, 0), (4096, 516, 1101, 0), (4096, 516, 1281, 0)])   # 256 tokens
+@pytest.mark.parametrize("aligned", [True, False])
+def test_long_four_bit_products(cout, cin, batch, room, aligned):
+    pk = _pack(cout, cin, 0.5, 0.25, seed=batch)
+    q = hinm.quantize_mx4(pk)
+    w = _weight(q.dequantize())
+    split = 65536 + 512 * 64 * 4 * room if room else 0
+    ld = -(-batch // 8) * 8 if aligned else batch + 1 + batch % 2
+    x = torch.randn(cin, ld, generator=torch.Generator().manual_seed(batch)).bfloat16().to(DEV)[:, ld - batch if not aligned else 0:]
+    x = x[:, :batch]
+    print(f"[mx4 spmm] {cout}x{cin} batch={batch} aligned={aligned}", flush=True)
+    assert hinm.spmm_experts_workspace_bytes(q.plan, 1, batch) == split
+    copy = -(-cin * -(-batch // 8) * 8 * 2 // 256) * 256     # more than 32 tokens a workgroup: unaligned rows are copied
+    assert hinm.spmm_experts_workspace_bytes(q.plan, 1, batch, x_aligned=False) == max(split, 65536) + copy
+    y = hinm.spmm(q, x)
+    again = hinm.spmm(q, x)
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    _check(y, w, x, cin - q.plan.z, f"batch {batch}")
+
+
+# --------------------------------------------------------------------------- blocks of 16 and 32 tokens
+
+@pytest.mark.parametrize("cin", [992, 1024, 1056, 2016, 2048, 2080])
+@pytest.mark.parametrize("batch", [1, 16, 17, 32, 33])
+def test_splits_of_short_products(cin, batch):
+    """31, 32, 33, 63, 64 and 65 K-blocks of dense values, at which the number of splits steps, and the token counts
+    around blocks of 16 and 32."""
+    pk = _pack(128, cin, 0.0, 0.0, seed=cin)
+    assert pk.plan.n_dense_pad // 32 == cin // 32
+    q = hinm.quantize_mx4(pk)
+    x = torch.randn(cin, batch, generator=torch.Generator().manual_seed(batch)).bfloat16().to(DEV)
+    print(f"[mx4 spmm] 128x{cin} batch={batch}", flush=True)
+    assert _block_of(q.plan, 1, batch) == (16 if batch <= 16 else 32)
+    _check(hinm.spmm(q, x), _weight(q.dequantize()), x, cin, f"batch {batch}")
+    st = hinm.Experts.stack([pk, pk])
+    counts = [batch, 3]
+    _run(st, [_weight(pk)] * 2, counts, "gaps", seed=cin + batch)
+
+
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("counts,block", [([16, 17, 3], 16), ([20, 20, 20], 16), ([21, 20, 23], 32), ([48, 32, 33], 32),
+                                          ([1, 0, 140], 32)])
+def test_short_ranges(counts, block, mx4):
+    st, ws = _stack(192, 516, 0.75, 0.55, 3, mx4, seed=9)
+    assert _block_of(st.plan, 3, sum(counts)) == block
+    for how in ("aligned", "gaps", "end"):
+        print(f"[experts] counts={counts} mx4={mx4} {how}", flush=True)
+        _run(st, ws, counts, how, seed=sum(counts))
