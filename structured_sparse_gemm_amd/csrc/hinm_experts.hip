@@ -34,9 +34,9 @@ struct ExpArgs {
   uint16_t* y;
   int64_t ldx, ldy;
   int x_end;                         // 1: the buffer of X ends with row cin - 1's last column (0: its rows are padded)
+  int may_split;                     // the workspace has room for arrival counters and partial sums
   const int32_t *starts, *counts;    // NULL: one range, all columns
   int n_experts, n_cols;
-  int may_split;                     // the workspace has room for arrival counters and partial sums
   int cin, cout, rows, n_tiles, nkb_d, nkb_s;
 };
 
