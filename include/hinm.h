@@ -597,16 +597,17 @@ int hinm_combine(const void* ys_bf16, int64_t channels, int64_t n_cols, int64_t 
  * them (hinm_pack fills one expert when its output pointers are offset so).
  * X (device) bf16 [cin][ldx], ldx >= n_cols; Y (device) bf16 [cout][ldy], ldy
  * >= n_cols.  starts, counts (device) int32 [n_experts] are read on the
- * device, so a routing needs no host synchronisation; ranges are clipped to
- * 0 .. n_cols, and should not overlap.  Y columns outside every range are left
- * as they were.  Requires tile_rows % 64 == 0 and each expert's buffers below
- * 2^31 bytes (HINM_ESHAPE).  X rows that are 16-byte aligned (X aligned, ldx %
- * 8 == 0) and ranges that start at multiples of 8 (align 8 in hinm_route) run
- * fastest.  Rounding, determinism, workspace (its first 64 KiB zero-filled
- * before its first use) and errors as hinm_spmm; the options of
- * hinm_set_option do not apply.  The workspace query's x_aligned says whether
- * X rows are 16-byte aligned; with unaligned rows and many tokens the
- * workspace also holds a copy of X whose rows are. */
+ * device, so a routing needs no host synchronisation; ranges are clipped to 0
+ * .. n_cols, and should not overlap.  Y columns outside every range are left
+ * as they were; Y must not overlap X.  n_cols is at most 2^24.  Requires
+ * tile_rows % 64 == 0 and each expert's buffers below 2^31 bytes
+ * (HINM_ESHAPE).  X rows that are 16-byte aligned (X aligned, ldx % 8 == 0)
+ * and ranges that start at multiples of 8 (align 8 in hinm_route) run fastest.
+ * Rounding, determinism, workspace (its first 64 KiB zero-filled before its
+ * first use) and errors as hinm_spmm; the options of hinm_set_option do not
+ * apply.  The workspace query's x_aligned says whether X rows are 16-byte
+ * aligned; with unaligned rows and many tokens the workspace also holds a copy
+ * of X whose rows are. */
 int hinm_spmm_experts_workspace_bytes(const hinm_plan_t* plan, int32_t n_experts, int64_t n_cols, int32_t x_aligned,
                                       size_t* bytes);
 int hinm_spmm_experts(const hinm_packed_t* stack, int32_t n_experts, const void* x_bf16, int64_t n_cols, int64_t ldx,

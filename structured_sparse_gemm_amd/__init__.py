@@ -1155,7 +1155,8 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     """Every expert's product over its own columns (hinm_spmm_experts, or hinm_spmm_experts_mx4 for a quantised
     stack): x bf16 [cin, columns] in the routing's order, as many as it has -> bf16 [cout, columns].
 
-    Columns that belong to no expert are left as they were in ``out`` (unspecified in a new one).  The ranges are
+    Columns that belong to no expert are left as they were in ``out`` (unspecified in a new one), which must not
+    overlap x.  The ranges are
     read on the device: no host synchronisation.  Asynchronous on the current stream; workspace as in spmm, but
     while a graph is captured each call has its own."""
     mx4 = isinstance(experts, HinmMx4)

@@ -283,9 +283,10 @@ __global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(Exp
   const int items = plan_blocks(a, NT, pre) * n_rb;
   // A split costs its row blocks a round trip through the workspace (about 2.5
   // us), so one is made only where compute units would have no item, and for
-  // at least four K-blocks a wave (4-bit, 1 token: 4096x11008 10.4
-  // us with four splits of its 64 row blocks, 11.2 with eight; 11008x4096's
-  // 172 row blocks 8.3 us whole, 10.6 in two).
+  // at least four K-blocks a wave (4-bit, 1 token: 4096x11008 9.5 us with
+  // four splits of its 64 row blocks and slower with eight, 11.2 against 10.4
+  // before the join had several shares in flight; 11008x4096's 172 row blocks
+  // 8.3 us whole, 10.6 in two).
   int splits = 1;
   while (a.may_split && items * splits * 2 <= kCus && nblk >= 32 * splits) splits *= 2;
 
@@ -499,7 +500,7 @@ __global__ __launch_bounds__(256, decode_wgs(NT)) void experts_decode_kernel(Exp
 // blocks ahead), 4-bit ones becoming bf16 on the way, once a workgroup.  The
 // regions' loops are separate, dense on 32x32x16 MFMA, 2:4 on 32x32x32 SMFMAC.
 //
-// 8 experts of 4096x11008, 4094 columns, bf16: 258 us, 3.9 GB of lines from L2
+// 8 experts of 4096x11008, 4094 columns, bf16: 258-279 us, 3.9 GB of lines from L2
 // with 64 of them in flight a compute unit at a mean 330 cycles, which is all
 // a unit holds.  One 4-bit weight of 11008x4096, 2047 tokens: 123 us with the
 // copy of X (10); 17 lines in flight, the step's barrier and the expansion
@@ -892,15 +893,23 @@ int check_bufs(const Buf* b, int n) {
 // Tokens a workgroup takes, from the columns an expert has on average (the
 // counts themselves are on the device): 16 or 32 in the decode kernel, 128 or
 // 256 in the prefill kernel.  The decode kernel is the better one for few
-// columns, and for more of them while its items still run at once, three on a
-// compute unit (us, decode 32 against prefill 128, 4-bit: 11008x4096 at 128
-// tokens, 688 items, 18 against 23; at 200, 1204 items, 30 against 28; 8
-// experts of 4096x4096, 39 columns on average, 21 against 32; 55, 30 against
-// 32).  Of the prefill's blocks, 256 halves the bytes of packed values, but an
-// expert a little above 256 then takes two (8 experts of 4096x4096, 128
-// against 256: 64 columns 48 against 42, 135 46 against 62, 199 69 against
-// 64; one weight of 11008x4096: 200 tokens 28 against 32, 400 44 against 40;
-// of 2048x2048: 2048 tokens 19 against 29).
+// columns, and for more of them while it has no more than 768 items, three a
+// compute unit of the four it runs at once (us, decode 32 against prefill 128,
+// 4-bit: 11008x4096 at 128 tokens, 688 items, 18 against 23; at 200, 1204
+// items, 30 against 28; 8 experts of 4096x4096, 39 columns on average, 21
+// against 32; 55, 30 against 32).  Of the prefill's blocks, 256 halves the
+// bytes of packed values, but costs an expert with few columns the whole
+// block, and one a little above 256 two.  How many experts that is depends on
+// the counts, which the average does not tell, so the steps for several
+// experts are those of one weight and moderate skew, 8 experts of 4096x4096
+// at top 2 (128 against 256, bf16, three routings each: 65 columns 30 against
+// 42, 71 48 against 41, 87 46 against 41, 142 52 against 62, 172 53 against
+// 41-64, 206 54-72 against 65, 237 72 against 65).  16 experts of 2048x4096
+// follow them less well (71 49 against 39, 107 49 against 63) and 8 of
+// 11008x4096 not below 172 columns, where 128 is the better one throughout (65
+// 75-90 against 102, 107 93-115 against 107-122, 142 112-121 against 125).
+// One weight of 11008x4096: 200 tokens 28 against 32, 400 44 against 40; of
+// 2048x2048: 2048 tokens 19 against 29.
 int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
   if (avg <= (n_experts == 1 ? 16 : 20)) return 16;
