@@ -26,7 +26,9 @@ HINM_ABI_VERSION = 2
 HINM_PACKED_WINDOWED = 1     # flags bit: block-diagonal perms (blocks of 64), see include/hinm.h
 HINM_FORMAT_VERSION = 1       # packed-buffer layout version (include/hinm.h)
 HINM_MX4_FORMAT_VERSION = 1   # layout version of 4-bit microscaled values (include/hinm.h)
+HINM_FP8_FORMAT_VERSION = 1   # layout version of 8-bit values (include/hinm.h)
 HINM_BF16, HINM_FP32 = 0, 1   # element types of the router's logits
+HINM_MOE_MAX_TOKENS = 32      # most tokens of moe_layer
 HINM_NOALLOC_SCRATCH_BYTES = 65536 + (32 << 20)   # hinm_spmm_noalloc's device array (include/hinm.h)
 STATUS = {0: "HINM_OK", 1: "HINM_EINVAL", 2: "HINM_ESHAPE", 3: "HINM_EPERM", 4: "HINM_EIMPORTANCE",
           5: "HINM_EALIGN", 6: "HINM_EWORKSPACE", 7: "HINM_EHIP", 8: "HINM_EDEVICE"}
@@ -41,7 +43,9 @@ EXPORTS = ("hinm_abi_version", "hinm_plan", "hinm_pack_workspace_bytes", "hinm_p
            "hinm_spmm_group", "hinm_route_columns", "hinm_route_workspace_bytes", "hinm_route", "hinm_dispatch",
            "hinm_combine", "hinm_spmm_experts_workspace_bytes", "hinm_spmm_experts", "hinm_mx4_quantize",
            "hinm_mx4_dequantize", "hinm_spmm_mx4_workspace_bytes", "hinm_spmm_mx4", "hinm_spmm_experts_mx4",
-           "hinm_status_str", "hinm_last_error")
+           "hinm_fp8_quantize", "hinm_fp8_dequantize", "hinm_spmm_fp8_workspace_bytes", "hinm_spmm_fp8",
+           "hinm_spmm_experts_fp8_workspace_bytes", "hinm_spmm_experts_fp8", "hinm_moe_layer_workspace_bytes",
+           "hinm_moe_layer", "hinm_status_str", "hinm_last_error")
 
 # Launch-shape options (hinm_set_option): name -> HINM_OPT_* key.
 OPTIONS = {"decode_path": 1, "decode_wgs": 2, "prefill_nt": 3, "prefill_splits": 4, "prefill_path": 5,
@@ -77,6 +81,10 @@ class Mx4T(ctypes.Structure):
     _fields_ = [("plan", PlanT), ("val_dense", ctypes.c_void_p), ("scale_dense", ctypes.c_void_p),
                 ("idx_dense", ctypes.c_void_p), ("val_24", ctypes.c_void_p), ("scale_24", ctypes.c_void_p),
                 ("meta_24", ctypes.c_void_p), ("idx_24", ctypes.c_void_p)]
+
+
+class Fp8T(Mx4T):
+    """hinm_fp8_t: the same members as hinm_mx4_t."""
 
 
 class TPlanT(ctypes.Structure):
@@ -152,6 +160,16 @@ def library() -> ctypes.CDLL:
             "hinm_mx4_dequantize": ([ctypes.POINTER(Mx4T), I32, ctypes.POINTER(PackedT), VP], ctypes.c_int),
             "hinm_spmm_mx4_workspace_bytes": ([P, I64, I32, ctypes.POINTER(S)], ctypes.c_int),
             "hinm_spmm_mx4": ([ctypes.POINTER(Mx4T), VP, I64, I64, VP, I64, VP, S, VP], ctypes.c_int),
+            "hinm_fp8_quantize": ([ctypes.POINTER(PackedT), I32, ctypes.POINTER(Fp8T), VP], ctypes.c_int),
+            "hinm_fp8_dequantize": ([ctypes.POINTER(Fp8T), I32, ctypes.POINTER(PackedT), VP], ctypes.c_int),
+            "hinm_spmm_fp8_workspace_bytes": ([P, I64, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_spmm_fp8": ([ctypes.POINTER(Fp8T), VP, I64, I64, VP, I64, VP, S, VP], ctypes.c_int),
+            "hinm_spmm_experts_fp8_workspace_bytes": ([P, I32, I64, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_spmm_experts_fp8": ([ctypes.POINTER(Fp8T), I32, VP, I64, I64, VP, VP, VP, I64, VP, S, VP],
+                                      ctypes.c_int),
+            "hinm_moe_layer_workspace_bytes": ([P, P, I32, I64, I32, ctypes.POINTER(S)], ctypes.c_int),
+            "hinm_moe_layer": ([VP, I32, I64, VP, I64, I64, I32, I32, I32, I32, VP, VP, VP, VP, I64, VP, S, VP],
+                               ctypes.c_int),
             "hinm_get_option": ([ctypes.c_int, ctypes.POINTER(I64)], ctypes.c_int),
             "hinm_status_str": ([ctypes.c_int], ctypes.c_char_p),
             "hinm_last_error": ([], ctypes.c_char_p),
@@ -485,10 +503,12 @@ def _one_weight(packed, what: str) -> None:
     """Refuses what is not a single uniform bf16 weight: the C calls read its buffers as such."""
     if isinstance(packed, HinmPacked):
         return
-    if isinstance(packed, Experts) or (isinstance(packed, HinmMx4) and packed.n_experts is not None):
+    if isinstance(packed, Experts) or (isinstance(packed, (HinmMx4, HinmFp8)) and packed.n_experts is not None):
         raise ValueError(f"{what} takes one weight; a stack of experts is multiplied by spmm_experts")
     if isinstance(packed, HinmMx4):
         raise ValueError(f"{what} takes bf16 values; 4-bit weights are multiplied one at a time by spmm")
+    if isinstance(packed, HinmFp8):
+        raise ValueError(f"{what} takes bf16 values; 8-bit weights are multiplied one at a time by spmm")
     if isinstance(packed, HinmTPacked):
         raise ValueError(f"{what} takes uniform packed weights (pack, not pack_tiles)")
     raise ValueError(f"{what} takes a packed weight, not a {type(packed).__name__}")
@@ -564,9 +584,13 @@ def spmm(packed: HinmPacked, x: torch.Tensor, out: Optional[torch.Tensor] = None
     Asynchronous on the current stream.  ``workspace`` (uint8, device, zero-filled before its first use) may
     be given; otherwise each stream has its own default workspace, so products on different streams may
     overlap.  The per-call host work is kept to argument checks and one C call, so that small products are
-    not bound by Python.  A weight with 4-bit microscaled values (quantize_mx4) runs hinm_spmm_mx4; it takes no
-    ``out_rows``.
+    not bound by Python.  A weight with 4-bit microscaled values (quantize_mx4) runs hinm_spmm_mx4, one with 8-bit
+    values (quantize_fp8) hinm_spmm_fp8, which rounds x to 8 bits token by token; they take no ``out_rows``.
     """
+    if isinstance(packed, HinmFp8):
+        if out_rows is not None:
+            raise ValueError("out_rows is not supported with 8-bit values")
+        return _spmm_fp8(packed, x, out, workspace)
     if isinstance(packed, HinmMx4):
         if out_rows is not None:
             raise ValueError("out_rows is not supported with 4-bit values")
@@ -1143,6 +1167,145 @@ def _spmm_mx4(packed: HinmMx4, x: torch.Tensor, out, workspace) -> torch.Tensor:
     return out
 
 
+def _fp8_shapes(p: Plan) -> dict:
+    T, R, D, S = p.n_tiles, p.tile_rows, p.n_dense_pad // 32, p.n_24_pad // 64
+    return {"val_dense": ((T, D, R, 32), torch.float8_e4m3fn), "scale_dense": ((T, -(-D // 4), R), torch.uint8),
+            "idx_dense": ((T, D * 32), torch.int32), "val_24": ((T, S, R, 32), torch.float8_e4m3fn),
+            "scale_24": ((T, -(-S // 4), R), torch.uint8), "meta_24": ((T, S, R), torch.int64),
+            "idx_24": ((T, S * 64), torch.int32)}
+
+
+@dataclasses.dataclass
+class HinmFp8:
+    """A packed weight, or a stack of them, with 8-bit values (hinm_fp8_t; buffers of a stack have a leading expert
+    axis).  Made by quantize_fp8; the tensors must not be replaced afterwards."""
+
+    plan: Plan
+    val_dense: torch.Tensor    # float8_e4m3fn
+    scale_dense: torch.Tensor  # uint8, 2^(e - 127)
+    idx_dense: torch.Tensor    # int32
+    val_24: torch.Tensor
+    scale_24: torch.Tensor
+    meta_24: torch.Tensor      # int64 bits of uint64
+    idx_24: torch.Tensor
+    n_experts: Optional[int] = None   # None: one weight
+    flags: int = 0                    # of the one weight it was made from, for dequantize
+
+    @property
+    def device(self) -> torch.device:
+        return self.idx_24.device
+
+    def nbytes(self) -> int:
+        return sum(getattr(self, k).numel() * getattr(self, k).element_size() for k in _MX4_BUFFERS)
+
+    def struct(self) -> Fp8T:
+        st = self.__dict__.get("_struct")
+        if st is None:
+            st = self.__dict__["_struct"] = Fp8T(self.plan.raw, *[_ptr(getattr(self, k)) for k in _MX4_BUFFERS])
+            self.__dict__["_need"] = {}
+        return st
+
+    def dequantize(self):
+        """The bf16 packed weight (or Experts stack) of the same values, exact (hinm_fp8_dequantize).  One weight
+        keeps the flags of the weight it was made from: they describe the index lists, which are copied."""
+        _on_gpu(self.device)
+        lead = () if self.n_experts is None else (self.n_experts,)
+        bufs = {k: _empty((*lead, *s), t, self.device) for k, (s, t) in _packed_shapes(self.plan).items()}
+        out = (HinmPacked if self.n_experts is None else Experts)(self.plan, **bufs)
+        _call(self.device, library().hinm_fp8_dequantize, ctypes.byref(self.struct()), self.n_experts or 1,
+              ctypes.byref(out.struct()), _stream_ptr(self.device))
+        if self.n_experts is None:
+            out.flags = out.struct().flags = int(self.flags)
+        return out
+
+    def state_dict(self) -> dict:
+        """As HinmPacked.state_dict; n_experts 0 marks a single weight."""
+        p = self.plan
+        return {"format": "hinm-fp8", "format_version": HINM_FP8_FORMAT_VERSION, "n_experts": self.n_experts or 0,
+                "cout": p.cout, "cin": p.cin, "tile_rows": p.tile_rows, "t_s": p.t_s, "v_s": p.v_s,
+                "flags": int(self.flags), **{k: getattr(self, k) for k in _MX4_BUFFERS}}
+
+    @classmethod
+    def from_state_dict(cls, sd: dict, device=None) -> "HinmFp8":
+        _check_format(sd, "hinm-fp8", HINM_FP8_FORMAT_VERSION)
+        p = plan(int(sd["cout"]), int(sd["cin"]), int(sd["tile_rows"]), float(sd["t_s"]), float(sd["v_s"]))
+        n = int(sd["n_experts"])
+        if n < 0 or p.tile_rows % 64:
+            raise ValueError("a stored 8-bit weight needs tile_rows % 64 == 0 and n_experts >= 0")
+        lead = (n,) if n else ()
+        want = {k: ((*lead, *s), t) for k, (s, t) in _fp8_shapes(p).items()}
+        return cls(p, **_checked_buffers(sd, want, device), n_experts=n or None, flags=int(sd.get("flags", 0)))
+
+
+def quantize_fp8(packed) -> HinmFp8:
+    """Rounds the values of a packed weight or an Experts stack to 8 bits (hinm_fp8_quantize): E4M3 codes, one
+    power-of-two scale for each block of 128 kept values of a row.  Needs tile_rows a multiple of 64.  Asynchronous on
+    the current stream."""
+    if not isinstance(packed, (HinmPacked, Experts)):
+        raise ValueError("quantize_fp8 takes a HinmPacked weight or an Experts stack")
+    p, n = packed.plan, packed.n_experts if isinstance(packed, Experts) else None
+    lead = () if n is None else (n,)
+    dev = packed.device
+    _on_gpu(dev)
+    out = HinmFp8(p, **{k: _empty((*lead, *s), t, dev) for k, (s, t) in _fp8_shapes(p).items()}, n_experts=n,
+                  flags=packed.flags if n is None else 0)
+    _call(dev, library().hinm_fp8_quantize, ctypes.byref(packed.struct()), n or 1, ctypes.byref(out.struct()),
+          _stream_ptr(dev))
+    return out
+
+
+_WS_KEPT = 64 << 20        # a stream keeps workspaces up to this size between calls
+
+
+def _sized_workspace(dev: torch.device, stream: int, need: int) -> Optional[torch.Tensor]:
+    """The default workspace of an 8-bit product or a mixture-of-experts layer: the stream's own, grown in powers of
+    two.  A new one where it is large (rounded activations of a long prompt), and while a graph is captured, out of
+    the graph's memory, so that graphs captured on one stream and replayed on several never share one; its arrival
+    counters are cleared on the stream (by a node of the graph)."""
+    if need == 0:
+        return None
+    if need > _WS_KEPT or torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws[:65536].zero_()
+        return ws
+    return _workspace(dev, stream, 1 << (need - 1).bit_length())
+
+
+def _given_workspace(workspace: torch.Tensor, dev: torch.device) -> torch.Tensor:
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace
+
+
+def _fp8_need(w: HinmFp8, cols: int) -> int:
+    needs = w.__dict__["_need"]
+    need = needs.get(cols)
+    if need is None:
+        n = ctypes.c_size_t()
+        _check(library().hinm_spmm_experts_fp8_workspace_bytes(ctypes.byref(w.plan.raw), w.n_experts or 1, cols,
+                                                               ctypes.byref(n)))
+        need = needs[cols] = n.value
+    return need
+
+
+def _spmm_fp8(packed: HinmFp8, x: torch.Tensor, out, workspace) -> torch.Tensor:
+    if packed.n_experts is not None:
+        raise ValueError("spmm takes one weight; multiply a stack with spmm_experts")
+    p, dev = packed.plan, packed.idx_24.device
+    ldx = _matrix(x, p.cin, None, dev, "x")
+    _on_gpu(dev)
+    batch = x.shape[1]
+    if out is None:
+        out = torch.empty((p.cout, batch), dtype=torch.bfloat16, device=dev)
+    ldy = _matrix(out, p.cout, batch, dev, "out")
+    st, lib, stream = packed.struct(), library(), _stream_ptr(dev)
+    need = _fp8_need(packed, batch)
+    ws = _sized_workspace(dev, stream, need) if workspace is None else _given_workspace(workspace, dev)
+    _call(dev, lib.hinm_spmm_fp8, ctypes.byref(st), x.data_ptr(), batch, ldx, out.data_ptr(), ldy,
+          ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
+    return out
+
+
 def spmm_experts_workspace_bytes(p: Plan, n_experts: int, n_cols: int, x_aligned: bool = True) -> int:
     n = ctypes.c_size_t()
     _check(library().hinm_spmm_experts_workspace_bytes(ctypes.byref(p.raw), n_experts, n_cols, int(x_aligned),
@@ -1152,15 +1315,15 @@ def spmm_experts_workspace_bytes(p: Plan, n_experts: int, n_cols: int, x_aligned
 
 def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Every expert's product over its own columns (hinm_spmm_experts, or hinm_spmm_experts_mx4 for a quantised
-    stack): x bf16 [cin, columns] in the routing's order, as many as it has -> bf16 [cout, columns].
+    """Every expert's product over its own columns (hinm_spmm_experts, hinm_spmm_experts_mx4 or hinm_spmm_experts_fp8
+    by the stack's values): x bf16 [cin, columns] in the routing's order, as many as it has -> bf16 [cout, columns].
 
     Columns that belong to no expert are left as they were in ``out`` (unspecified in a new one), which must not
     overlap x.  The ranges are
     read on the device: no host synchronisation.  Asynchronous on the current stream; workspace as in spmm, but
     while a graph is captured each call has its own."""
-    mx4 = isinstance(experts, HinmMx4)
-    if not (mx4 and experts.n_experts is not None) and not isinstance(experts, Experts):
+    mx4, fp8 = isinstance(experts, HinmMx4), isinstance(experts, HinmFp8)
+    if not ((mx4 or fp8) and experts.n_experts is not None) and not isinstance(experts, Experts):
         raise ValueError("spmm_experts takes an Experts stack or a quantised one")
     p, dev, e = experts.plan, experts.idx_24.device, experts.n_experts
     ldx = _matrix(x, p.cin, None, dev, "x")
@@ -1175,6 +1338,14 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     if out is None:
         out = torch.empty((p.cout, cols), dtype=torch.bfloat16, device=dev)
     ldy = _matrix(out, p.cout, cols, dev, "out")
+    if fp8:
+        st, stream = experts.struct(), _stream_ptr(dev)
+        need = _fp8_need(experts, cols)
+        ws = _sized_workspace(dev, stream, need) if workspace is None else _given_workspace(workspace, dev)
+        _call(dev, library().hinm_spmm_experts_fp8, ctypes.byref(st), e, x.data_ptr(), cols, ldx,
+              routing.starts.data_ptr(), routing.counts.data_ptr(), out.data_ptr(), ldy,
+              ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
+        return out
     needs = experts.__dict__.setdefault("_expert_need", {})
     key = (cols, ldx % 8 == 0 and x.data_ptr() % 16 == 0)
     need = needs.get(key)
@@ -1193,7 +1364,64 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     return out
 
 
-__all__ = ["HinmError", "HinmPacked", "Plan", "plan", "pack", "spmm", "spmm_noalloc", "Group", "spmm_group", "set_option", "get_option", "options",
+_VALUES = {"Experts": 0, "HinmMx4": 1, "HinmFp8": 2}   # HINM_VALUES_*
+
+
+@functools.lru_cache(maxsize=1024)
+def _moe_need(up: tuple, down: tuple, n_experts: int, n_tokens: int, top_k: int) -> int:
+    n = ctypes.c_size_t()
+    _check(library().hinm_moe_layer_workspace_bytes(ctypes.byref(plan(*up).raw), ctypes.byref(plan(*down).raw),
+                                                    n_experts, n_tokens, top_k, ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_workspace_bytes(up: Plan, down: Plan, n_experts: int, n_tokens: int, top_k: int) -> int:
+    """Bytes of moe_layer's workspace (hinm_moe_layer_workspace_bytes, host only)."""
+    return _moe_need(*[(p.cout, p.cin, p.tile_rows, p.t_s, p.v_s) for p in (up, down)], n_experts, n_tokens, top_k)
+
+
+def moe_layer(x: torch.Tensor, logits: torch.Tensor, gate, up, down, top_k: int, renormalize: bool = True,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole gated mixture-of-experts layer for up to 32 tokens in two kernels (hinm_moe_layer):
+    y[:, n] = sum over the token's top_k experts of w * down(silu(gate x_n) * up x_n).
+
+    x bf16 [hidden, tokens], logits bf16 or fp32 [experts, tokens] (as route takes them), gate and up stacks of
+    [inter x hidden] weights, down of [hidden x inter]: Experts, or all three quantize_mx4 or quantize_fp8 stacks.
+    Returns (or fills) bf16 [hidden, tokens].  Asynchronous on the current stream; workspace as in spmm_experts.  More
+    tokens go through route, dispatch, spmm_experts and combine."""
+    kind = type(gate).__name__
+    if kind not in _VALUES or type(up) is not type(gate) or type(down) is not type(gate) or any(
+            w.n_experts is None for w in (gate, up, down)):
+        raise ValueError("gate, up and down must be stacks of experts of one kind (Experts, quantize_mx4's or "
+                         "quantize_fp8's)")
+    pg, pu, pd, dev, e = gate.plan, up.plan, down.plan, gate.idx_24.device, gate.n_experts
+    if up.n_experts != e or down.n_experts != e or up.device != dev or down.device != dev:
+        raise ValueError("gate, up and down must have equal numbers of experts and be on one device")
+    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or logits.shape[0] != e or logits.device != dev:
+        raise ValueError(f"logits must be bf16 or fp32 [{e}, tokens] on {dev}")
+    n = logits.shape[1]
+    ldl = logits.stride(0)
+    if (n > 1 and logits.stride(1) != 1) or (e > 1 and ldl < n):
+        raise ValueError("logits must have unit column stride and rows that do not overlap")
+    ldx = _matrix(x, pu.cin, n, dev, "x")
+    _on_gpu(dev)
+    if out is None:
+        out = torch.empty((pd.cout, n), dtype=torch.bfloat16, device=dev)
+    ldy = _matrix(out, pd.cout, n, dev, "out")
+    lib, stream = library(), _stream_ptr(dev)
+    needs = gate.__dict__.setdefault("_moe_need", {})
+    need = needs.get((n, top_k))
+    if need is None:
+        need = needs[(n, top_k)] = moe_layer_workspace_bytes(pu, pd, e, n, top_k)
+    ws = _sized_workspace(dev, stream, need) if workspace is None else _given_workspace(workspace, dev)
+    _call(dev, lib.hinm_moe_layer, logits.data_ptr(), HINM_BF16 if logits.dtype == torch.bfloat16 else HINM_FP32,
+          max(ldl, n), x.data_ptr(), n, ldx, e, top_k, int(renormalize), _VALUES[kind], ctypes.byref(gate.struct()),
+          ctypes.byref(up.struct()), ctypes.byref(down.struct()), out.data_ptr(), ldy,
+          ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
+    return out
+
+
+__all__ = ["HinmFp8", "quantize_fp8", "moe_layer", "moe_layer_workspace_bytes", "HINM_MOE_MAX_TOKENS", "HinmError", "HinmPacked", "Plan", "plan", "pack", "spmm", "spmm_noalloc", "Group", "spmm_group", "set_option", "get_option", "options",
            "OPTIONS", "translate_indices", "boundary_search", "plan_tiles", "pack_tiles", "boundary_search_tiles",
            "HinmTPacked", "TilePlan", "spmm_tiles_workspace_bytes", "alloc_packed",
            "pack_workspace_bytes",

@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhinm.so")
 SOURCES = ("hinm_plan.cpp", "hinm_pack.hip", "hinm_spmm.hip", "hinm_gyro.hip", "hinm_route.hip", "hinm_mx4.hip",
-           "hinm_experts.hip")
+           "hinm_experts.hip", "hinm_fp8.hip", "hinm_fp8_spmm.hip", "hinm_moe.hip")
 ARCH = "gfx950"
 # Packed-fp32 VALU forms are kept off for every kernel of this library.  MFMA
 # accumulators stay in ordinary VGPRs: with one wave per SIMD the compiler

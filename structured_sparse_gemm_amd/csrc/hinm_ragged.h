@@ -31,9 +31,11 @@ __device__ inline void range_of(const Args& a, int e, int& lo, int& hi) {
   hi = s < 0 || c <= 0 ? lo : lo + min(c, a.n_cols - lo);
 }
 
-// Blocks of nt columns before every expert, and their number in all.
+// Blocks of nt columns before every expert, and their number in all; an
+// expert's first block starts at its first column rounded down to a multiple
+// of `align`.
 template <class Args>
-__device__ inline int plan_blocks(const Args& a, int nt, int* pre) {
+__device__ inline int plan_blocks(const Args& a, int nt, int* pre, int align = 1) {
   if (!a.starts) return (a.n_cols + nt - 1) / nt;
   if (threadIdx.x < 64) {
     int carry = 0;
@@ -41,7 +43,7 @@ __device__ inline int plan_blocks(const Args& a, int nt, int* pre) {
       const int e = e0 + (int)threadIdx.x;
       int lo = 0, hi = 0;
       if (e < a.n_experts) range_of(a, e, lo, hi);
-      const int nb = (hi - lo + nt - 1) / nt;
+      const int nb = hi > lo ? (hi - (lo & -align) + nt - 1) / nt : 0;
       int sum = nb;
       for (int d = 1; d < 64; d *= 2) {
         const int v = __shfl_up(sum, d);
