@@ -761,8 +761,8 @@ int hinm_spmm_experts_fp8(const hinm_fp8_t* stack, int32_t n_experts, const void
  *     h_j = silu(G_e x_n) * (U_e x_n),   silu(g) = g / (1 + exp(-g)),
  *     Y[:, n] = sum over j of w_j * (D_e h_j).
  * G and U (gate, up) are [inter x hidden], D (down) is [hidden x inter].
- * Products, the activation and the weighted sum are in fp32; h is rounded to
- * bf16 (it is a matrix operand) and Y to bf16 once.  The experts' terms are
+ * Products, the activation and the weighted sum are in fp32; h is held as the
+ * sum of two bf16 values (16 bits of mantissa) and Y is rounded to bf16 once.  The experts' terms are
  * added in an order that depends on the sizes and the routing alone: the same
  * inputs give the same bits.  Choosing experts and their terms is per token: a
  * NaN in one token, or in an expert that a token did not choose, stays out of

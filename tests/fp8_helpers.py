@@ -84,8 +84,8 @@ def moe_layer(logits, x, gate, up, down, top_k: int, renormalize: bool, kept):
     down).  Returns the output and a bound of the kernel's error.
 
     Bound: a sum of k products is off by (k + 64) 2^-23 of the sum of magnitudes (as moe_helpers.product_bound); silu's
-    slope is at most 1.1, its exponential, addition and division add less than 2^-20 of the result; h is rounded to
-    bf16 (2^-8); a router weight is off by (2 |l - m| + 10) 2^-24; one rounding to bf16 of the output."""
+    slope is at most 1.1, its exponential, addition and division add less than 2^-20 of the result; h is the
+    sum of two bf16 values (2^-16: the second is off by half a step, 2^-8, of at most 2^-8 of h); a router weight is off by (2 |l - m| + 10) 2^-24; one rounding to bf16 of the output."""
     E, N = logits.shape
     r = mh.route(logits, top_k, renormalize, 1, N * top_k)
     out, tol = np.zeros((down[0].shape[0], N)), np.zeros((down[0].shape[0], N))
@@ -102,8 +102,8 @@ def moe_layer(logits, x, gate, up, down, top_k: int, renormalize: bool, kept):
             with np.errstate(over="ignore"):
                 s = g / (1 + np.exp(-g))
             h = s * u
-            dh = (1.1 * dg) * (np.abs(u) + du) + (np.abs(s) + 1.1 * dg) * du + (2.0 ** -20 + 2.0 ** -8) * np.abs(h)
-            dh += 2.0 ** -8 * dh + 2.0 ** -133
+            dh = (1.1 * dg) * (np.abs(u) + du) + (np.abs(s) + 1.1 * dg) * du + (2.0 ** -20 + 2.0 ** -16) * np.abs(h)
+            dh += 2.0 ** -16 * dh + 2.0 ** -133
             mag = np.abs(down[e]) @ (np.abs(h) + dh)
             out[:, n] += w * (down[e] @ h)
             tol[:, n] += w * (np.abs(down[e]) @ dh + (kept[1] + 64) * 2.0 ** -23 * mag)
