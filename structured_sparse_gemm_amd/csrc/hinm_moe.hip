@@ -45,8 +45,9 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTokens = HINM_MOE_MAX_TOKENS;
 constexpr int kPairs = kTokens * HINM_MAX_TOP_K;   // (token, expert) pairs at most; a segment holds at least one
 constexpr int kSlab = 131328;                      // bytes of LDS for a segment's activations and a row of zeros
-constexpr int kMaxChannels = 16384;                // of four tokens, with the row of zeros
-static_assert((kMaxChannels + 1) * 8 <= kSlab, "four tokens of the most channels fit");
+constexpr int kMaxChannels = 16384;                // of four columns, with the row of zeros
+static_assert((kMaxChannels + 1) * 8 <= kSlab, "four columns of the most channels fit");
+constexpr int kRed = 260;                          // floats between the waves' sums: 256, and conflict-free reads
 
 // One stack of packed weights; strides are bytes of one expert.
 struct MoeStack {
@@ -89,132 +90,216 @@ __device__ inline int row_columns(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : 16; 
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// One K-block's operands of a lane: 64 rows' fragments f = 0 .. 3.
-template <int VALUES>
+// One K-block's operands of a lane: the fragments (16 rows each) of an item.
+template <int VALUES, int F>
 struct Operand {                   // bf16
-  u32x4 v[4];
-  uint32_t m[4];
+  u32x4 v[F];
+  uint32_t m[F];
+  int index;
 };
-template <>
-struct Operand<HINM_VALUES_MX4> {
-  u32x4 v;
-  uint32_t scale, m[2];
+template <int F>
+struct Operand<HINM_VALUES_MX4, F> {
+  uint32_t v[F];
+  uint32_t scale, m[F / 2];        // scale: a byte a fragment; m: 16 bits a fragment
+  int index;
 };
-template <>
-struct Operand<HINM_VALUES_FP8> {
-  u32x2 v[4];
-  uint32_t m[4], scale[4];
+template <int F>
+struct Operand<HINM_VALUES_FP8, F> {
+  u32x2 v[F];
+  uint32_t m[F], scale[F];
+  int index;
 };
 
-// acc += 64 rows (row block rb of the stack's rows) x 16 tokens over K-blocks
-// v, v + nw, ... below b1, counted from b0; the activations are in `slab`,
-// rows of `pitch` bytes, zeros in row cin.
-template <int VALUES>
-__device__ inline void multiply(const MoeStack& w, int expert, int rb, int b0, int b1, int v, int nw,
-                                const uint8_t* slab, int pitch, f32x4 (&acc)[4]) {
-  constexpr int D = 2;                             // blocks in flight
-  const int lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
-  const int nrb = w.rows / 64, t = rb / nrb, rt = rb % nrb;
-  const __amdgpu_buffer_rsrc_t rvd = buffer(w.val_d + expert * w.b_val_d, w.b_val_d);
-  const __amdgpu_buffer_rsrc_t rvs = buffer(w.val_s + expert * w.b_val_s, w.b_val_s);
-  const __amdgpu_buffer_rsrc_t rm = buffer(w.meta + expert * w.b_meta, w.b_meta);
-  const __amdgpu_buffer_rsrc_t rid = buffer(w.idx_d + expert * w.b_idx_d, w.b_idx_d);
-  const __amdgpu_buffer_rsrc_t ris = buffer(w.idx_s + expert * w.b_idx_s, w.b_idx_s);
-  const __amdgpu_buffer_rsrc_t rsd = buffer(w.scale_d + expert * w.b_scale_d, w.b_scale_d);
-  const __amdgpu_buffer_rsrc_t rss = buffer(w.scale_s + expert * w.b_scale_s, w.b_scale_s);
-  const int first = b0 + v, cnt = first < b1 ? (b1 - first + nw - 1) / nw : 0;
-  if (cnt == 0) return;
+// An item: 16 F rows of one expert's weight over K-blocks b0 .. b1 - 1.
+struct Item {
+  int expert, rows16, b0, b1;      // rows16: its first row / 16
+};
 
-  // Past the end the last block is read again, so that the loop has no
-  // conditions; its products are not added.
-  auto block = [&](int i) { return first + nw * min(i, cnt - 1); };
-  auto load = [&](int i, Operand<VALUES>& o, int& iw) {
-    const int b = block(i);
-    const bool dense = b < w.nkb_d;
-    const uint32_t k = (uint32_t)(dense ? b : b - w.nkb_d);
-    const uint32_t kb = dense ? (uint32_t)(t * w.nkb_d) + k : (uint32_t)(t * w.nkb_s) + k;
-    const __amdgpu_buffer_rsrc_t rv = dense ? rvd : rvs;
-    iw = (int)__builtin_amdgcn_raw_buffer_load_b32(dense ? rid : ris, dense ? 4u * (lane & 31) : 4u * lane,
-                                                   kb * (dense ? 128u : 256u), 0);
-    if constexpr (VALUES == HINM_VALUES_MX4) {
-      const uint32_t u = kb * (uint32_t)nrb + rt;
-      o.v = __builtin_amdgcn_raw_buffer_load_b128(rv, 256u * kc + 16u * i16, u * 1024u, 0);
-      o.scale = __builtin_amdgcn_raw_buffer_load_b32(dense ? rsd : rss, 4u * i16, u * 64u, 0);
-      const u32x2 m = __builtin_amdgcn_raw_buffer_load_b64(rm, 128u * kc + 8u * i16, dense ? 0u : u * 512u, 0);
+// Where a wave reads an item's operands; all scalars.
+struct Source {
+  const uint8_t *val_d, *val_s, *meta, *idx_d, *idx_s, *scale_d, *scale_s;
+  int tile, row;                   // tile, and the item's first row in it
+  int first, end;                  // the wave's blocks: first, first + nw, ... below end
+};
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ inline Source source_of(const MoeStack& w, const Item& it, int v) {
+  const int t = it.rows16 * 16 / w.rows;
+  const int64_t e = it.expert;
+  return {w.val_d + e * w.b_val_d, w.val_s + e * w.b_val_s, w.meta + e * w.b_meta, w.idx_d + e * w.b_idx_d,
+          w.idx_s + e * w.b_idx_s, w.scale_d + e * w.b_scale_d, w.scale_s + e * w.b_scale_s,
+          t, it.rows16 * 16 - t * w.rows, it.b0 + v, it.b1};
+}
+
+template <class T>
+__device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpret_cast<const T*>(base + offset); }
+
+// Block b's operands.  The block's place is scalar and the lane's share a
+// constant; a dense block has no metadata and reads its values' bytes instead.
+template <int VALUES, int F>
+__device__ inline void load_block(const MoeStack& w, const Source& s, int b, Operand<VALUES, F>& o) {
+  const uint32_t lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
+  const bool dense = b < w.nkb_d;
+  const int k = dense ? b : b - w.nkb_d;
+  const int64_t kb = (int64_t)s.tile * (dense ? w.nkb_d : w.nkb_s) + k;
+  o.index = dense ? at<int>(s.idx_d + kb * 128, 4 * (lane & 31)) : at<int>(s.idx_s + kb * 256, 4 * lane);
+  if constexpr (VALUES == HINM_VALUES_MX4) {
+    const int64_t u = kb * (w.rows / 64) + s.row / 64;
+    const uint8_t* val = (dense ? s.val_d : s.val_s) + u * 1024;
+    const uint32_t f0 = (uint32_t)(s.row >> 4) & 3;          // 0 or 2 with two fragments
+    o.scale = at<uint32_t>((dense ? s.scale_d : s.scale_s) + u * 64, 4 * i16) >> (8 * f0);
+    const uint8_t* meta = dense ? val : s.meta + u * 512;
+    if constexpr (F == 4) {
+      const u32x4 v = at<u32x4>(val, 256 * kc + 16 * i16);
+      const u32x2 m = at<u32x2>(meta, 128 * kc + 8 * i16);
+      for (int f = 0; f < 4; ++f) o.v[f] = v[f];
       o.m[0] = m[0];
       o.m[1] = m[1];
     } else {
-      const uint32_t row = kb * (uint32_t)w.rows + rt * 64u;
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if constexpr (VALUES == HINM_VALUES_FP8) {
-          o.v[f] = __builtin_amdgcn_raw_buffer_load_b64(rv, 32u * i16 + 8u * kc + 512u * f, row * 32u, 0);
-          const uint32_t group = dense ? (uint32_t)(t * ((w.nkb_d + 3) / 4)) + k / 4 : (uint32_t)(t * ((w.nkb_s + 3) / 4)) + k / 4;
-          o.scale[f] = __builtin_amdgcn_raw_buffer_load_b8(dense ? rsd : rss, 16u * f + i16, group * w.rows + rt * 64u, 0);
-        } else {
-          o.v[f] = __builtin_amdgcn_raw_buffer_load_b128(rv, 64u * i16 + 16u * kc + 1024u * f, row * 64u, 0);
-        }
-        o.m[f] = __builtin_amdgcn_raw_buffer_load_b16(rm, 8u * i16 + 2u * kc + 128u * f, dense ? 0u : row * 8u, 0);
-      }
+      const u32x2 v = at<u32x2>(val, 256 * kc + 16 * i16 + 4 * f0);
+      o.v[0] = v[0];
+      o.v[1] = v[1];
+      o.m[0] = at<uint32_t>(meta, 128 * kc + 8 * i16 + 2 * f0);
     }
-  };
-  // The lane's share of the transposed reads: 8 bytes of tokens 4 s .. 4 s + 3
-  // (past a short row the first ones again: columns that nothing reads) of
-  // positions 8 kc + i16 / 4 + {0, 4, 32, 36}.
-  const int s8 = 8 * min(i16 & 3, pitch / 8 - 1), p0 = 8 * kc + (i16 >> 2);
-  auto compute = [&](int i, const Operand<VALUES>& o, int iw) {
-    const bool dense = block(i) < w.nkb_d;
-    const int row = (iw < 0 || iw >= w.cin ? w.cin : iw) * pitch;
-    v4i16 b[4];
+  } else {
+    constexpr int kRow = VALUES == HINM_VALUES_FP8 ? 32 : 64;      // bytes of a row
+    const int64_t row = kb * w.rows + s.row;
+    const uint8_t* val = (dense ? s.val_d : s.val_s) + row * kRow;
+    const uint8_t* meta = dense ? val : s.meta + row * 8;
+    const int64_t group = (int64_t)s.tile * (((dense ? w.nkb_d : w.nkb_s) + 3) / 4) + k / 4;
+    const uint8_t* scale = (dense ? s.scale_d : s.scale_s) + group * w.rows + s.row;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int p = p0 + 4 * (k & 1) + 32 * (k >> 1);
-      // a dense block is multiplied as a 2:4 block whose groups keep positions 0 and 1: column 2 q + u at 4 q + u
-      b[k] = tr_read_b(slab + __shfl(row, dense ? 2 * (p >> 2) + (p & 1) : p) + s8);
-    }
-    const bf16x8 lo8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7));
-    const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(b[2], b[3], 0, 1, 2, 3, 4, 5, 6, 7));
-    const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      bf16x8 av;
-      int sidx;
-      if constexpr (VALUES == HINM_VALUES_MX4) {
-        av = mx4_expand(o.v[f], mx4_scale((o.scale >> (8 * f)) & 255u));
-        sidx = (int)((o.m[f >> 1] >> (16 * (f & 1))) & 0xffffu);
-      } else if constexpr (VALUES == HINM_VALUES_FP8) {
-        av = __builtin_bit_cast(bf16x8, fp8_expand(o.v[f], fp8_scale(o.scale[f])));
-        sidx = (int)o.m[f];
+    for (int f = 0; f < F; ++f) {
+      if constexpr (VALUES == HINM_VALUES_FP8) {
+        o.v[f] = at<u32x2>(val, 32 * i16 + 8 * kc + 512 * f);
+        o.scale[f] = at<uint8_t>(scale, 16 * f + i16);
       } else {
-        av = __builtin_bit_cast(bf16x8, o.v[f]);
-        sidx = (int)o.m[f];
+        o.v[f] = at<u32x4>(val, 64 * i16 + 16 * kc + 1024 * f);
       }
-      acc[f] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av, bv, acc[f], dense ? 0x4444 : sidx, 0, 0);
-    }
-  };
-  Operand<VALUES> o[D];
-  int iw[D];
-#pragma unroll
-  for (int k = 0; k < D; ++k) load(k, o[k], iw[k]);
-  for (int i = 0; i < cnt; i += D) {
-#pragma unroll
-    for (int k = 0; k < D; ++k) {
-      if (i + k < cnt) compute(i + k, o[k], iw[k]);
-      load(i + k + D, o[k], iw[k]);
+      o.m[f] = at<uint16_t>(meta, 8 * i16 + 2 * kc + 128 * f);
     }
   }
 }
 
-// The wave's sums of fragment f into its 1 KiB: element (row r, token c) at 16 r + c.
-__device__ inline void put_sums(float* red, const f32x4& acc) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// acc += the block's rows x 16 columns of the slab: rows of `pitch` bytes,
+// zeros in row cin.
+template <int VALUES, int F>
+__device__ inline void multiply_block(const MoeStack& w, int b, const Operand<VALUES, F>& o, const uint8_t* slab,
+                                      int pitch, f32x4 (&acc)[F]) {
+  const int lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
+  // The lane's share of the transposed reads: 8 bytes of columns 4 s .. 4 s + 3
+  // (past a short row the first ones again: columns that nothing reads) of
+  // positions 8 kc + i16 / 4 + {0, 4, 32, 36}.
+  const int s8 = 8 * min(i16 & 3, pitch / 8 - 1), p0 = 8 * kc + (i16 >> 2);
+  const bool dense = b < w.nkb_d;
+  const int row = (o.index < 0 || o.index >= w.cin ? w.cin : o.index) * pitch;
+  v4i16 q[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) red[wave * 256 + (4 * (lane >> 4) + q) * 16 + (lane & 15)] = acc[q];
+  for (int k = 0; k < 4; ++k) {
+    const int p = p0 + 4 * (k & 1) + 32 * (k >> 1);
+    // a dense block is multiplied as a 2:4 block whose groups keep positions 0 and 1: column 2 q + u at 4 q + u
+    q[k] = tr_read_b(slab + __shfl(row, dense ? 2 * (p >> 2) + (p & 1) : p) + s8);
+  }
+  const bf16x8 lo8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(q[2], q[3], 0, 1, 2, 3, 4, 5, 6, 7));
+  const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    bf16x8 av;
+    int sidx;
+    if constexpr (VALUES == HINM_VALUES_MX4) {
+      av = mx4_expand(o.v[f], mx4_scale((o.scale >> (8 * f)) & 255u));
+      sidx = (int)((o.m[f >> 1] >> (16 * (f & 1))) & 0xffffu);
+    } else if constexpr (VALUES == HINM_VALUES_FP8) {
+      av = __builtin_bit_cast(bf16x8, fp8_expand(o.v[f], fp8_scale(o.scale[f])));
+      sidx = (int)o.m[f];
+    } else {
+      av = __builtin_bit_cast(bf16x8, o.v[f]);
+      sidx = (int)o.m[f];
+    }
+    acc[f] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av, bv, acc[f], dense ? 0x4444 : sidx, 0, 0);
+  }
+}
+
+// The wave's share - blocks v, v + NW, ... - of `items` items, in one stream:
+// while a pair of blocks is multiplied the next pair's operands are on their
+// way, across the items' ends too.  item_of(i) names an item, begin(i) makes
+// its activations ready (in step for the whole workgroup) and returns their
+// pitch, and finish(i, acc) takes its sums (in step, too).  One loop body for
+// the first loads, the products and the items' ends: a launch reads every
+// instruction from memory once, and these kernels last some ten times that.
+template <int VALUES, int F, int NW, class ItemOf, class Begin, class Finish>
+__device__ inline void stream(const MoeStack& w, int items, int v, const uint8_t* slab, ItemOf item_of, Begin begin,
+                              Finish finish) {
+  Operand<VALUES, F> o[2];
+  int block[2] = {-1, -1};         // the operands' blocks; -1: none
+  Source src{};
+  int ahead = -1, pairs = 0;       // the item that loads are at, and its pairs left
+  int pitch = 8;
+  f32x4 acc[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma nounroll
+  while (true) {
+    const bool enter = pairs == 0;
+    if (enter) {
+      src.end = src.first;
+      pairs = 1;
+      if (++ahead < items) {
+        src = source_of(w, item_of(ahead), v);
+        pairs = max(1, (src.end - src.first + 2 * NW - 1) / (2 * NW));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (block[k] >= 0) multiply_block<VALUES, F>(w, block[k], o[k], slab, pitch, acc);
+      block[k] = -1;
+      if (src.first < src.end) {
+        block[k] = src.first;
+        load_block<VALUES, F>(w, src, src.first, o[k]);
+        src.first += NW;
+      }
+    }
+    --pairs;
+    if (enter) {
+      if (ahead > 0) finish(ahead - 1, acc);
+      if (ahead >= items) return;
+      pitch = begin(ahead);
+#pragma unroll
+      for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+}
+
+// The waves' sums of the rows r0 .. r0 + 256 / width - 1 (of 16 F) in `width`
+// columns: put by each wave, summed over four waves by each thread, which has
+// element threadIdx.x / 4 and waves 4 (threadIdx.x % 4) .. + 3.
+template <int F>
+__device__ inline void put_sums(float* red, const f32x4 (&acc)[F], int r0, int width) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15;
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+    if (16 * f >= r0 && 16 * f < r0 + 256 / width && col < width)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) red[wave * kRed + (16 * f - r0 + 4 * (lane >> 4) + q) * width + col] = acc[f][q];
+}
+__device__ inline float four_sums(const float* red) {
+  const float* p = red + (threadIdx.x & 3) * 4 * kRed + (threadIdx.x >> 2);
+  return (p[0] + p[kRed]) + (p[2 * kRed] + p[3 * kRed]);
+}
+// The value of lane ^ 1 or ^ 2.
+__device__ inline float quad1(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xf, 0xf, true)); }
+__device__ inline float quad2(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xf, 0xf, true)); }
+
+// A segment's scalars.
+__device__ inline Seg uniform_seg(const Seg& s) {
+  return {(uint16_t)uniform(s.expert), (uint16_t)uniform(s.slot), (uint8_t)uniform(s.n), (uint8_t)uniform(s.rank0),
+          (uint8_t)uniform(s.count), 0, (uint16_t)uniform(s.down)};
 }
 
 // ---------------------------------------------------------------------------
-// Routing of all tokens, by every workgroup for itself (16 waves, a token at a
-// time each: some 1 us, against a launch of its own).
+// Routing of all tokens, by every workgroup for itself: a wave takes a token.
 // ---------------------------------------------------------------------------
 struct RouteScratch {
   uint32_t mask[HINM_MAX_EXPERTS];       // tokens of every expert
@@ -223,89 +308,125 @@ struct RouteScratch {
   float weight[kPairs];
 };
 
-__device__ inline float logit(const MoeArgs& a, int e, int n) {
-  const float l = a.logits_fp32 ? static_cast<const float*>(a.logits)[e * a.ldl + n]
-                                : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[e * a.ldl + n] << 16);
-  return l == l ? l : -__builtin_inff();
+// A logit as a whole number of the same order, 0 for what is not eligible; and
+// back.
+__device__ inline uint32_t key_of(const MoeArgs& a, int e, int n) {
+  float l = a.logits_fp32 ? static_cast<const float*>(a.logits)[e * a.ldl + n]
+                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[e * a.ldl + n] << 16);
+  l += 0.f;                                        // -0 is 0
+  const uint32_t u = __float_as_uint(l);
+  return l > -__builtin_inff() ? ((int)u < 0 ? ~u : u | 0x80000000u) : 0u;
+}
+__device__ inline float logit_of(uint32_t key) { return __uint_as_float((int)key < 0 ? key & 0x7fffffffu : ~key); }
+
+// The wave's largest key (lane 63 of a chain of shifts within rows of 16 and
+// broadcasts between them), and the wave's sum.
+template <int CTRL>
+__device__ inline uint32_t shifted(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false); }
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = max(v, shifted<0x111>(v));
+  v = max(v, shifted<0x112>(v));
+  v = max(v, shifted<0x114>(v));
+  v = max(v, shifted<0x118>(v));
+  v = max(v, shifted<0x142>(v));
+  v = max(v, shifted<0x143>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ inline float wave_sum(float v) {
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
 }
 
-// The up kernel's segments and their tokens by slot go to `seg` and `token`;
-// down (one workgroup's): the table for the down kernel.  Returns the number of
-// segments through n_seg.
+// Token n's experts and weights; NL keys a lane, expert 64 i + lane.
+template <int NL>
+__device__ inline void route_token(const MoeArgs& a, RouteScratch& r, int n) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) key[i] = 64 * i + lane < a.n_experts ? key_of(a, 64 * i + lane, n) : 0u;
+  float top = 0.f, sum = 0.f, mine = 0.f;          // mine: lane j's exp(l_j - top)
+  int chosen = -1;                                 // lane j's expert
+#pragma nounroll
+  for (int j = 0; j < a.top_k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NL; ++i) best = max(best, key[i]);
+    best = wave_max(best);
+    if (best == 0u) break;
+    int id = -1;
+#pragma unroll
+    for (int i = NL - 1; i >= 0; --i) {
+      const uint64_t who = __ballot(key[i] == best);
+      if (who) id = 64 * i + __builtin_ctzll(who);
+    }
+    const float l = logit_of(best);
+    if (j == 0) {
+      top = l;
+      if (!a.renormalize) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const float li = logit_of(key[i]);
+          sum += key[i] == 0u ? 0.f : li == top ? 1.f : expf(li - top);
+        }
+        sum = wave_sum(sum);
+      }
+    }
+    const float p = l == top ? 1.f : expf(l - top);
+    if (a.renormalize) sum += p;
+    if (lane == j) mine = p, chosen = id;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (64 * i + lane == id) key[i] = 0u;
+  }
+  if (lane < a.top_k) {
+    r.id[n * a.top_k + lane] = (int16_t)chosen;
+    r.weight[n * a.top_k + lane] = chosen >= 0 ? mine / sum : 0.f;
+    if (chosen >= 0) atomicOr(&r.mask[chosen], 1u << n);
+  }
+}
+
+// The up kernel's segments and their tokens by slot go to `seg` and `token`,
+// their number to n_seg; down (one workgroup's): the table for the down kernel.
 __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_seg, Seg* seg, uint16_t* token, Table* down) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const float none = -__builtin_inff();
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   for (int e = threadIdx.x; e < a.n_experts; e += kThreads) r.mask[e] = 0u;
   __syncthreads();
   for (int n = wave; n < a.n_tokens; n += kWaves) {
-    constexpr int kLane = HINM_MAX_EXPERTS / 64;
-    float l[kLane];                                // experts lane + 64 i
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) l[i] = 64 * i + lane < a.n_experts ? logit(a, 64 * i + lane, n) : none;
-    float top = none, sum = 0.f, mine = 0.f;       // mine: lane j's exp(l_j - top)
-    int chosen = -1;                               // lane j's expert
-    for (int j = 0; j < a.top_k; ++j) {
-      float best = none;
-      int id = HINM_MAX_EXPERTS;
-#pragma unroll
-      for (int i = 0; i < kLane; ++i)
-        if (l[i] > best) best = l[i], id = 64 * i + lane;
-      for (int d = 1; d < 64; d *= 2) {
-        const float ob = __shfl_xor(best, d);
-        const int oi = __shfl_xor(id, d);
-        if (ob > best || (ob == best && oi < id)) best = ob, id = oi;
-      }
-      if (best == none) break;
-      if (j == 0) {
-        top = best;
-        if (!a.renormalize) {
-#pragma unroll
-          for (int i = 0; i < kLane; ++i) sum += l[i] == top ? 1.f : l[i] == none ? 0.f : expf(l[i] - top);
-          for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-        }
-      }
-      const float p = best == top ? 1.f : expf(best - top);
-      if (a.renormalize) sum += p;
-      if (lane == j) mine = p, chosen = id;
-#pragma unroll
-      for (int i = 0; i < kLane; ++i)
-        if (64 * i + lane == id) l[i] = none;
-    }
-    if (lane < a.top_k) {
-      r.id[n * a.top_k + lane] = (int16_t)chosen;
-      r.weight[n * a.top_k + lane] = chosen >= 0 ? mine / sum : 0.f;
-      if (chosen >= 0) atomicOr(&r.mask[chosen], 1u << n);
-    }
+    if (a.n_experts <= 64) route_token<1>(a, r, n);
+    else if (a.n_experts <= 256) route_token<4>(a, r, n);
+    else route_token<HINM_MAX_EXPERTS / 64>(a, r, n);
   }
   __syncthreads();
-  // slots by expert and token, and the segments of both kernels
+  // slots by expert and token, and the segments of both kernels; the three running counts (each at most kPairs) share
+  // a word
   if (wave == 0) {
-    int slots = 0, ups = 0, downs = 0;             // of the experts before
+    uint32_t before = 0;                           // counts of the experts before
+#pragma nounroll
     for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
       const int e = e0 + lane;
       const int c = e < a.n_experts ? __popc(r.mask[e]) : 0;
       const int nu = (c + a.up_cap - 1) / a.up_cap, nd = (c + a.down_cap - 1) / a.down_cap;
-      int sc = c, su = nu, sd = nd;
+      const uint32_t own = (uint32_t)c | (uint32_t)nu << 10 | (uint32_t)nd << 20;
+      uint32_t all = own;
       for (int d = 1; d < 64; d *= 2) {
-        const int vc = __shfl_up(sc, d), vu = __shfl_up(su, d), vd = __shfl_up(sd, d);
-        if (lane >= d) sc += vc, su += vu, sd += vd;
+        const uint32_t v = __shfl_up(all, d);
+        if (lane >= d) all += v;
       }
-      const int s0 = slots + sc - c, u0 = ups + su - nu, d0 = downs + sd - nd;
+      const uint32_t at = before + all - own;
+      const int s0 = at & 1023, u0 = at >> 10 & 1023, d0 = at >> 20;
       if (e < a.n_experts) r.start[e] = (uint16_t)s0;
       for (int q = 0; q < nu; ++q)
         seg[u0 + q] = {(uint16_t)e, (uint16_t)(s0 + q * a.up_cap), (uint8_t)min(a.up_cap, c - q * a.up_cap),
-                          (uint8_t)(q * a.up_cap), (uint8_t)c, 0, (uint16_t)d0};
+                       (uint8_t)(q * a.up_cap), (uint8_t)c, 0, (uint16_t)d0};
       if (down)
         for (int q = 0; q < nd; ++q)
           down->seg[d0 + q] = {(uint16_t)e, (uint16_t)(s0 + q * a.down_cap), (uint8_t)min(a.down_cap, c - q * a.down_cap),
                                (uint8_t)(q * a.down_cap), (uint8_t)c, 0, (uint16_t)d0};
-      slots += __shfl(sc, 63);
-      ups += __shfl(su, 63);
-      downs += __shfl(sd, 63);
+      before += __shfl(all, 63);
     }
     if (lane == 0) {
-      *n_seg = ups;
-      if (down) down->n_seg = downs;
+      *n_seg = before >> 10 & 1023;
+      if (down) down->n_seg = before >> 20;
     }
   }
   __syncthreads();
@@ -323,11 +444,56 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
   __syncthreads();
 }
 
+// A segment's tokens from X into the slab, [channel][column], and the row of
+// zeros.  A thread reads eight tokens of a channel at once and writes those of
+// the segment, four channels in flight.
+__device__ inline void load_tokens(const MoeArgs& a, const Seg& seg, const uint16_t* token, uint16_t* slab) {
+  const int cin = a.up.cin, width = row_columns(seg.n);
+  uint32_t mask = 0;
+  for (int j = 0; j < seg.n; ++j) mask |= 1u << token[seg.slot + j];
+  mask = (uint32_t)uniform((int)mask);
+  const int64_t end = (int64_t)(cin - 1) * a.ldx + a.n_tokens;       // elements of X
+  constexpr int U = 4;
+  int col = 0;
+  for (int g = 0; g < 32; g += 8) {
+    const uint32_t some = (mask >> g) & 255u;
+    if (!some) continue;
+    for (int c0 = threadIdx.x; c0 < cin; c0 += U * kThreads) {
+      u32x4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = (int64_t)min(c0 + u * kThreads, cin - 1) * a.ldx + g;
+        if (a.n_tokens == 1) v[u][0] = a.x[at];
+        else if (at + 8 <= end) v[u] = *reinterpret_cast<const any_u32x4*>(a.x + at);
+        else {
+          v[u] = u32x4{0u, 0u, 0u, 0u};
+          for (int t = 0; t < 8 && at + t < end; ++t) v[u][t >> 1] |= (uint32_t)a.x[at + t] << (16 * (t & 1));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * kThreads;
+        if (c >= cin) continue;
+        int j = col;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if ((some >> t) & 1u) slab[c * width + j++] = (uint16_t)(v[u][t >> 1] >> (16 * (t & 1)));
+      }
+    }
+    col += __popc(some);
+  }
+  if ((int)threadIdx.x < width) slab[cin * width + threadIdx.x] = 0;
+}
+
+// Items are (segment, 32 rows of the inner channels), a contiguous range of
+// them a workgroup: of 64 rows, the 344 items of a token's two experts of 11008
+// channels left the busiest of 256 workgroups two.
 template <int VALUES>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
+  constexpr int F = 2, R = 16 * F;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
   __shared__ __attribute__((aligned(16))) union {
-    float red[kWaves * 256];
+    float red[kWaves * kRed];
     RouteScratch route;
   } sh;
   __shared__ int n_seg;
@@ -335,108 +501,130 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
   __shared__ uint16_t token[kPairs];
   route_tokens(a, sh.route, &n_seg, segs, token, blockIdx.x == 0 ? a.table : nullptr);
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n_rb = a.up.cout / 64;
-  const int64_t items = (int64_t)n_seg * n_rb;
-  const int i0 = (int)(blockIdx.x * items / gridDim.x), i1 = (int)((blockIdx.x + 1) * items / gridDim.x);
+  const int wave = uniform(threadIdx.x >> 6);
+  const int n_rb = a.up.cout / R, all = uniform(n_seg) * n_rb;     // at most 512 * 512
+  const int i0 = (int)((int64_t)blockIdx.x * all / kCus), i1 = (int)((int64_t)(blockIdx.x + 1) * all / kCus);
   const MoeStack& w = wave < kWaves / 2 ? a.gate : a.up;
-  int held = -1, pitch = 8;
-  for (int item = i0; item < i1; ++item) {
-    const int sg = item / n_rb, rb = item % n_rb;
-    const Seg seg = segs[sg];
-    if (sg != held) {
-      __syncthreads();
-      pitch = 2 * row_columns(seg.n);
-      for (int q = threadIdx.x; q < a.up.cin * (pitch / 2); q += kThreads) {
-        const int c = q / (pitch / 2), j = q % (pitch / 2);
-        reinterpret_cast<uint16_t*>(slab)[q] = j < seg.n ? a.x[c * a.ldx + token[seg.slot + j]] : (uint16_t)0;
-      }
-      if ((int)threadIdx.x < pitch / 2) reinterpret_cast<uint16_t*>(slab)[a.up.cin * (pitch / 2) + threadIdx.x] = 0;
-      __syncthreads();
-      held = sg;
-    }
-    f32x4 acc[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    multiply<VALUES>(w, seg.expert, rb, 0, w.nkb_d + w.nkb_s, wave % (kWaves / 2), kWaves / 2, slab, pitch, acc);
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      put_sums(sh.red, acc[f]);
-      __syncthreads();
-      if (threadIdx.x < 256) {
-        float g = 0.f, u = 0.f;
-        for (int k = 0; k < kWaves / 2; ++k) {
-          g += sh.red[k * 256 + threadIdx.x];
-          u += sh.red[(kWaves / 2 + k) * 256 + threadIdx.x];
+  int held = -1;
+  Seg seg{};                       // of the item at hand
+  int rb = 0;
+  stream<VALUES, F, kWaves / 2>(
+      w, i1 - i0, wave % (kWaves / 2), slab,
+      [&](int i) -> Item {
+        const int sg = (i0 + i) / n_rb;
+        return {uniform(segs[sg].expert), (i0 + i - sg * n_rb) * F, 0, w.nkb_d + w.nkb_s};
+      },
+      [&](int i) {
+        const int sg = (i0 + i) / n_rb;
+        rb = i0 + i - sg * n_rb;
+        if (sg != held) {
+          seg = uniform_seg(segs[sg]);
+          __syncthreads();
+          load_tokens(a, seg, token, reinterpret_cast<uint16_t*>(slab));
+          __syncthreads();
+          held = sg;
         }
-        const int row = rb * 64 + 16 * f + (threadIdx.x >> 4), col = threadIdx.x & 15;
-        if (col < seg.n) {
-          // where the down kernel's segment of this token has it
-          const int rank = seg.rank0 + col, q = rank / a.down_cap;
-          const int width = row_columns(2 * min(a.down_cap, seg.count - q * a.down_cap));
-          const float h = g / (1.f + expf(-g)) * u;
-          const uint16_t hi = to_bf16(h);
-          uint16_t* dst = a.h + (seg.down + q) * a.h_seg + (int64_t)row * width + rank % a.down_cap;
-          dst[0] = hi;
-          dst[width / 2] = to_bf16(h - __uint_as_float((uint32_t)hi << 16));
+        return 2 * row_columns(seg.n);
+      },
+      [&](int, f32x4 (&acc)[F]) {
+        const int width = row_columns(seg.n);
+#pragma nounroll
+        for (int r0 = 0; r0 < R; r0 += 256 / width) {
+          put_sums<F>(sh.red, acc, r0, width);
+          __syncthreads();
+          // of four adjacent threads the first two have the gate's sum, the others the up projection's
+          float g = four_sums(sh.red);
+          g += quad1(g);
+          const float u = quad2(g);
+          const int e = threadIdx.x >> 2, row = r0 + e / width, col = e % width;
+          if ((threadIdx.x & 3) == 0 && col < seg.n && row < R) {
+            // where the down kernel's segment of this token has it
+            const int rank = seg.rank0 + col, q = rank / a.down_cap;
+            const int wide = row_columns(2 * min(a.down_cap, seg.count - q * a.down_cap));
+            const float h = g / (1.f + expf(-g)) * u;
+            const uint16_t hi = to_bf16(h);
+            uint16_t* dst = a.h + (seg.down + q) * a.h_seg + (int64_t)(rb * R + row) * wide + rank - q * a.down_cap;
+            dst[0] = hi;
+            dst[wide / 2] = to_bf16(h - __uint_as_float((uint32_t)hi << 16));
+          }
+          __syncthreads();
         }
-      }
-      __syncthreads();
-    }
-  }
+      });
 }
 
 template <int VALUES>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
+  constexpr int F = 4;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
-  __shared__ float red[kWaves * 256];
+  __shared__ float red[kWaves * kRed];
   __shared__ float out[64 * kTokens];
+  __shared__ float weight[8];      // of the segment at hand, and its tokens
+  __shared__ int token[8];
   __shared__ int s_last;
   const Table& table = *a.table;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n_rb = a.down.cout / 64, nblk = a.down.nkb_d + a.down.nkb_s, n_seg = table.n_seg;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int n_rb = a.down.cout / 64, nblk = a.down.nkb_d + a.down.nkb_s, n_seg = uniform(table.n_seg);
   const int units = n_seg * nblk;
   // shares of a row block's K-blocks: as many as leave no compute unit idle, and a block for each wave
-  const int splits = max(1, min((int)gridDim.x / n_rb, units / kWaves));
-  for (int item = blockIdx.x; item < n_rb * splits; item += gridDim.x) {
+  const int splits = max(1, min(kCus / n_rb, units / kWaves));
+#pragma nounroll
+  for (int item = blockIdx.x; item < n_rb * splits; item += kCus) {
     const int rb = item / splits, split = item % splits;
     // whole segments in turn (an expert's are adjacent: they share its weights in the caches), then an even share of
     // the remaining ones' blocks
-    const int rounds = n_seg / splits, rest = n_seg % splits * nblk, r0 = rounds * splits * nblk;
-    const int u0 = r0 + (int)((int64_t)split * rest / splits), u1 = r0 + (int)((int64_t)(split + 1) * rest / splits);
+    const int rounds = n_seg / splits, rest = (n_seg - rounds * splits) * nblk, r0 = rounds * splits * nblk;
+    const int u0 = r0 + split * rest / splits, u1 = r0 + (split + 1) * rest / splits;
+    const int s0 = u0 / max(nblk, 1), parts = u0 < u1 ? (u1 - 1) / nblk - s0 + 1 : 0;
     for (int q = threadIdx.x; q < 64 * kTokens; q += kThreads) out[q] = 0.f;
-    for (int round = 0, u = u0; round < rounds || u < u1; ++round) {
-      int sg = round * splits + split, b0 = 0, b1 = nblk;
-      if (round >= rounds) {
-        sg = u / nblk;
-        b0 = u % nblk;
-        b1 = min(nblk, b0 + u1 - u);
-        u += b1 - b0;
-      }
-      const Seg seg = table.seg[sg];
-      const int pitch = 2 * row_columns(2 * seg.n);
-      __syncthreads();
-      const u32x2* src = reinterpret_cast<const u32x2*>(a.h + sg * a.h_seg);
-      for (int q = threadIdx.x; q < (a.down.cin + 1) * (pitch / 8); q += kThreads)
-        reinterpret_cast<u32x2*>(slab)[q] = q < a.down.cin * (pitch / 8) ? src[q] : u32x2{0u, 0u};
-      __syncthreads();
-      f32x4 acc[4];
+    auto seg_of = [&](int i) { return i < rounds ? i * splits + split : s0 + i - rounds; };
+    int n = 0;                     // tokens of the segment at hand
+    stream<VALUES, F, kWaves>(
+        a.down, rounds + parts, wave, slab,
+        [&](int i) -> Item {
+          const int sg = seg_of(i);
+          return {uniform(table.seg[sg].expert), rb * F, i < rounds ? 0 : max(0, u0 - sg * nblk),
+                  i < rounds ? nblk : min(nblk, u1 - sg * nblk)};
+        },
+        [&](int i) {
+          const int sg = seg_of(i), slot = uniform(table.seg[sg].slot);
+          n = uniform(table.seg[sg].n);
+          const int pitch = 2 * row_columns(2 * n);
+          const u32x4* src = reinterpret_cast<const u32x4*>(a.h + sg * a.h_seg);
+          const int words = a.down.cin * pitch / 16;         // cin is a multiple of 64
+          __syncthreads();
+          constexpr int U = 4;
+#pragma nounroll
+          for (int q0 = threadIdx.x; q0 < words; q0 += U * kThreads) {
+            u32x4 v[U];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-      multiply<VALUES>(a.down, seg.expert, rb, b0, b1, wave, kWaves, slab, pitch, acc);
+            for (int u = 0; u < U; ++u) v[u] = src[min(q0 + u * kThreads, words - 1)];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        put_sums(red, acc[f]);
-        __syncthreads();
-        if (threadIdx.x < 256) {
-          float s = 0.f;
-          const int row = 16 * f + (threadIdx.x >> 4), col = threadIdx.x & 15, low = min(col + pitch / 4, 15) - col;
-          for (int k = 0; k < kWaves; ++k) s += red[k * 256 + threadIdx.x] + red[k * 256 + threadIdx.x + low];
-          if (col < seg.n) out[row * kTokens + table.token[seg.slot + col]] += table.weight[seg.slot + col] * s;
-        }
-        __syncthreads();
-      }
-    }
+            for (int u = 0; u < U; ++u)
+              if (q0 + u * kThreads < words) reinterpret_cast<u32x4*>(slab)[q0 + u * kThreads] = v[u];
+          }
+          if ((int)threadIdx.x < pitch / 2) reinterpret_cast<uint16_t*>(slab)[a.down.cin * (pitch / 2) + threadIdx.x] = 0;
+          if ((int)threadIdx.x < n) {
+            weight[threadIdx.x] = table.weight[slot + threadIdx.x];
+            token[threadIdx.x] = table.token[slot + threadIdx.x];
+          }
+          __syncthreads();
+          return pitch;
+        },
+        [&](int, f32x4 (&acc)[F]) {
+          const int width = row_columns(2 * n);
+#pragma nounroll
+          for (int r = 0; r < 64; r += 256 / width) {
+            put_sums<F>(red, acc, r, width);
+            __syncthreads();
+            float s = four_sums(red);
+            s += quad1(s);
+            s += quad2(s);
+            s += __shfl_xor(s, 2 * width);                   // the other of the token's two columns
+            const int e = threadIdx.x >> 2, row = r + e / width, col = e % width;
+            if ((threadIdx.x & 3) == 0 && col < n) out[row * kTokens + token[col]] += weight[col] * s;
+            __syncthreads();
+          }
+        });
     __syncthreads();
     constexpr int N = 64 * kTokens / kThreads;     // outputs a thread
     float v[N];
@@ -456,6 +644,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
         const float* p0 = a.part + (int64_t)rb * splits * 64 * kTokens + threadIdx.x;
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = 0.f;
+#pragma unroll 4
         for (int s = 0; s < splits; ++s)
 #pragma unroll
           for (int k = 0; k < N; ++k)
@@ -465,8 +654,8 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     if (last)
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const int q = k * kThreads + threadIdx.x, row = q / kTokens, n = q % kTokens;
-        if (n < a.n_tokens) a.y[((int64_t)rb * 64 + row) * a.ldy + n] = to_bf16(v[k]);
+        const int q = k * kThreads + threadIdx.x, row = q / kTokens, col = q % kTokens;
+        if (col < a.n_tokens) a.y[((int64_t)rb * 64 + row) * a.ldy + col] = to_bf16(v[k]);
       }
     __syncthreads();
   }
