@@ -792,8 +792,8 @@ int hinm_moe_layer_workspace_bytes(const hinm_plan_t* up, const hinm_plan_t* dow
  * may differ), down the reverse cout and cin; every tile_rows is a multiple of
  * 64; each expert's buffers are below 2^31 bytes.  0 <= n_tokens <=
  * HINM_MOE_MAX_TOKENS (0 is a no-op), experts and top_k as in hinm_route.
- * hidden and inter are at most 16384 (HINM_ESHAPE): a few tokens' activations
- * are held in LDS whole.  The workspace is as in hinm_spmm.  Asynchronous on
+ * hidden and inter are at most 16384: a few tokens' activations are held in
+ * LDS whole; every projection keeps a value (HINM_ESHAPE otherwise).  The workspace is as in hinm_spmm.  Asynchronous on
  * `stream`.  Errors: HINM_EINVAL, HINM_ESHAPE, HINM_EALIGN, HINM_EWORKSPACE,
  * HINM_EHIP, HINM_EDEVICE. */
 int hinm_moe_layer(const void* logits, int32_t logits_type, int64_t ldl, const void* x_bf16, int64_t n_tokens,

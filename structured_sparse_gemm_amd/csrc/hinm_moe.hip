@@ -63,11 +63,12 @@ struct Seg {
   uint16_t down;                   // the expert's first segment of the down kernel
 };
 
-// What the up kernel leaves for the down kernel.
+// What the up kernel leaves for the down kernel: its segments as expert, first
+// slot (10 bits each) and tokens, and the tokens and weights by slot.
 struct Table {
   int n_seg;
-  Seg seg[kPairs];
-  uint16_t token[kPairs];          // by slot
+  uint32_t seg[kPairs];
+  uint16_t token[kPairs];
   float weight[kPairs];
 };
 
@@ -224,7 +225,8 @@ __device__ inline void multiply_block(const MoeStack& w, int b, const Operand<VA
 
 // The wave's share - blocks v, v + NW, ... - of `items` items, in one stream:
 // while a pair of blocks is multiplied the next pair's operands are on their
-// way, across the items' ends too.  item_of(i) names an item, begin(i) makes
+// way, across the items' ends too.  item_of(i) names an item (with one block at
+// least) without reading memory, begin(i) makes
 // its activations ready (in step for the whole workgroup) and returns their
 // pitch, and finish(i, acc) takes its sums (in step, too).  One loop body for
 // the first loads, the products and the items' ends: a launch reads every
@@ -232,6 +234,7 @@ __device__ inline void multiply_block(const MoeStack& w, int b, const Operand<VA
 template <int VALUES, int F, int NW, class ItemOf, class Begin, class Finish>
 __device__ inline void stream(const MoeStack& w, int items, int v, const uint8_t* slab, ItemOf item_of, Begin begin,
                               Finish finish) {
+  if (items <= 0) return;
   Operand<VALUES, F> o[2];
   int block[2] = {-1, -1};         // the operands' blocks; -1: none
   Source src{};
@@ -244,7 +247,6 @@ __device__ inline void stream(const MoeStack& w, int items, int v, const uint8_t
   while (true) {
     const bool enter = pairs == 0;
     if (enter) {
-      src.end = src.first;
       pairs = 1;
       if (++ahead < items) {
         src = source_of(w, item_of(ahead), v);
@@ -254,12 +256,12 @@ __device__ inline void stream(const MoeStack& w, int items, int v, const uint8_t
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (block[k] >= 0) multiply_block<VALUES, F>(w, block[k], o[k], slab, pitch, acc);
-      block[k] = -1;
-      if (src.first < src.end) {
-        block[k] = src.first;
-        load_block<VALUES, F>(w, src, src.first, o[k]);
-        src.first += NW;
-      }
+      // past its end an item's last block is read again: a load that only sometimes happens would make every wait one
+      // for all loads in flight
+      const int b = min(src.first, src.end - 1);
+      load_block<VALUES, F>(w, src, b, o[k]);
+      block[k] = src.first < src.end ? b : -1;
+      src.first += NW;
     }
     --pairs;
     if (enter) {
@@ -310,9 +312,7 @@ struct RouteScratch {
 
 // A logit as a whole number of the same order, 0 for what is not eligible; and
 // back.
-__device__ inline uint32_t key_of(const MoeArgs& a, int e, int n) {
-  float l = a.logits_fp32 ? static_cast<const float*>(a.logits)[e * a.ldl + n]
-                          : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[e * a.ldl + n] << 16);
+__device__ inline uint32_t key_of(float l) {
   l += 0.f;                                        // -0 is 0
   const uint32_t u = __float_as_uint(l);
   return l > -__builtin_inff() ? ((int)u < 0 ? ~u : u | 0x80000000u) : 0u;
@@ -341,9 +341,17 @@ __device__ inline float wave_sum(float v) {
 template <int NL>
 __device__ inline void route_token(const MoeArgs& a, RouteScratch& r, int n) {
   const int lane = threadIdx.x & 63;
+  uint32_t raw[NL];
+  if (a.logits_fp32) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) raw[i] = static_cast<const uint32_t*>(a.logits)[min(64 * i + lane, a.n_experts - 1) * a.ldl + n];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) raw[i] = static_cast<const uint16_t*>(a.logits)[min(64 * i + lane, a.n_experts - 1) * a.ldl + n];
+  }
   uint32_t key[NL];
 #pragma unroll
-  for (int i = 0; i < NL; ++i) key[i] = 64 * i + lane < a.n_experts ? key_of(a, 64 * i + lane, n) : 0u;
+  for (int i = 0; i < NL; ++i) key[i] = 64 * i + lane < a.n_experts ? key_of(__uint_as_float(a.logits_fp32 ? raw[i] : raw[i] << 16)) : 0u;
   float top = 0.f, sum = 0.f, mine = 0.f;          // mine: lane j's exp(l_j - top)
   int chosen = -1;                                 // lane j's expert
 #pragma nounroll
@@ -420,8 +428,7 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
                        (uint8_t)(q * a.up_cap), (uint8_t)c, 0, (uint16_t)d0};
       if (down)
         for (int q = 0; q < nd; ++q)
-          down->seg[d0 + q] = {(uint16_t)e, (uint16_t)(s0 + q * a.down_cap), (uint8_t)min(a.down_cap, c - q * a.down_cap),
-                               (uint8_t)(q * a.down_cap), (uint8_t)c, 0, (uint16_t)d0};
+          down->seg[d0 + q] = (uint32_t)e | (uint32_t)(s0 + q * a.down_cap) << 10 | (uint32_t)min(a.down_cap, c - q * a.down_cap) << 20;
       before += __shfl(all, 63);
     }
     if (lane == 0) {
@@ -460,15 +467,21 @@ __device__ inline void load_tokens(const MoeArgs& a, const Seg& seg, const uint1
     if (!some) continue;
     for (int c0 = threadIdx.x; c0 < cin; c0 += U * kThreads) {
       u32x4 v[U];
+      int past[U];                 // elements that the load begins before its own, at the end of X
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t at = (int64_t)min(c0 + u * kThreads, cin - 1) * a.ldx + g;
-        if (a.n_tokens == 1) v[u][0] = a.x[at];
-        else if (at + 8 <= end) v[u] = *reinterpret_cast<const any_u32x4*>(a.x + at);
-        else {
-          v[u] = u32x4{0u, 0u, 0u, 0u};
-          for (int t = 0; t < 8 && at + t < end; ++t) v[u][t >> 1] |= (uint32_t)a.x[at + t] << (16 * (t & 1));
-        }
+        const int64_t from = min(at, end - 8);     // X has 64 elements or more
+        past[u] = (int)(at - from);
+        v[u] = *reinterpret_cast<const any_u32x4*>(a.x + from);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (past[u] & 4) v[u][0] = v[u][2], v[u][1] = v[u][3];
+        if (past[u] & 2) v[u][0] = v[u][1], v[u][1] = v[u][2], v[u][2] = v[u][3];
+        if (past[u] & 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[u][k] = v[u][k] >> 16 | (k < 3 ? v[u][k + 1] << 16 : 0u);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -558,10 +571,13 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
   __shared__ float red[kWaves * kRed];
   __shared__ float out[64 * kTokens];
-  __shared__ float weight[8];      // of the segment at hand, and its tokens
-  __shared__ int token[8];
+  __shared__ Table table;
   __shared__ int s_last;
-  const Table& table = *a.table;
+  static_assert(sizeof(Table) % 4 == 0 && sizeof(Table) / 4 <= 2 * kThreads, "the table is two words a thread");
+#pragma unroll
+  for (int q = threadIdx.x; q < (int)sizeof(Table) / 4; q += kThreads)
+    reinterpret_cast<uint32_t*>(&table)[q] = reinterpret_cast<const uint32_t*>(a.table)[q];
+  __syncthreads();
   const int wave = uniform(threadIdx.x >> 6);
   const int n_rb = a.down.cout / 64, nblk = a.down.nkb_d + a.down.nkb_s, n_seg = uniform(table.n_seg);
   const int units = n_seg * nblk;
@@ -574,20 +590,21 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     // the remaining ones' blocks
     const int rounds = n_seg / splits, rest = (n_seg - rounds * splits) * nblk, r0 = rounds * splits * nblk;
     const int u0 = r0 + split * rest / splits, u1 = r0 + (split + 1) * rest / splits;
-    const int s0 = u0 / max(nblk, 1), parts = u0 < u1 ? (u1 - 1) / nblk - s0 + 1 : 0;
+    const int s0 = u0 / nblk, parts = u0 < u1 ? (u1 - 1) / nblk - s0 + 1 : 0;
     for (int q = threadIdx.x; q < 64 * kTokens; q += kThreads) out[q] = 0.f;
     auto seg_of = [&](int i) { return i < rounds ? i * splits + split : s0 + i - rounds; };
-    int n = 0;                     // tokens of the segment at hand
+    int n = 0, slot = 0;           // tokens of the segment at hand, and the first one's slot
     stream<VALUES, F, kWaves>(
         a.down, rounds + parts, wave, slab,
         [&](int i) -> Item {
           const int sg = seg_of(i);
-          return {uniform(table.seg[sg].expert), rb * F, i < rounds ? 0 : max(0, u0 - sg * nblk),
+          return {uniform(table.seg[sg] & 1023), rb * F, i < rounds ? 0 : max(0, u0 - sg * nblk),
                   i < rounds ? nblk : min(nblk, u1 - sg * nblk)};
         },
         [&](int i) {
-          const int sg = seg_of(i), slot = uniform(table.seg[sg].slot);
-          n = uniform(table.seg[sg].n);
+          const int sg = seg_of(i), word = uniform((int)table.seg[sg]);
+          slot = word >> 10 & 1023;
+          n = word >> 20;
           const int pitch = 2 * row_columns(2 * n);
           const u32x4* src = reinterpret_cast<const u32x4*>(a.h + sg * a.h_seg);
           const int words = a.down.cin * pitch / 16;         // cin is a multiple of 64
@@ -603,10 +620,6 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
               if (q0 + u * kThreads < words) reinterpret_cast<u32x4*>(slab)[q0 + u * kThreads] = v[u];
           }
           if ((int)threadIdx.x < pitch / 2) reinterpret_cast<uint16_t*>(slab)[a.down.cin * (pitch / 2) + threadIdx.x] = 0;
-          if ((int)threadIdx.x < n) {
-            weight[threadIdx.x] = table.weight[slot + threadIdx.x];
-            token[threadIdx.x] = table.token[slot + threadIdx.x];
-          }
           __syncthreads();
           return pitch;
         },
@@ -621,7 +634,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
             s += quad2(s);
             s += __shfl_xor(s, 2 * width);                   // the other of the token's two columns
             const int e = threadIdx.x >> 2, row = r + e / width, col = e % width;
-            if ((threadIdx.x & 3) == 0 && col < n) out[row * kTokens + token[col]] += weight[col] * s;
+            if ((threadIdx.x & 3) == 0 && col < n) out[row * kTokens + table.token[slot + col]] += table.weight[slot + col] * s;
             __syncthreads();
           }
         });
@@ -687,6 +700,7 @@ int check_shapes(const hinm_plan_t& up, const hinm_plan_t& down, int32_t n_exper
     return fail(HINM_ESHAPE, "tile_rows=%d and %d must be multiples of 64", up.tile_rows, down.tile_rows);
   if (down.cout != up.cin || down.cin != up.cout)
     return fail(HINM_ESHAPE, "down is [%d x %d]; [%d x %d] is needed", down.cout, down.cin, up.cin, up.cout);
+  if (up.n_dense + up.n_24 == 0 || down.n_dense + down.n_24 == 0) return fail(HINM_ESHAPE, "a projection keeps no value");
   if (up.cin > kMaxChannels || up.cout > kMaxChannels)
     return fail(HINM_ESHAPE, "%d hidden and %d inner channels; at most %d are supported", up.cin, up.cout, kMaxChannels);
   if (n_experts < 1 || n_experts > HINM_MAX_EXPERTS)
