@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "hinm_device.h"
 #include "hinm_fp8.h"
@@ -24,24 +25,37 @@ __device__ inline fp8_u32x2 tr_read8(const uint8_t* lds) {
   return __builtin_bit_cast(fp8_u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i32*)(lds_u8*)lds));
 }
 
-// The weights of all experts, the activations and a window of their columns.
-// Strides are per expert.
+// The weights of all experts and a window of the activations' columns: x, y
+// and n_cols are the window's, `before` columns precede it of `total`.  Strides
+// are per expert.
 struct Fp8Args {
-  const uint8_t *val_d, *val_s, *scale_d, *scale_s;
-  const uint64_t* meta;
-  const int32_t *idx_d, *idx_s;
-  int64_t n_val_d, n_val_s, n_scale_d, n_scale_s, n_meta, n_idx_d, n_idx_s;   // elements of one expert
+  const uint8_t *val_d, *val_s, *scale_d, *scale_s, *meta, *idx_d, *idx_s;
+  int64_t b_val_d, b_val_s, b_scale_d, b_scale_s, b_meta, b_idx_d, b_idx_s;   // bytes of one expert
   const uint16_t* x;                 // bf16 [cin][ldx]
   int64_t ldx;
-  const uint8_t* x8;                 // E4M3 [cin][ld8], columns col0 .. col1 - 1; E8M0 xs [ld8]
-  const uint8_t* xs;
-  int ld8, col0, col1;
+  const uint8_t *x8, *xs;            // E4M3 [cin][ld8], E8M0 [ld8]
+  int ld8;
   uint16_t* y;
   int64_t ldy;
   const int32_t *starts, *counts;    // NULL: one range, all columns
-  int n_experts, n_cols;
+  int n_experts, n_cols, before, total;
+  int may_split;                     // the workspace has room for partial sums
   int cin, cout, rows, n_tiles, nkb_d, nkb_s;
 };
+
+// Columns [lo, hi) of expert e within the window.
+__device__ inline void range_of(const Fp8Args& a, int e, int& lo, int& hi) {
+  lo = 0;
+  hi = a.n_cols;
+  if (!a.starts) return;
+  const int s = a.starts[e], c = a.counts[e];
+  if (s < 0 || c <= 0 || s >= a.total) {
+    hi = 0;
+    return;
+  }
+  lo = min(max(s - a.before, 0), a.n_cols);
+  hi = min(max(s + min(c, a.total - s) - a.before, lo), a.n_cols);
+}
 
 // ---------------------------------------------------------------------------
 // Activations to 8 bits.  The scale of a token needs its whole column, so one
@@ -62,34 +76,34 @@ __device__ inline u32x4 load_row8(const uint16_t* row, int n, int n_cols) {
 // Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece.
 __global__ __launch_bounds__(256) void fp8_colmax_kernel(Fp8Args a, uint16_t* __restrict__ part) {
   __shared__ u32x4 sh[256];
-  const int c8 = threadIdx.x & 31, n = a.col0 + blockIdx.x * 256 + 8 * c8;
+  const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
   u32x4 m = {0u, 0u, 0u, 0u};
-  if (n < a.col1)
+  if (n < a.n_cols)
     for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
-      const u32x4 v = load_row8(a.x + r * a.ldx, n, a.col1);
+      const u32x4 v = load_row8(a.x + r * a.ldx, n, a.n_cols);
 #pragma unroll
       for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], v[u]);
     }
   sh[threadIdx.x] = m;
   __syncthreads();
-  if (threadIdx.x < 32 && n < a.col1) {
+  if (threadIdx.x < 32 && n < a.n_cols) {
     for (int k = 1; k < 8; ++k)
 #pragma unroll
       for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], sh[32 * k + threadIdx.x][u]);
-    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + blockIdx.x * 256 + 8 * c8) = m;
+    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = m;
   }
 }
 
 __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint16_t* __restrict__ part, int chunks,
                                                           uint8_t* __restrict__ x8, uint8_t* __restrict__ xs) {
   __shared__ u32x4 sh[256];
-  const int c8 = threadIdx.x & 31, k0 = blockIdx.x * 256 + 8 * c8, n = a.col0 + k0;
+  const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
   u32x4 m = {0u, 0u, 0u, 0u};
-  if (n < a.col1)
+  if (n < a.n_cols)
     for (int k = threadIdx.x >> 5; k < chunks; k += 8) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(part + (int64_t)k * a.ld8 + k0);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(part + (int64_t)k * a.ld8 + n);
 #pragma unroll
       for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], v[u]);
     }
@@ -105,73 +119,297 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
     e[u] = fp8_scale_of((m[u >> 1] >> (16 * (u & 1))) & 0xffffu);
     inv[u] = fp8_inverse(e[u]);
   }
-  if (k0 >= a.ld8) return;
+  if (n >= a.ld8) return;
   if (blockIdx.y == 0 && threadIdx.x < 32)
-    for (int u = 0; u < 8; ++u) xs[k0 + u] = (uint8_t)e[u];
+    for (int u = 0; u < 8; ++u) xs[n + u] = (uint8_t)e[u];
   for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
-    const u32x4 v = n < a.col1 ? load_row8(a.x + r * a.ldx, n, a.col1) : u32x4{0u, 0u, 0u, 0u};
+    const u32x4 v = n < a.n_cols ? load_row8(a.x + r * a.ldx, n, a.n_cols) : u32x4{0u, 0u, 0u, 0u};
     fp8_u32x2 c;
     c[0] = fp8_codes<true>(fp8_codes<false>(0u, v[0], inv[0], inv[1]), v[1], inv[2], inv[3]);
     c[1] = fp8_codes<true>(fp8_codes<false>(0u, v[2], inv[4], inv[5]), v[3], inv[6], inv[7]);
-    *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)r * a.ld8 + k0) = c;
+    *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)r * a.ld8 + n) = c;
   }
 }
 
-// Columns [lo, hi) of expert e within the window.
-__device__ inline void window_of(const Fp8Args& a, int e, int& lo, int& hi) {
-  range_of(a, e, lo, hi);
-  lo = max(lo, a.col0);
-  hi = max(lo, min(hi, a.col1));
+// ---------------------------------------------------------------------------
+// Many tokens.  Workgroup = 64 rows x NT tokens, four waves of 64 rows x NT / 4
+// tokens.  The gathered X rows bound such a product (their lines on the way from
+// L2 to the compute unit); as codes they are half the bytes of bf16.  They go
+// straight from memory into a double-buffered LDS tile, one block ahead; values,
+// metadata and scales follow into LDS buffers of their own, two blocks ahead.
+// Codes of both sides become bf16 between LDS and the matrix instruction.
+//
+// Tile layout: position p's row of NT bytes, its 16-byte chunk c at chunk
+// c ^ turned(p), so that a 32-lane half of a transposed read covers every bank
+// once.  An expert's token blocks start at multiples of 16 columns (aligned
+// loads of codes); columns before its first are not written.
+// ---------------------------------------------------------------------------
+__device__ inline void vmem_fence() { __builtin_amdgcn_sched_barrier(0x78f); }   // vector-memory instructions stay put
+
+template <int NT>
+struct Pre {
+  static constexpr int TW = NT / 4;            // tokens of a wave
+  static constexpr int NTB = TW / 32;          // 32-token tiles of a wave
+  static constexpr int CPR = NT / 16;          // 16-byte chunks of a row
+  static constexpr int RPL = 64 / CPR;         // positions of one load
+  static constexpr int TILE = 64 * NT;         // bytes of an X tile
+};
+template <int NT>
+__device__ inline int turned(int p) { return NT == 256 ? 2 * (p & 7) : 2 * ((p >> 1) & 3); }
+
+constexpr int kAux = 4096;                     // a block's values, metadata (at 2048) and scales (at 3072)
+
+template <int NT, bool DENSE>
+__device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1, uint8_t* a0, uint8_t* a1, uint8_t* a2,
+                                      uint8_t* a3, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t raux,
+                                      __amdgpu_buffer_rsrc_t ri, int tile, int nkb, int kbase, int nb, int rot, int rb,
+                                      int n0, const float (&xs)[Pre<NT>::NTB], f32x16 (&acc)[2][Pre<NT>::NTB]) {
+  using C = Pre<NT>;
+  constexpr int KPOS = DENSE ? 32 : 64;        // positions of a block
+  constexpr int RPW = KPOS / 4;                // positions a wave stages
+  constexpr int NJ = RPW / C::RPL;             // X loads of a wave
+  if (nb == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane / C::CPR, sl = lane % C::CPR;
+  uint32_t xoff[NJ];                           // source byte in a row; past the buffer for columns past its rows
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int n = n0 + 16 * (sl ^ turned<NT>(wave * RPW + j * C::RPL + q));
+    xoff[j] = n < a.ld8 ? (uint32_t)n : 0x80000000u;
+  }
+  auto block = [&](int b) {                    // the order starts at block rot and wraps around
+    b = min(b, nb - 1) + rot;
+    return kbase + (b < nb ? b : b - nb);
+  };
+  const uint32_t ipos = (uint32_t)(wave * RPW + (lane % RPW));
+  auto load_idx = [&](int b) -> int {
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, ((uint32_t)(tile * nkb + block(b)) * KPOS + ipos) * 4u, 0, 0);
+  };
+  auto load_x = [&](int iw, uint8_t* xt) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int c = __shfl(iw, j * C::RPL + q);
+      load_lds16(rx, xt + (wave * RPW + j * C::RPL) * NT,
+                 c < 0 || c >= a.cin ? kOob : (uint32_t)c * (uint32_t)a.ld8 + xoff[j]);
+    }
+  };
+  // waves 0 and 1: 32 rows' values each; 2: metadata; 3: scales
+  auto load_aux = [&](int b, uint8_t* at) {
+    const int k = block(b);
+    const uint32_t row = (uint32_t)(tile * nkb + k) * (uint32_t)a.rows + rb * 64u;
+    uint32_t off = row * 32u + 1024u * wave + 16u * lane;
+    if (wave == 2) off = !DENSE && lane < 32 ? row * 8u + 16u * lane : kOob;
+    if (wave == 3) off = lane < 4 ? (uint32_t)(tile * ((nkb + 3) / 4) + k / 4) * (uint32_t)a.rows + rb * 64u + 16u * lane : kOob;
+    load_lds16(raux, at + 1024 * wave, off);
+  };
+  const int m32 = lane & 31, h = lane >> 5;    // operand row or column, and half of the positions
+  const int tg = (lane >> 4) & 1, p = (lane & 15) >> 1, s8 = lane & 1;
+  uint32_t boff[C::NTB];                       // the lane's share of a transposed read
+#pragma unroll
+  for (int j = 0; j < C::NTB; ++j)
+    boff[j] = (uint32_t)((8 * h + p) * NT + 16 * ((wave * (C::TW / 16) + 2 * j + tg) ^ turned<NT>(8 * h + p)) + 8 * s8);
+  auto compute = [&](const uint8_t* xt, const uint8_t* at) {
+    bf16x8 av[2][2];
+    int sidx[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = 32 * r + m32;
+      const float scale = fp8_scale(at[3072 + row]);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)              // values 8 (2 s + h) .. + 7
+        av[r][s] = __builtin_bit_cast(bf16x8, fp8_expand(*reinterpret_cast<const fp8_u32x2*>(at + row * 32 + 16 * s + 8 * h), scale));
+      if constexpr (!DENSE) {
+        const fp8_u32x2 m = *reinterpret_cast<const fp8_u32x2*>(at + 2048 + row * 8);
+        sidx[r][0] = (int)(m[0] >> (16 * h));
+        sidx[r][1] = (int)(m[1] >> (16 * h));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j) {
+        const uint8_t* base = xt + boff[j] + (DENSE ? 16 : 32) * s * NT;
+        const bf16x8 lo8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base), xs[j]));
+        if constexpr (DENSE) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[r][s], lo8, acc[r][j], 0, 0, 0);
+        } else {
+          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base + 16 * NT), xs[j]));
+          const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            acc[r][j] = __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av[r][s], bv, acc[r][j], sidx[r][s], 0, 0);
+        }
+      }
+  };
+
+  uint8_t* const xt[2] = {x0, x1};
+  uint8_t* const at[4] = {a0, a1, a2, a3};
+  int iw[2];                                   // index words of the next block but one (even, odd)
+  __syncthreads();                             // the buffers may still be read by the previous region
+  iw[0] = load_idx(0);
+  iw[1] = load_idx(1);
+  load_aux(0, at[0]);
+  load_x(iw[0], xt[0]);
+  vmem_fence();                                // wait_vm counts the loads behind these
+  iw[0] = load_idx(2);
+  load_aux(1, at[1]);
+  vmem_fence();
+  wait_vm<2>();                                // block 0's X rows and values
+  __syncthreads();
+  // Step b: X rows of b + 1, index words of b + 3, values of b + 2; multiply b;
+  // wait for the X rows, and with them for the values of b + 1.
+  auto step = [&](auto kk, int b) {
+    constexpr int k = decltype(kk)::value, k2 = k % 2;
+    __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
+    load_x(iw[1 - k2], xt[1 - k2]);
+    vmem_fence();
+    iw[1 - k2] = load_idx(b + 3);
+    load_aux(b + 2, at[(k + 2) % 4]);
+    vmem_fence();
+    __builtin_amdgcn_s_setprio(0);
+    compute(xt[k2], at[k]);
+    vmem_fence();
+    wait_vm<2>();
+    __syncthreads();
+  };
+  int b = 0;
+  for (; b + 4 <= nb; b += 4) {
+    step(std::integral_constant<int, 0>{}, b);
+    step(std::integral_constant<int, 1>{}, b + 1);
+    step(std::integral_constant<int, 2>{}, b + 2);
+    step(std::integral_constant<int, 3>{}, b + 3);
+  }
+  if (b < nb) step(std::integral_constant<int, 0>{}, b);
+  if (b + 1 < nb) step(std::integral_constant<int, 1>{}, b + 1);
+  if (b + 2 < nb) step(std::integral_constant<int, 2>{}, b + 2);
+  wait_vm<0>();                                // what was loaded past the end
 }
 
-// ---------------------------------------------------------------------------
-// Simple kernel: 64 rows x 16 tokens of one expert a workgroup, four waves of
-// 16 rows; X rows go through LDS element by element.
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void fp8_simple_kernel(Fp8Args a) {
-  __shared__ __attribute__((aligned(16))) uint8_t xt[64 * 16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, kc = lane >> 4;
-  const int nrb = a.rows / 64;
-  const int t = blockIdx.x / nrb, rb = blockIdx.x % nrb;
-  int first = 0;
-  for (int e = 0; e < a.n_experts; ++e) {
+template <int NT>
+__global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* __restrict__ part,
+                                                             unsigned* __restrict__ counters) {
+  using C = Pre<NT>;
+  // separate LDS objects: loads into one never hold up reads of another
+  __shared__ __attribute__((aligned(16))) uint8_t xs_a[C::TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t xs_b[C::TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t aux_a[kAux];
+  __shared__ __attribute__((aligned(16))) uint8_t aux_b[kAux];
+  __shared__ __attribute__((aligned(16))) uint8_t aux_c[kAux];
+  __shared__ __attribute__((aligned(16))) uint8_t aux_d[kAux];
+  __shared__ int pre[HINM_MAX_EXPERTS + 1];
+  __shared__ int s_last;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nrb = a.rows / 64, n_rb = a.n_tiles * nrb;
+  const int tok_w = wave * C::TW;
+
+  const int items = plan_blocks(a, NT, pre, 16) * n_rb;
+  int splits = 1;
+  while (a.may_split && splits < 4 && items * splits * 2 <= (int)gridDim.x && a.nkb_d + 2 * a.nkb_s >= 16 * splits)
+    splits *= 2;
+  const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8, per_xcd = gridDim.x / 8;
+  const int w_lo = (int)((int64_t)xcd * items * splits / 8), w_hi = (int)((int64_t)(xcd + 1) * items * splits / 8);
+  const __amdgpu_buffer_rsrc_t rx = buffer(a.x8, (int64_t)a.cin * a.ld8);
+
+  for (int work = w_lo + slot; work < w_hi; work += per_xcd) {
+    const int item = work / splits, split = work % splits;
+    const int tb = item / n_rb, trb = item % n_rb, t = trb / nrb, rb = trb % nrb;
+    const int e = find_expert(a, pre, tb);
     int lo, hi;
-    window_of(a, e, lo, hi);
-    const int nb = (hi - lo + 15) / 16;
-    int tb = (int)((blockIdx.y + gridDim.y - first % gridDim.y) % gridDim.y);
-    for (; tb < nb; tb += gridDim.y) {
-      const int n0 = lo + tb * 16;
-      const float xs = n0 + i16 < hi ? fp8_scale(a.xs[n0 + i16 - a.col0]) : 1.f;
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      for (int b = 0; b < a.nkb_d + a.nkb_s; ++b) {
-        const bool dense = b < a.nkb_d;
-        const int k = dense ? b : b - a.nkb_d;
-        const int64_t kb = dense ? (int64_t)t * a.nkb_d + k : (int64_t)t * a.nkb_s + k;
-        const int32_t* idx = dense ? a.idx_d + e * a.n_idx_d + kb * 32 : a.idx_s + e * a.n_idx_s + kb * 64;
-        // a dense block is multiplied as a 2:4 block whose groups keep positions 0 and 1: column 2 q + u at 4 q + u
-        for (int q = threadIdx.x; q < 1024; q += 256) {
-          const int p = q / 16, n = q % 16, c = idx[dense ? 2 * (p >> 2) + (p & 1) : p];
-          xt[q] = c >= 0 && c < a.cin && n0 + n < hi ? a.x8[(int64_t)c * a.ld8 + n0 + n - a.col0] : (uint8_t)0;
-        }
-        __syncthreads();
-        const int64_t row = kb * a.rows + rb * 64 + wave * 16;
-        const uint8_t* val = dense ? a.val_d + e * a.n_val_d : a.val_s + e * a.n_val_s;
-        const int64_t group = dense ? (int64_t)t * ((a.nkb_d + 3) / 4) + k / 4 : (int64_t)t * ((a.nkb_s + 3) / 4) + k / 4;
-        const uint8_t* sc = (dense ? a.scale_d + e * a.n_scale_d : a.scale_s + e * a.n_scale_s) + group * a.rows + rb * 64 + wave * 16;
-        const bf16x8 av = __builtin_bit_cast(bf16x8, fp8_expand(*reinterpret_cast<const fp8_u32x2*>(val + (row + i16) * 32 + 8 * kc), fp8_scale(sc[i16])));
-        const int sidx = dense ? 0x4444 : reinterpret_cast<const uint16_t*>(a.meta + e * a.n_meta)[(row + i16) * 4 + kc];
-        const uint8_t* bp = xt + (8 * kc + (i16 >> 1)) * 16 + 8 * (i16 & 1);
-        const bf16x8 b0 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(bp), xs)), b1 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(bp + 32 * 16), xs));
-        const bf16x16 bv = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-        sum = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av, bv, sum, sidx, 0, 0);
-        __syncthreads();
-      }
-      if (n0 + i16 < hi)
-        for (int k = 0; k < 4; ++k)
-          a.y[((int64_t)t * a.rows + rb * 64 + wave * 16 + 4 * kc + k) * a.ldy + n0 + i16] = to_bf16(sum[k]);
+    range_of(a, e, lo, hi);
+    const int n0 = (lo & -16) + (tb - (a.starts ? pre[e] : 0)) * NT;
+    auto pick = [&](const uint8_t* val, int64_t bv, int64_t bs, const uint8_t* scale, bool meta) {
+      const uint8_t* p = val + e * bv;
+      int64_t n = bv;
+      if (wave == 2) p = a.meta + e * a.b_meta, n = meta ? a.b_meta : 0;
+      if (wave == 3) p = scale + e * bs, n = bs;
+      return buffer(p, n);
+    };
+    const __amdgpu_buffer_rsrc_t rad = pick(a.val_d, a.b_val_d, a.b_scale_d, a.scale_d, false);
+    const __amdgpu_buffer_rsrc_t ras = pick(a.val_s, a.b_val_s, a.b_scale_s, a.scale_s, true);
+    const __amdgpu_buffer_rsrc_t rid = buffer(a.idx_d + e * a.b_idx_d, a.b_idx_d);
+    const __amdgpu_buffer_rsrc_t ris = buffer(a.idx_s + e * a.b_idx_s, a.b_idx_s);
+    float xs[C::NTB];                              // scales of this lane's tokens
+#pragma unroll
+    for (int j = 0; j < C::NTB; ++j) xs[j] = fp8_scale(a.xs[min(n0 + tok_w + 32 * j + (lane & 31), a.ld8 - 1)]);
+
+    f32x16 acc[2][C::NTB];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[r][j][q] = 0.f;
+
+    // this split's share of the K-blocks, by cost: a dense block one unit, a 2:4 block two
+    const int units = a.nkb_d + 2 * a.nkb_s;
+    const int u0 = (int)((int64_t)split * units / splits), u1 = (int)((int64_t)(split + 1) * units / splits);
+    const int d0 = min(u0, a.nkb_d), d1 = min(u1, a.nkb_d);
+    const int k0 = (max(u0, a.nkb_d) - a.nkb_d) / 2, k1 = split + 1 == splits ? a.nkb_s : (max(u1, a.nkb_d) - a.nkb_d) / 2;
+    // tiles, and the token blocks that the XCDs work on at one time, start their loops at different blocks, so
+    // that they do not all read the same rows of X or the same values at once
+    auto turn = [&](int n) { return n > 0 ? (int)(((int64_t)t * n / a.n_tiles + (int64_t)((3 * tb) & 7) * n / 8) % n) : 0; };
+    prefill_region<NT, true>(a, xs_a, xs_b, aux_a, aux_b, aux_c, aux_d, rx, rad, rid, t, a.nkb_d, d0, d1 - d0,
+                             turn(d1 - d0), rb, n0, xs, acc);
+    prefill_region<NT, false>(a, xs_a, xs_b, aux_a, aux_b, aux_c, aux_d, rx, ras, ris, t, a.nkb_s, k0, k1 - k0,
+                              turn(k1 - k0), rb, n0, xs, acc);
+    __syncthreads();
+
+    if (splits > 1) {
+      float flat[2 * C::NTB * 16];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) flat[(r * C::NTB + j) * 16 + q] = acc[r][j][q];
+      if (!join_splits(flat, part, counters, item, split, splits, &s_last)) continue;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[r][j][q] = flat[(r * C::NTB + j) * 16 + q];
     }
-    first += nb;
+
+    // Y through LDS, 32 rows in each tile: acc[r][j][q] is row m = 8 (q / 4) + 4 (lane / 32) + q % 4 of half r, token
+    // tok_w + 32 j + lane % 32
+    uint16_t* const ya = reinterpret_cast<uint16_t*>(xs_a);
+    uint16_t* const yb = reinterpret_cast<uint16_t*>(xs_b);
+    static_assert(32 * NT * 2 <= C::TILE, "32 rows of Y fit a tile");
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          (r ? yb : ya)[(8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * NT + tok_w + 32 * j + (lane & 31)] = to_bf16(acc[r][j][q]);
+    __syncthreads();
+    // 16-byte stores at 16-byte aligned addresses whatever the row's alignment: piece 0 of a row is what precedes its
+    // first aligned address
+    const int from = max(lo - n0, 0), to = min(hi - n0, NT);
+    constexpr int PIECES = NT / 8 + 1;
+    for (int c = threadIdx.x; c < 64 * PIECES; c += 256) {
+      const int rr = c / PIECES, k = c % PIECES;
+      uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + rr) * a.ldy + n0;
+      const int head = (int)(-(uintptr_t)dst / 2 % 8);
+      const int at = max(k == 0 ? 0 : head + 8 * (k - 1), from), end = min(k == 0 ? head : head + 8 * k, to);
+      const uint16_t* src = ((rr >> 5) ? yb : ya) + (rr & 31) * NT;
+      if (end - at == 8 && at % 8 == 0) {
+        *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
+      } else if (end - at == 8) {
+        u32x4 v;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = (uint32_t)src[at + 2 * u] | ((uint32_t)src[at + 2 * u + 1] << 16);
+        *reinterpret_cast<u32x4*>(dst + at) = v;
+      } else {
+        for (int q = at; q < end; ++q) dst[q] = src[q];
+      }
+    }
+    __syncthreads();                           // the tiles are the next item's
   }
 }
 
@@ -201,13 +439,22 @@ int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n
   return HINM_OK;
 }
 
-// Workspace: arrival counters and partial sums, then the rounded activations of
-// one window of columns (at most 2^30 bytes, a multiple of 256 columns), their
-// scales and the pieces' largest magnitudes.
+// Tokens a workgroup takes.  256 halves the bytes of packed values of 128 but
+// costs an expert with few columns the whole block.
+int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
+  const int64_t avg = (n_cols + n_experts - 1) / n_experts;
+  if (n_experts == 1) return (p.cout / 64) * ((n_cols + 255) / 256) <= kCus ? 128 : 256;
+  return avg <= 64 || (avg > 110 && avg <= 170) ? 128 : 256;
+}
+
+// Workspace: arrival counters and the partial sums of kMaxWgs workgroups, where
+// a launch may split; then the rounded activations of one window of columns (at
+// most 2^30 bytes, a multiple of 256 columns), their scales and the pieces'
+// largest magnitudes.
 struct Workspace {
   int64_t window, ld8;               // columns of a window, their pitch
   int64_t x8, xs, part, bytes;       // offsets
-  int chunks;
+  int chunks, split;
 };
 Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   Workspace w{};
@@ -215,7 +462,10 @@ Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) 
   w.window = std::min(n_cols, std::max<int64_t>(256, ((int64_t)1 << 30) / p.cin / 256 * 256));
   w.ld8 = (w.window + 127) / 128 * 128;
   w.chunks = (int)std::min<int64_t>(kChunks, (p.cin + 63) / 64);
-  w.x8 = hinm::kWsCounterBytes;
+  const int nt = token_block(p, n_experts, n_cols);
+  const int64_t fewest = (p.cout / 64) * (n_experts == 1 ? (w.window + nt - 1) / nt : 1);   // items, if any
+  w.split = fewest * 2 <= kMaxWgs;
+  w.x8 = hinm::kWsCounterBytes + (w.split ? (int64_t)kMaxWgs * nt * 64 * 4 : 0);
   w.xs = w.x8 + p.cin * w.ld8;
   w.part = w.xs + w.ld8;
   w.bytes = w.part + (int64_t)w.chunks * w.ld8 * 2;
@@ -243,51 +493,54 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
   st = hinm::ensure_device();
   if (st) return st;
   char* const ws = static_cast<char*>(workspace);
+  auto bytes = [](const void* q) { return static_cast<const uint8_t*>(q); };
   Fp8Args a{};
   a.val_d = k->val_dense;
   a.val_s = k->val_24;
   a.scale_d = k->scale_dense;
   a.scale_s = k->scale_24;
-  a.meta = k->meta_24;
-  a.idx_d = k->idx_dense;
-  a.idx_s = k->idx_24;
+  a.meta = bytes(k->meta_24);
+  a.idx_d = bytes(k->idx_dense);
+  a.idx_s = bytes(k->idx_24);
   a.nkb_d = p.n_dense_pad / HINM_KB_DENSE;
   a.nkb_s = p.n_24_pad / HINM_KB_24;
-  a.n_val_d = p.bytes_val_dense / 2;
-  a.n_val_s = p.bytes_val_24 / 2;
-  a.n_scale_d = (int64_t)p.cout * ((a.nkb_d + 3) / 4);
-  a.n_scale_s = (int64_t)p.cout * ((a.nkb_s + 3) / 4);
-  a.n_meta = p.bytes_meta_24 / 8;
-  a.n_idx_d = p.bytes_idx_dense / 4;
-  a.n_idx_s = p.bytes_idx_24 / 4;
-  a.x = static_cast<const uint16_t*>(x);
+  a.b_val_d = p.bytes_val_dense / 2;
+  a.b_val_s = p.bytes_val_24 / 2;
+  a.b_scale_d = (int64_t)p.cout * ((a.nkb_d + 3) / 4);
+  a.b_scale_s = (int64_t)p.cout * ((a.nkb_s + 3) / 4);
+  a.b_meta = p.bytes_meta_24;
+  a.b_idx_d = p.bytes_idx_dense;
+  a.b_idx_s = p.bytes_idx_24;
   a.ldx = ldx;
-  a.x8 = reinterpret_cast<const uint8_t*>(ws + w.x8);
-  a.xs = reinterpret_cast<const uint8_t*>(ws + w.xs);
+  a.x8 = bytes(ws + w.x8);
+  a.xs = bytes(ws + w.xs);
   a.ld8 = (int)w.ld8;
-  a.y = static_cast<uint16_t*>(y);
   a.ldy = ldy;
   a.starts = starts;
   a.counts = counts;
   a.n_experts = n_experts;
-  a.n_cols = (int)n_cols;
+  a.total = (int)n_cols;
+  a.may_split = w.split;
   a.cin = p.cin;
   a.cout = p.cout;
   a.rows = p.tile_rows;
   a.n_tiles = p.n_tiles;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-  uint16_t* const part = reinterpret_cast<uint16_t*>(ws + w.part);
+  uint16_t* const tops = reinterpret_cast<uint16_t*>(ws + w.part);
+  float* const part = reinterpret_cast<float*>(ws + hinm::kWsCounterBytes);
+  unsigned* const counters = reinterpret_cast<unsigned*>(ws);
+  const int nt = token_block(p, n_experts, n_cols);
   for (int64_t c0 = 0; c0 < n_cols; c0 += w.window) {
-    a.col0 = (int)c0;
-    a.col1 = (int)std::min(n_cols, c0 + w.window);
-    const int cols = a.col1 - a.col0;
-    const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)w.chunks);
-    hipLaunchKernelGGL(fp8_colmax_kernel, grid, dim3(256), 0, stream, a, part);
-    hipLaunchKernelGGL(fp8_columns_kernel, grid, dim3(256), 0, stream, a, part, w.chunks,
+    a.before = (int)c0;
+    a.n_cols = (int)std::min(n_cols - c0, w.window);
+    a.x = static_cast<const uint16_t*>(x) + c0;
+    a.y = static_cast<uint16_t*>(y) + c0;
+    const dim3 grid((unsigned)((a.n_cols + 255) / 256), (unsigned)w.chunks);
+    hipLaunchKernelGGL(fp8_colmax_kernel, grid, dim3(256), 0, stream, a, tops);
+    hipLaunchKernelGGL(fp8_columns_kernel, grid, dim3(256), 0, stream, a, tops, w.chunks,
                        reinterpret_cast<uint8_t*>(ws + w.x8), reinterpret_cast<uint8_t*>(ws + w.xs));
-    const int64_t tbs = cols / 16 + std::min<int64_t>(n_experts, cols) + 1;
-    const dim3 g2((unsigned)(p.cout / 64), (unsigned)std::min<int64_t>(tbs, 65535));
-    hipLaunchKernelGGL(fp8_simple_kernel, g2, dim3(256), 0, stream, a);
+    if (nt == 256) hipLaunchKernelGGL(fp8_prefill_kernel<256>, dim3(kMaxWgs), dim3(256), 0, stream, a, part, counters);
+    else hipLaunchKernelGGL(fp8_prefill_kernel<128>, dim3(kMaxWgs), dim3(256), 0, stream, a, part, counters);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(HINM_EHIP, "8-bit product launch: %s", hipGetErrorString(e));
   }

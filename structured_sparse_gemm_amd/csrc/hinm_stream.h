@@ -1,0 +1,85 @@
+// The loop of the kernels for a few tokens (not installed): a wave's share of
+// the K-blocks of several items, as one stream of loads.
+#ifndef HINM_STREAM_H_
+#define HINM_STREAM_H_
+
+#include "hinm_device.h"
+
+namespace {
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <class T>
+__device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpret_cast<const T*>(base + offset); }
+
+// While DEPTH of a wave's blocks are multiplied the next DEPTH blocks' operands
+// are on their way, across the items' ends too.  For item i:
+//   open(i)       names the wave's blocks, first, first + NW, ... below end, and
+//                 where they lie; the item has one block at least (for some
+//                 wave), and no memory is read (loads that only sometimes
+//                 happen would make every wait one for all loads in flight);
+//   load(s, b, o) loads block b's operands;
+//   multiply(b, o) adds its products;
+//   begin(i), finish(i): before its first and after its last product, in step
+//                 for the whole workgroup.
+// One loop body serves the first loads, the products and the items' ends: a
+// launch fetches every instruction from memory once, at some 2 cycles a byte,
+// and the kernels that use this last only a few times as long.
+template <class Operand, class Source, int DEPTH, int NW, class Open, class Load, class Multiply, class Begin, class Finish>
+__device__ inline void stream(int items, Open open, Load load, Multiply multiply, Begin begin, Finish finish) {
+  if (items <= 0) return;
+  Operand o[DEPTH];
+  int block[DEPTH];                // the operands' blocks; -1: none
+#pragma unroll
+  for (int k = 0; k < DEPTH; ++k) block[k] = -1;
+  Source src{};
+  int ahead = -1, turns = 0;       // the item that loads are at, and its turns of DEPTH blocks left
+#pragma nounroll
+  while (true) {
+    const bool enter = turns == 0;
+    if (enter) {
+      turns = 1;
+      if (++ahead < items) {
+        src = open(ahead);
+        turns = max(1, (src.end - src.first + DEPTH * NW - 1) / (DEPTH * NW));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) {
+      if (block[k] >= 0) multiply(block[k], o[k]);
+      const int b = min(src.first, src.end - 1);   // past its end an item's last block is read again
+      load(src, b, o[k]);
+      block[k] = src.first < src.end ? b : -1;
+      src.first += NW;
+    }
+    --turns;
+    if (enter) {
+      if (ahead > 0) finish(ahead - 1);
+      if (ahead >= items) return;
+      begin(ahead);
+    }
+  }
+}
+
+// Sums over a workgroup's waves of their products' rows r0 .. r0 + 256 / width - 1
+// (of 16 F) in `width` columns.  Each wave puts its own, at a pitch that keeps
+// the reads free of bank conflicts; acc[f][q] is row 16 f + 4 (lane / 16) + q,
+// column lane % 16.
+constexpr int kRed = 260;
+template <int F>
+__device__ inline void put_sums(float* red, const f32x4 (&acc)[F], int r0, int width) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15;
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+    if (16 * f >= r0 && 16 * f < r0 + 256 / width && col < width)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) red[wave * kRed + (16 * f - r0 + 4 * (lane >> 4) + q) * width + col] = acc[f][q];
+}
+
+// The value of lane ^ 1 or ^ 2.
+__device__ inline float quad1(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xf, 0xf, true)); }
+__device__ inline float quad2(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xf, 0xf, true)); }
+
+}  // namespace
+
+#endif  // HINM_STREAM_H_
