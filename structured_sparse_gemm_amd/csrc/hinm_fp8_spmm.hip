@@ -73,61 +73,124 @@ __device__ inline u32x4 load_row8(const uint16_t* row, int n, int n_cols) {
   return v;
 }
 
-// Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece.
+// The largest finite magnitude of a column's piece as bf16 bits; bit 15 marks a
+// NaN or an infinity among its values.
+constexpr uint32_t kBad = 0x80008000u;
+__device__ inline uint32_t pk_max(uint32_t m, uint32_t v) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m), __builtin_bit_cast(u16x2, v)));
+}
+
+// Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece, four
+// loads a thread in flight.
 __global__ __launch_bounds__(256) void fp8_colmax_kernel(Fp8Args a, uint16_t* __restrict__ part) {
   __shared__ u32x4 sh[256];
+  constexpr int U = 4;
   const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
   u32x4 m = {0u, 0u, 0u, 0u};
-  if (n < a.n_cols)
-    for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
-      const u32x4 v = load_row8(a.x + r * a.ldx, n, a.n_cols);
+  if (n < a.n_cols && r0 < r1) {
+    for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * U) {
+      u32x4 v[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], v[u]);
+      for (int u = 0; u < U; ++u) v[u] = load_row8(a.x + (int64_t)min(r + 8 * u, r1 - 1) * a.ldx, n, a.n_cols);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = pk_max(m[k], v[u][k] & 0x7fff7fffu);
     }
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad |= (m[k] & 0xffffu) >= 0x7f80u || m[k] >= 0x7f800000u;
+    if (bad) {                                 // again, without what is not finite
+      const u32x4 all = m;
+      m = u32x4{0u, 0u, 0u, 0u};
+      for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
+        const u32x4 v = load_row8(a.x + r * a.ldx, n, a.n_cols);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fp8_max_finite(m[k], v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        m[k] |= ((all[k] & 0xffffu) >= 0x7f80u ? 0x8000u : 0u) | (all[k] >= 0x7f800000u ? 0x80000000u : 0u);
+    }
+  }
   sh[threadIdx.x] = m;
   __syncthreads();
   if (threadIdx.x < 32 && n < a.n_cols) {
+    u32x4 flags = m & kBad, top = m & ~kBad;
     for (int k = 1; k < 8; ++k)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], sh[32 * k + threadIdx.x][u]);
-    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = m;
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t v = sh[32 * k + threadIdx.x][u];
+        flags[u] |= v & kBad;
+        top[u] = pk_max(top[u], v & ~kBad);
+      }
+    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = flags | top;
   }
 }
 
 __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint16_t* __restrict__ part, int chunks,
                                                           uint8_t* __restrict__ x8, uint8_t* __restrict__ xs) {
-  __shared__ u32x4 sh[256];
+  __shared__ u32x4 sh[2][256];
+  constexpr int U = 4;
   const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
-  u32x4 m = {0u, 0u, 0u, 0u};
-  if (n < a.n_cols)
+  u32x4 flags = {0u, 0u, 0u, 0u}, top = {0u, 0u, 0u, 0u};
+  if (n < a.n_cols) {
+#pragma unroll 4
     for (int k = threadIdx.x >> 5; k < chunks; k += 8) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(part + (int64_t)k * a.ld8 + n);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], v[u]);
+      for (int u = 0; u < 4; ++u) {
+        flags[u] |= v[u] & kBad;
+        top[u] = pk_max(top[u], v[u] & ~kBad);
+      }
     }
-  sh[threadIdx.x] = m;
+  }
+  sh[0][threadIdx.x] = top;
+  sh[1][threadIdx.x] = flags;
   __syncthreads();
   for (int k = 0; k < 8; ++k)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) m[u] = fp8_max_finite(m[u], sh[32 * k + c8][u]);
+    for (int u = 0; u < 4; ++u) {
+      top[u] = pk_max(top[u], sh[0][32 * k + c8][u]);
+      flags[u] |= sh[1][32 * k + c8][u];
+    }
   uint32_t e[8];
   float inv[8];
+  bool plain = true;                           // every value of the eight columns is finite and below the saturation
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    e[u] = fp8_scale_of((m[u >> 1] >> (16 * (u & 1))) & 0xffffu);
+    const uint32_t t = (top[u >> 1] >> (16 * (u & 1))) & 0xffffu;
+    e[u] = fp8_scale_of(t);
     inv[u] = fp8_inverse(e[u]);
+    plain &= e[u] < 246u && !((flags[u >> 1] >> (16 * (u & 1))) & 0x8000u);
   }
   if (n >= a.ld8) return;
   if (blockIdx.y == 0 && threadIdx.x < 32)
     for (int u = 0; u < 8; ++u) xs[n + u] = (uint8_t)e[u];
-  for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
-    const u32x4 v = n < a.n_cols ? load_row8(a.x + r * a.ldx, n, a.n_cols) : u32x4{0u, 0u, 0u, 0u};
-    fp8_u32x2 c;
-    c[0] = fp8_codes<true>(fp8_codes<false>(0u, v[0], inv[0], inv[1]), v[1], inv[2], inv[3]);
-    c[1] = fp8_codes<true>(fp8_codes<false>(0u, v[2], inv[4], inv[5]), v[3], inv[6], inv[7]);
-    *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)r * a.ld8 + n) = c;
+  for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * U) {
+    u32x4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = n < a.n_cols ? load_row8(a.x + (int64_t)min(r + 8 * u, r1 - 1) * a.ldx, n, a.n_cols) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      fp8_u32x2 c = {0u, 0u};
+      if (plain) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lo = __uint_as_float(v[u][k] << 16) * inv[2 * k], hi = __uint_as_float(v[u][k] & 0xffff0000u) * inv[2 * k + 1];
+          c[k >> 1] = (k & 1) ? (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)c[k >> 1], true)
+                              : (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)c[k >> 1], false);
+        }
+      } else {
+        c[0] = fp8_codes<true>(fp8_codes<false>(0u, v[u][0], inv[0], inv[1]), v[u][1], inv[2], inv[3]);
+        c[1] = fp8_codes<true>(fp8_codes<false>(0u, v[u][2], inv[4], inv[5]), v[u][3], inv[6], inv[7]);
+      }
+      if (r + 8 * u < r1) *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)(r + 8 * u) * a.ld8 + n) = c;
+    }
   }
 }
 
@@ -135,9 +198,10 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
 // Many tokens.  Workgroup = 64 rows x NT tokens, four waves of 64 rows x NT / 4
 // tokens.  The gathered X rows bound such a product (their lines on the way from
 // L2 to the compute unit); as codes they are half the bytes of bf16.  They go
-// straight from memory into a double-buffered LDS tile, one block ahead; values,
-// metadata and scales follow into LDS buffers of their own, two blocks ahead.
-// Codes of both sides become bf16 between LDS and the matrix instruction.
+// straight from memory into LDS, two blocks ahead in a ring of three stages (one
+// block ahead in two, a step waited for its own loads: 4096x11008 at 2047 tokens
+// 87 us), and values, metadata and scales with them.  Codes of both sides become
+// bf16 between LDS and the matrix instruction.
 //
 // Tile layout: position p's row of NT bytes, its 16-byte chunk c at chunk
 // c ^ turned(p), so that a 32-lane half of a transposed read covers every bank
@@ -160,8 +224,8 @@ __device__ inline int turned(int p) { return NT == 256 ? 2 * (p & 7) : 2 * ((p >
 constexpr int kAux = 4096;                     // a block's values, metadata (at 2048) and scales (at 3072)
 
 template <int NT, bool DENSE>
-__device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1, uint8_t* a0, uint8_t* a1, uint8_t* a2,
-                                      uint8_t* a3, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t raux,
+__device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1, uint8_t* x2, uint8_t* a0, uint8_t* a1,
+                                      uint8_t* a2, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t raux,
                                       __amdgpu_buffer_rsrc_t ri, int tile, int nkb, int kbase, int nb, int rot, int rb,
                                       int n0, const float (&xs)[Pre<NT>::NTB], f32x16 (&acc)[2][Pre<NT>::NTB]) {
   using C = Pre<NT>;
@@ -208,7 +272,9 @@ __device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1
   uint32_t boff[C::NTB];                       // the lane's share of a transposed read
 #pragma unroll
   for (int j = 0; j < C::NTB; ++j)
-    boff[j] = (uint32_t)((8 * h + p) * NT + 16 * ((wave * (C::TW / 16) + 2 * j + tg) ^ turned<NT>(8 * h + p)) + 8 * s8);
+    boff[j] = (uint32_t)(((DENSE ? 16 : 8) * h + p) * NT + 16 * ((wave * (C::TW / 16) + 2 * j + tg) ^ turned<NT>(p)) + 8 * s8);
+  // Half h of instruction s takes the row's values 8 (2 h + s) .. + 7, so that a
+  // lane's values of both instructions are 16 adjacent bytes.
   auto compute = [&](const uint8_t* xt, const uint8_t* at) {
     bf16x8 av[2][2];
     int sidx[2][2];
@@ -216,27 +282,28 @@ __device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1
     for (int r = 0; r < 2; ++r) {
       const int row = 32 * r + m32;
       const float scale = fp8_scale(at[3072 + row]);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)              // values 8 (2 s + h) .. + 7
-        av[r][s] = __builtin_bit_cast(bf16x8, fp8_expand(*reinterpret_cast<const fp8_u32x2*>(at + row * 32 + 16 * s + 8 * h), scale));
+      const u32x4 v = *reinterpret_cast<const u32x4*>(at + row * 32 + 16 * h);
+      av[r][0] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[0], v[1]}, scale));
+      av[r][1] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[2], v[3]}, scale));
       if constexpr (!DENSE) {
-        const fp8_u32x2 m = *reinterpret_cast<const fp8_u32x2*>(at + 2048 + row * 8);
-        sidx[r][0] = (int)(m[0] >> (16 * h));
-        sidx[r][1] = (int)(m[1] >> (16 * h));
+        const uint32_t m = *reinterpret_cast<const uint32_t*>(at + 2048 + row * 8 + 4 * h);
+        sidx[r][0] = (int)m;
+        sidx[r][1] = (int)(m >> 16);
       }
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < C::NTB; ++j) {
-        const uint8_t* base = xt + boff[j] + (DENSE ? 16 : 32) * s * NT;
+        // positions 16 s + 8 h + p (the lane's row is in boff) and 32 further on; dense: 16 h + 8 s + p
+        const uint8_t* base = xt + boff[j] + (DENSE ? 8 : 16) * s * NT;
         const bf16x8 lo8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base), xs[j]));
         if constexpr (DENSE) {
 #pragma unroll
           for (int r = 0; r < 2; ++r)
             acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[r][s], lo8, acc[r][j], 0, 0, 0);
         } else {
-          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base + 16 * NT), xs[j]));
+          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base + 32 * NT), xs[j]));
           const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
 #pragma unroll
           for (int r = 0; r < 2; ++r)
@@ -245,46 +312,44 @@ __device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1
       }
   };
 
-  uint8_t* const xt[2] = {x0, x1};
-  uint8_t* const at[4] = {a0, a1, a2, a3};
-  int iw[2];                                   // index words of the next block but one (even, odd)
+  uint8_t* const xt[3] = {x0, x1, x2};
+  uint8_t* const at[3] = {a0, a1, a2};
+  int iw[3];                                   // index words by block number
   __syncthreads();                             // the buffers may still be read by the previous region
-  iw[0] = load_idx(0);
-  iw[1] = load_idx(1);
-  load_aux(0, at[0]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) iw[k] = load_idx(k);
   load_x(iw[0], xt[0]);
+  load_aux(0, at[0]);
   vmem_fence();                                // wait_vm counts the loads behind these
-  iw[0] = load_idx(2);
+  load_x(iw[1], xt[1]);
   load_aux(1, at[1]);
+  iw[0] = load_idx(3);
   vmem_fence();
-  wait_vm<2>();                                // block 0's X rows and values
+  wait_vm<NJ + 2>();                           // block 0
   __syncthreads();
-  // Step b: X rows of b + 1, index words of b + 3, values of b + 2; multiply b;
-  // wait for the X rows, and with them for the values of b + 1.
+  // Step b: X rows and values of b + 2, index words of b + 4; multiply b; wait
+  // for b + 1, which the step before loaded.
   auto step = [&](auto kk, int b) {
-    constexpr int k = decltype(kk)::value, k2 = k % 2;
+    constexpr int k = decltype(kk)::value, next = (k + 2) % 3;
     __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
-    load_x(iw[1 - k2], xt[1 - k2]);
-    vmem_fence();
-    iw[1 - k2] = load_idx(b + 3);
-    load_aux(b + 2, at[(k + 2) % 4]);
+    load_x(iw[next], xt[next]);
+    load_aux(b + 2, at[next]);
+    iw[(k + 1) % 3] = load_idx(b + 4);
     vmem_fence();
     __builtin_amdgcn_s_setprio(0);
-    compute(xt[k2], at[k]);
+    compute(xt[k], at[k]);
     vmem_fence();
-    wait_vm<2>();
+    wait_vm<NJ + 2>();
     __syncthreads();
   };
   int b = 0;
-  for (; b + 4 <= nb; b += 4) {
+  for (; b + 3 <= nb; b += 3) {
     step(std::integral_constant<int, 0>{}, b);
     step(std::integral_constant<int, 1>{}, b + 1);
     step(std::integral_constant<int, 2>{}, b + 2);
-    step(std::integral_constant<int, 3>{}, b + 3);
   }
   if (b < nb) step(std::integral_constant<int, 0>{}, b);
   if (b + 1 < nb) step(std::integral_constant<int, 1>{}, b + 1);
-  if (b + 2 < nb) step(std::integral_constant<int, 2>{}, b + 2);
   wait_vm<0>();                                // what was loaded past the end
 }
 
@@ -295,10 +360,10 @@ __global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* _
   // separate LDS objects: loads into one never hold up reads of another
   __shared__ __attribute__((aligned(16))) uint8_t xs_a[C::TILE];
   __shared__ __attribute__((aligned(16))) uint8_t xs_b[C::TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t xs_c[C::TILE];
   __shared__ __attribute__((aligned(16))) uint8_t aux_a[kAux];
   __shared__ __attribute__((aligned(16))) uint8_t aux_b[kAux];
   __shared__ __attribute__((aligned(16))) uint8_t aux_c[kAux];
-  __shared__ __attribute__((aligned(16))) uint8_t aux_d[kAux];
   __shared__ int pre[HINM_MAX_EXPERTS + 1];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63;
@@ -352,9 +417,9 @@ __global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* _
     // tiles, and the token blocks that the XCDs work on at one time, start their loops at different blocks, so
     // that they do not all read the same rows of X or the same values at once
     auto turn = [&](int n) { return n > 0 ? (int)(((int64_t)t * n / a.n_tiles + (int64_t)((3 * tb) & 7) * n / 8) % n) : 0; };
-    prefill_region<NT, true>(a, xs_a, xs_b, aux_a, aux_b, aux_c, aux_d, rx, rad, rid, t, a.nkb_d, d0, d1 - d0,
+    prefill_region<NT, true>(a, xs_a, xs_b, xs_c, aux_a, aux_b, aux_c, rx, rad, rid, t, a.nkb_d, d0, d1 - d0,
                              turn(d1 - d0), rb, n0, xs, acc);
-    prefill_region<NT, false>(a, xs_a, xs_b, aux_a, aux_b, aux_c, aux_d, rx, ras, ris, t, a.nkb_s, k0, k1 - k0,
+    prefill_region<NT, false>(a, xs_a, xs_b, xs_c, aux_a, aux_b, aux_c, rx, ras, ris, t, a.nkb_s, k0, k1 - k0,
                               turn(k1 - k0), rb, n0, xs, acc);
     __syncthreads();
 
@@ -460,7 +525,7 @@ Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) 
   Workspace w{};
   if (n_cols == 0) return w;
   w.window = std::min(n_cols, std::max<int64_t>(256, ((int64_t)1 << 30) / p.cin / 256 * 256));
-  w.ld8 = (w.window + 127) / 128 * 128;
+  w.ld8 = w.window <= 128 ? 128 : ((w.window + 255) / 256 | 1) * 256;
   w.chunks = (int)std::min<int64_t>(kChunks, (p.cin + 63) / 64);
   const int nt = token_block(p, n_experts, n_cols);
   const int64_t fewest = (p.cout / 64) * (n_experts == 1 ? (w.window + nt - 1) / nt : 1);   // items, if any
