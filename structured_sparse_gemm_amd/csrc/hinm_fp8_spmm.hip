@@ -196,20 +196,25 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
 
 // ---------------------------------------------------------------------------
 // Many tokens.  Workgroup = 64 rows x NT tokens, four waves of 64 rows x NT / 4
-// tokens.  The gathered X rows bound such a product (their lines on the way from
-// L2 to the compute unit); as codes they are half the bytes of bf16.  They go
-// straight from memory into LDS, two blocks ahead in a ring of three stages (one
-// block ahead in two, a step waited for its own loads: 4096x11008 at 2047 tokens
-// 87 us), and values, metadata and scales with them.  Codes of both sides become
-// bf16 between LDS and the matrix instruction.
+// tokens.  Everything goes straight from memory into LDS: the gathered X rows
+// two blocks ahead into a ring of three tiles, the weight's blocks (values,
+// metadata, scales, indices) four blocks ahead into a ring of five slots, so
+// that the indices of a block's rows have come when its rows are asked for.
+// Codes of both sides become bf16 between LDS and the matrix instruction.
+//
+// A wave's loads complete in order, and at the end of step b those of step
+// b - 1 must have: what step b asked for has two steps' time.  The weight's
+// blocks need it: they come from the last-level cache or from memory, some two
+// thousand cycles away (with __syncthreads(), which waits for all loads into
+// LDS, 4096x11008 at 2047 tokens took 87 us, and 67 without the rows or without
+// the products).  Hence the loads are inline assembly, which the compiler does
+// not wait for, and the barrier waits for LDS operations alone.
 //
 // Tile layout: position p's row of NT bytes, its 16-byte chunk c at chunk
 // c ^ turned(p), so that a 32-lane half of a transposed read covers every bank
 // once.  An expert's token blocks start at multiples of 16 columns (aligned
 // loads of codes); columns before its first are not written.
 // ---------------------------------------------------------------------------
-__device__ inline void vmem_fence() { __builtin_amdgcn_sched_barrier(0x78f); }   // vector-memory instructions stay put
-
 template <int NT>
 struct Pre {
   static constexpr int TW = NT / 4;            // tokens of a wave
@@ -221,149 +226,186 @@ struct Pre {
 template <int NT>
 __device__ inline int turned(int p) { return NT == 256 ? 2 * (p & 7) : 2 * ((p >> 1) & 3); }
 
-constexpr int kAux = 4096;                     // a block's values, metadata (at 2048) and scales (at 3072)
+// A slot of the weight's ring: 64 rows' values of a block, then what one load
+// brings: metadata, scales and indices.
+constexpr int kTiles = 3, kRing = 5, kSlot = 3072, kMeta = 2048, kScale = kMeta + 512, kIndex = kScale + 64;
 
-template <int NT, bool DENSE>
-__device__ inline void prefill_region(const Fp8Args& a, uint8_t* x0, uint8_t* x1, uint8_t* x2, uint8_t* a0, uint8_t* a1,
-                                      uint8_t* a2, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t raux,
-                                      __amdgpu_buffer_rsrc_t ri, int tile, int nkb, int kbase, int nb, int rot, int rb,
-                                      int n0, const float (&xs)[Pre<NT>::NTB], f32x16 (&acc)[2][Pre<NT>::NTB]) {
+// Sixteen bytes a lane into LDS at `lds` + 16 lane: from a buffer (past its end
+// zeros; sc0 as in load_lds16), and from an address.
+__device__ inline void lds_load(u32x4 buffer, uint32_t lds, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen sc0 lds"
+               :: "s"(lds), "v"(offset), "s"(buffer) : "memory");
+}
+__device__ inline void lds_load(const uint8_t* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(src) : "memory");
+}
+// A barrier that waits for this wave's LDS operations, not for its loads.
+__device__ inline void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// An item: row block rb of tile t of an expert, blocks d0 .. d0 + nd - 1 of its
+// dense region and k0 .. k0 + ns - 1 of its 2:4 region, each region from its
+// block turn on and around; the dense ones first.
+struct Work {
+  const uint8_t *val_d, *val_s, *scale_d, *scale_s, *meta, *idx_d, *idx_s;
+  int tile, rb, d0, nd, turn_d, k0, ns, turn_s;
+};
+
+template <int NT>
+__device__ inline void multiply_weight(const Fp8Args& a, const Work w, uint8_t* lds, u32x4 rx, int n0,
+                                       const float (&xs)[Pre<NT>::NTB], f32x16 (&acc)[2][Pre<NT>::NTB]) {
   using C = Pre<NT>;
-  constexpr int KPOS = DENSE ? 32 : 64;        // positions of a block
-  constexpr int RPW = KPOS / 4;                // positions a wave stages
-  constexpr int NJ = RPW / C::RPL;             // X loads of a wave
-  if (nb == 0) return;
-  const int lane = threadIdx.x & 63;
+  constexpr int NJ = 16 / C::RPL;              // X loads of a wave for 64 positions
+  const int lane = threadIdx.x & 63, nb = w.nd + w.ns;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const ring = lds + kTiles * C::TILE;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)lds, ring0 = lds0 + kTiles * C::TILE;
+
+  // Block b's bytes of the weight into its slot: waves 0 and 1 (and 3 again) half of the values each, wave 2 in lanes
+  // 0 .. 31 metadata (a dense block has none and reads values), 32 .. 35 scales, the others indices, the last sixteen
+  // bytes again where there are no more.
+  auto load_weight = [&](int b) {
+    const uint32_t slot = ring0 + (uint32_t)(b % kRing) * kSlot;
+    b = min(b, nb - 1);                        // past the end the last block again: waits are for known numbers of loads
+    const bool dense = b < w.nd;
+    int k = dense ? b + w.turn_d : b - w.nd + w.turn_s;
+    k = dense ? w.d0 + (k < w.nd ? k : k - w.nd) : w.k0 + (k < w.ns ? k : k - w.ns);
+    const int nkb = dense ? a.nkb_d : a.nkb_s;
+    const int64_t kb = (int64_t)w.tile * nkb + k, row = kb * a.rows + w.rb * 64;
+    const uint8_t* val = (dense ? w.val_d : w.val_s) + row * 32;
+    if (wave != 2) {
+      lds_load(val + 1024 * (wave & 1) * (wave < 2) + 16 * lane, slot + 1024u * (wave & 1) * (wave < 2));
+    } else {
+      const int64_t group = (int64_t)w.tile * ((nkb + 3) / 4) + k / 4;
+      const uint8_t* scale = (dense ? w.scale_d : w.scale_s) + group * a.rows + w.rb * 64;
+      const uint8_t* index = (dense ? w.idx_d : w.idx_s) + kb * (dense ? 128 : 256);
+      const uint8_t* src = dense ? val : w.meta + row * 8;
+      uint32_t off = 16u * lane;
+      if (lane >= 32) src = scale, off -= 512u;
+      if (lane >= 36) src = index, off = 16u * min(lane - 36, dense ? 7 : 15);
+      lds_load(src + off, slot + kMeta);
+    }
+  };
+  // A wave stages 16 positions of a 2:4 block, or 8 of a dense one, RPL a load: load j those from first + RPL j on,
+  // first a multiple of 8 or 16, so that turned() is the same for both.
   const int q = lane / C::CPR, sl = lane % C::CPR;
   uint32_t xoff[NJ];                           // source byte in a row; past the buffer for columns past its rows
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int n = n0 + 16 * (sl ^ turned<NT>(wave * RPW + j * C::RPL + q));
+    const int n = n0 + 16 * (sl ^ turned<NT>(j * C::RPL + q));
     xoff[j] = n < a.ld8 ? (uint32_t)n : 0x80000000u;
   }
-  auto block = [&](int b) {                    // the order starts at block rot and wraps around
-    b = min(b, nb - 1) + rot;
-    return kbase + (b < nb ? b : b - nb);
-  };
-  const uint32_t ipos = (uint32_t)(wave * RPW + (lane % RPW));
-  auto load_idx = [&](int b) -> int {
-    return (int)__builtin_amdgcn_raw_buffer_load_b32(ri, ((uint32_t)(tile * nkb + block(b)) * KPOS + ipos) * 4u, 0, 0);
-  };
-  auto load_x = [&](int iw, uint8_t* xt) {
+  auto load_x = [&](int b) {
+    const uint32_t tile = lds0 + (uint32_t)(b % kTiles) * C::TILE;
+    b = min(b, nb - 1);
+    const int* index = reinterpret_cast<const int*>(ring + (b % kRing) * kSlot + kIndex);
+    auto rows = [&](auto count, int first) {
+      int c[decltype(count)::value];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int c = __shfl(iw, j * C::RPL + q);
-      load_lds16(rx, xt + (wave * RPW + j * C::RPL) * NT,
-                 c < 0 || c >= a.cin ? kOob : (uint32_t)c * (uint32_t)a.ld8 + xoff[j]);
-    }
+      for (int j = 0; j < decltype(count)::value; ++j) c[j] = index[first + j * C::RPL + q];
+#pragma unroll
+      for (int j = 0; j < decltype(count)::value; ++j)
+        lds_load(rx, tile + (first + j * C::RPL) * NT,
+                 (uint32_t)c[j] < (uint32_t)a.cin ? (uint32_t)c[j] * (uint32_t)a.ld8 + xoff[j] : kOob);
+    };
+    if (b < w.nd) rows(std::integral_constant<int, NJ / 2>{}, wave * 8);
+    else rows(std::integral_constant<int, NJ>{}, wave * 16);
   };
-  // waves 0 and 1: 32 rows' values each; 2: metadata; 3: scales
-  auto load_aux = [&](int b, uint8_t* at) {
-    const int k = block(b);
-    const uint32_t row = (uint32_t)(tile * nkb + k) * (uint32_t)a.rows + rb * 64u;
-    uint32_t off = row * 32u + 1024u * wave + 16u * lane;
-    if (wave == 2) off = !DENSE && lane < 32 ? row * 8u + 16u * lane : kOob;
-    if (wave == 3) off = lane < 4 ? (uint32_t)(tile * ((nkb + 3) / 4) + k / 4) * (uint32_t)a.rows + rb * 64u + 16u * lane : kOob;
-    load_lds16(raux, at + 1024 * wave, off);
+  // until all but block b's rows and `more` other loads have come
+  auto wait_but = [&](int b, auto more) {
+    if (b < w.nd) wait_vm<NJ / 2 + decltype(more)::value>();
+    else wait_vm<NJ + decltype(more)::value>();
   };
   const int m32 = lane & 31, h = lane >> 5;    // operand row or column, and half of the positions
   const int tg = (lane >> 4) & 1, p = (lane & 15) >> 1, s8 = lane & 1;
-  uint32_t boff[C::NTB];                       // the lane's share of a transposed read
+  // The lane's share of a transposed read: the row of its position in the first
+  // read of instruction 0.  Instruction s's positions are 16 s + 8 h + p, and 32
+  // further on.  A dense block is multiplied as a 2:4 block whose groups keep
+  // positions 0 and 1 - column 2 q + u at 4 q + u, as many instructions as the
+  // dense ones would be - and positions 4 q + 2, + 3, which nothing reads, take
+  // those rows again.
+  const int row24 = 8 * h + p, row_dense = 4 * h + 2 * (p >> 2) + (p & 1);
+  uint32_t off24[C::NTB], off_dense[C::NTB];
 #pragma unroll
-  for (int j = 0; j < C::NTB; ++j)
-    boff[j] = (uint32_t)(((DENSE ? 16 : 8) * h + p) * NT + 16 * ((wave * (C::TW / 16) + 2 * j + tg) ^ turned<NT>(p)) + 8 * s8);
+  for (int j = 0; j < C::NTB; ++j) {
+    const int chunk = wave * (C::TW / 16) + 2 * j + tg;
+    off24[j] = (uint32_t)(row24 * NT + 16 * (chunk ^ turned<NT>(row24)) + 8 * s8);
+    off_dense[j] = (uint32_t)(row_dense * NT + 16 * (chunk ^ turned<NT>(row_dense)) + 8 * s8);
+  }
   // Half h of instruction s takes the row's values 8 (2 h + s) .. + 7, so that a
   // lane's values of both instructions are 16 adjacent bytes.
-  auto compute = [&](const uint8_t* xt, const uint8_t* at) {
+  auto compute = [&](int b) {
+    const bool dense = b < w.nd;
+    const uint8_t *xt = lds + (b % kTiles) * C::TILE, *slot = ring + (b % kRing) * kSlot;
+    const int second = dense ? 8 * NT : 16 * NT;
+    // all of the block's LDS reads first: with two waves a SIMD little else hides their latency
+    float scale[2];
+    u32x4 v[2];
+    uint32_t m[2];
+    fp8_u32x2 raw[2][C::NTB][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      scale[r] = fp8_scale(slot[kScale + 32 * r + m32]);
+      v[r] = *reinterpret_cast<const u32x4*>(slot + (32 * r + m32) * 32 + 16 * h);
+      m[r] = *reinterpret_cast<const uint32_t*>(slot + kMeta + (32 * r + m32) * 8 + 4 * h);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) raw[s][j][u] = tr_read8(xt + (dense ? off_dense[j] : off24[j]) + (s + 2 * u) * second);
+    __builtin_amdgcn_sched_barrier(0);
     bf16x8 av[2][2];
     int sidx[2][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = 32 * r + m32;
-      const float scale = fp8_scale(at[3072 + row]);
-      const u32x4 v = *reinterpret_cast<const u32x4*>(at + row * 32 + 16 * h);
-      av[r][0] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[0], v[1]}, scale));
-      av[r][1] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[2], v[3]}, scale));
-      if constexpr (!DENSE) {
-        const uint32_t m = *reinterpret_cast<const uint32_t*>(at + 2048 + row * 8 + 4 * h);
-        sidx[r][0] = (int)m;
-        sidx[r][1] = (int)(m >> 16);
-      }
+      av[r][0] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[r][0], v[r][1]}, scale[r]));
+      av[r][1] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[r][2], v[r][3]}, scale[r]));
+      sidx[r][0] = dense ? 0x4444 : (int)m[r];
+      sidx[r][1] = dense ? 0x4444 : (int)(m[r] >> 16);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < C::NTB; ++j) {
-        // positions 16 s + 8 h + p (the lane's row is in boff) and 32 further on; dense: 16 h + 8 s + p
-        const uint8_t* base = xt + boff[j] + (DENSE ? 8 : 16) * s * NT;
-        const bf16x8 lo8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base), xs[j]));
-        if constexpr (DENSE) {
+        const bf16x8 lo8 = __builtin_bit_cast(bf16x8, fp8_expand(raw[s][j][0], xs[j]));
+        const bf16x8 hi8 = __builtin_bit_cast(bf16x8, fp8_expand(raw[s][j][1], xs[j]));
+        const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[r][s], lo8, acc[r][j], 0, 0, 0);
-        } else {
-          const bf16x8 hi8 = __builtin_bit_cast(bf16x8, fp8_expand(tr_read8(base + 32 * NT), xs[j]));
-          const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            acc[r][j] = __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av[r][s], bv, acc[r][j], sidx[r][s], 0, 0);
-        }
+        for (int r = 0; r < 2; ++r)
+          acc[r][j] = __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av[r][s], bv, acc[r][j], sidx[r][s], 0, 0);
       }
   };
 
-  uint8_t* const xt[3] = {x0, x1, x2};
-  uint8_t* const at[3] = {a0, a1, a2};
-  int iw[3];                                   // index words by block number
-  __syncthreads();                             // the buffers may still be read by the previous region
-#pragma unroll
-  for (int k = 0; k < 3; ++k) iw[k] = load_idx(k);
-  load_x(iw[0], xt[0]);
-  load_aux(0, at[0]);
-  vmem_fence();                                // wait_vm counts the loads behind these
-  load_x(iw[1], xt[1]);
-  load_aux(1, at[1]);
-  iw[0] = load_idx(3);
-  vmem_fence();
-  wait_vm<NJ + 2>();                           // block 0
-  __syncthreads();
-  // Step b: X rows and values of b + 2, index words of b + 4; multiply b; wait
-  // for b + 1, which the step before loaded.
-  auto step = [&](auto kk, int b) {
-    constexpr int k = decltype(kk)::value, next = (k + 2) % 3;
+  step_barrier();                              // LDS is free
+  wait_vm<0>();                                // counted loads begin here
+  for (int b = 0; b < kRing - 1; ++b) load_weight(b);
+  wait_vm<kRing - 3>();                        // the indices of blocks 0 and 1
+  step_barrier();
+  load_x(0);
+  load_x(1);
+  wait_but(min(1, nb - 1), std::integral_constant<int, 0>{});
+  step_barrier();
+#pragma nounroll
+  for (int b = 0; b < nb; ++b) {
     __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
-    load_x(iw[next], xt[next]);
-    load_aux(b + 2, at[next]);
-    iw[(k + 1) % 3] = load_idx(b + 4);
-    vmem_fence();
+    load_x(b + 2);
+    load_weight(b + kRing - 1);
     __builtin_amdgcn_s_setprio(0);
-    compute(xt[k], at[k]);
-    vmem_fence();
-    wait_vm<NJ + 2>();
-    __syncthreads();
-  };
-  int b = 0;
-  for (; b + 3 <= nb; b += 3) {
-    step(std::integral_constant<int, 0>{}, b);
-    step(std::integral_constant<int, 1>{}, b + 1);
-    step(std::integral_constant<int, 2>{}, b + 2);
+    compute(b);
+    wait_but(min(b + 2, nb - 1), std::integral_constant<int, 1>{});
+    step_barrier();
   }
-  if (b < nb) step(std::integral_constant<int, 0>{}, b);
-  if (b + 1 < nb) step(std::integral_constant<int, 1>{}, b + 1);
   wait_vm<0>();                                // what was loaded past the end
 }
 
+constexpr int kPreThreads = 256;
+
 template <int NT>
-__global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* __restrict__ part,
-                                                             unsigned* __restrict__ counters) {
+__global__ __launch_bounds__(kPreThreads, 2) void fp8_prefill_kernel(Fp8Args a, float* __restrict__ part,
+                                                                     unsigned* __restrict__ counters) {
   using C = Pre<NT>;
-  // separate LDS objects: loads into one never hold up reads of another
-  __shared__ __attribute__((aligned(16))) uint8_t xs_a[C::TILE];
-  __shared__ __attribute__((aligned(16))) uint8_t xs_b[C::TILE];
-  __shared__ __attribute__((aligned(16))) uint8_t xs_c[C::TILE];
-  __shared__ __attribute__((aligned(16))) uint8_t aux_a[kAux];
-  __shared__ __attribute__((aligned(16))) uint8_t aux_b[kAux];
-  __shared__ __attribute__((aligned(16))) uint8_t aux_c[kAux];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kTiles * C::TILE + kRing * kSlot];
   __shared__ int pre[HINM_MAX_EXPERTS + 1];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63;
@@ -377,7 +419,8 @@ __global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* _
     splits *= 2;
   const int xcd = blockIdx.x % 8, slot = blockIdx.x / 8, per_xcd = gridDim.x / 8;
   const int w_lo = (int)((int64_t)xcd * items * splits / 8), w_hi = (int)((int64_t)(xcd + 1) * items * splits / 8);
-  const __amdgpu_buffer_rsrc_t rx = buffer(a.x8, (int64_t)a.cin * a.ld8);
+  const uint64_t x8 = reinterpret_cast<uint64_t>(a.x8);
+  const u32x4 rx = {(uint32_t)x8, (uint32_t)(x8 >> 32), (uint32_t)a.cin * (uint32_t)a.ld8, (uint32_t)kBufferWord3};
 
   for (int work = w_lo + slot; work < w_hi; work += per_xcd) {
     const int item = work / splits, split = work % splits;
@@ -386,28 +429,6 @@ __global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* _
     int lo, hi;
     range_of(a, e, lo, hi);
     const int n0 = (lo & -16) + (tb - (a.starts ? pre[e] : 0)) * NT;
-    auto pick = [&](const uint8_t* val, int64_t bv, int64_t bs, const uint8_t* scale, bool meta) {
-      const uint8_t* p = val + e * bv;
-      int64_t n = bv;
-      if (wave == 2) p = a.meta + e * a.b_meta, n = meta ? a.b_meta : 0;
-      if (wave == 3) p = scale + e * bs, n = bs;
-      return buffer(p, n);
-    };
-    const __amdgpu_buffer_rsrc_t rad = pick(a.val_d, a.b_val_d, a.b_scale_d, a.scale_d, false);
-    const __amdgpu_buffer_rsrc_t ras = pick(a.val_s, a.b_val_s, a.b_scale_s, a.scale_s, true);
-    const __amdgpu_buffer_rsrc_t rid = buffer(a.idx_d + e * a.b_idx_d, a.b_idx_d);
-    const __amdgpu_buffer_rsrc_t ris = buffer(a.idx_s + e * a.b_idx_s, a.b_idx_s);
-    float xs[C::NTB];                              // scales of this lane's tokens
-#pragma unroll
-    for (int j = 0; j < C::NTB; ++j) xs[j] = fp8_scale(a.xs[min(n0 + tok_w + 32 * j + (lane & 31), a.ld8 - 1)]);
-
-    f32x16 acc[2][C::NTB];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int j = 0; j < C::NTB; ++j)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[r][j][q] = 0.f;
 
     // this split's share of the K-blocks, by cost: a dense block one unit, a 2:4 block two
     const int units = a.nkb_d + 2 * a.nkb_s;
@@ -417,52 +438,55 @@ __global__ __launch_bounds__(256, 2) void fp8_prefill_kernel(Fp8Args a, float* _
     // tiles, and the token blocks that the XCDs work on at one time, start their loops at different blocks, so
     // that they do not all read the same rows of X or the same values at once
     auto turn = [&](int n) { return n > 0 ? (int)(((int64_t)t * n / a.n_tiles + (int64_t)((3 * tb) & 7) * n / 8) % n) : 0; };
-    prefill_region<NT, true>(a, xs_a, xs_b, xs_c, aux_a, aux_b, aux_c, rx, rad, rid, t, a.nkb_d, d0, d1 - d0,
-                             turn(d1 - d0), rb, n0, xs, acc);
-    prefill_region<NT, false>(a, xs_a, xs_b, xs_c, aux_a, aux_b, aux_c, rx, ras, ris, t, a.nkb_s, k0, k1 - k0,
-                              turn(k1 - k0), rb, n0, xs, acc);
+    const Work w{a.val_d + e * a.b_val_d, a.val_s + e * a.b_val_s, a.scale_d + e * a.b_scale_d, a.scale_s + e * a.b_scale_s,
+                 a.meta + e * a.b_meta, a.idx_d + e * a.b_idx_d, a.idx_s + e * a.b_idx_s,
+                 t, rb, d0, d1 - d0, turn(d1 - d0), k0, k1 - k0, turn(k1 - k0)};
+    f32x16 acc[2][C::NTB];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[r][j][q] = 0.f;
+    if (w.nd + w.ns > 0) {
+      float xs[C::NTB];                            // scales of this lane's tokens
+#pragma unroll
+      for (int j = 0; j < C::NTB; ++j) xs[j] = fp8_scale(a.xs[min(n0 + tok_w + 32 * j + (lane & 31), a.ld8 - 1)]);
+      multiply_weight<NT>(a, w, lds, rx, n0, xs, acc);
+    }
     __syncthreads();
 
     if (splits > 1) {
       float flat[2 * C::NTB * 16];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < C::NTB; ++j)
-#pragma unroll
-          for (int q = 0; q < 16; ++q) flat[(r * C::NTB + j) * 16 + q] = acc[r][j][q];
+      for (int k = 0; k < 2 * C::NTB * 16; ++k) flat[k] = acc[k / (16 * C::NTB)][k / 16 % C::NTB][k % 16];
       if (!join_splits(flat, part, counters, item, split, splits, &s_last)) continue;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < C::NTB; ++j)
-#pragma unroll
-          for (int q = 0; q < 16; ++q) acc[r][j][q] = flat[(r * C::NTB + j) * 16 + q];
+      for (int k = 0; k < 2 * C::NTB * 16; ++k) acc[k / (16 * C::NTB)][k / 16 % C::NTB][k % 16] = flat[k];
     }
 
-    // Y through LDS, 32 rows in each tile: acc[r][j][q] is row m = 8 (q / 4) + 4 (lane / 32) + q % 4 of half r, token
-    // tok_w + 32 j + lane % 32
-    uint16_t* const ya = reinterpret_cast<uint16_t*>(xs_a);
-    uint16_t* const yb = reinterpret_cast<uint16_t*>(xs_b);
-    static_assert(32 * NT * 2 <= C::TILE, "32 rows of Y fit a tile");
+    // Y through LDS: acc[r][j][q] is row m = 8 (q / 4) + 4 (lane / 32) + q % 4 of half r,
+    // token tok_w + 32 j + lane % 32
+    uint16_t* const ys = reinterpret_cast<uint16_t*>(lds);
+    static_assert(64 * NT * 2 <= kTiles * C::TILE, "64 rows of Y fit the tiles");
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int j = 0; j < C::NTB; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          (r ? yb : ya)[(8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * NT + tok_w + 32 * j + (lane & 31)] = to_bf16(acc[r][j][q]);
+          ys[(32 * r + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3)) * NT + tok_w + 32 * j + (lane & 31)] = to_bf16(acc[r][j][q]);
     __syncthreads();
     // 16-byte stores at 16-byte aligned addresses whatever the row's alignment: piece 0 of a row is what precedes its
     // first aligned address
     const int from = max(lo - n0, 0), to = min(hi - n0, NT);
     constexpr int PIECES = NT / 8 + 1;
-    for (int c = threadIdx.x; c < 64 * PIECES; c += 256) {
+    for (int c = threadIdx.x; c < 64 * PIECES; c += kPreThreads) {
       const int rr = c / PIECES, k = c % PIECES;
       uint16_t* dst = a.y + ((int64_t)t * a.rows + rb * 64 + rr) * a.ldy + n0;
       const int head = (int)(-(uintptr_t)dst / 2 % 8);
       const int at = max(k == 0 ? 0 : head + 8 * (k - 1), from), end = min(k == 0 ? head : head + 8 * k, to);
-      const uint16_t* src = ((rr >> 5) ? yb : ya) + (rr & 31) * NT;
+      const uint16_t* src = ys + rr * NT;
       if (end - at == 8 && at % 8 == 0) {
         *reinterpret_cast<u32x4*>(dst + at) = *reinterpret_cast<const u32x4*>(src + at);
       } else if (end - at == 8) {
@@ -604,8 +628,8 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
     hipLaunchKernelGGL(fp8_colmax_kernel, grid, dim3(256), 0, stream, a, tops);
     hipLaunchKernelGGL(fp8_columns_kernel, grid, dim3(256), 0, stream, a, tops, w.chunks,
                        reinterpret_cast<uint8_t*>(ws + w.x8), reinterpret_cast<uint8_t*>(ws + w.xs));
-    if (nt == 256) hipLaunchKernelGGL(fp8_prefill_kernel<256>, dim3(kMaxWgs), dim3(256), 0, stream, a, part, counters);
-    else hipLaunchKernelGGL(fp8_prefill_kernel<128>, dim3(kMaxWgs), dim3(256), 0, stream, a, part, counters);
+    if (nt == 256) hipLaunchKernelGGL(fp8_prefill_kernel<256>, dim3(kMaxWgs), dim3(kPreThreads), 0, stream, a, part, counters);
+    else hipLaunchKernelGGL(fp8_prefill_kernel<128>, dim3(kMaxWgs), dim3(kPreThreads), 0, stream, a, part, counters);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(HINM_EHIP, "8-bit product launch: %s", hipGetErrorString(e));
   }
