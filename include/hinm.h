@@ -694,9 +694,10 @@ int hinm_spmm_experts_mx4(const hinm_mx4_t* stack, int32_t n_experts, const void
  * is a bf16 value.
  *   weights:     128 kept values of a row = four K-blocks of one region (the
  *                region's last block may have fewer);
- *   activations: one token's column, all channels.  The product gathers
- *                channels in the order of the tile's lists, so a scale of some
- *                channels could not be taken out of its sums; the token's can.
+ *   activations: one token's column, all channels (scales up to 2^120, so that
+ *                none saturates).  The product gathers channels in the order of
+ *                the tile's lists: a scale of some channels could not be taken
+ *                out of its sums; the token's can.
  */
 
 /* Version of the layout described at hinm_fp8_t. */

@@ -11,6 +11,7 @@
 #include "hinm_fp8.h"
 #include "hinm_internal.h"
 #include "hinm_ragged.h"
+#include "hinm_stream.h"
 
 using hinm::fail;
 
@@ -73,12 +74,38 @@ __device__ inline u32x4 load_row8(const uint16_t* row, int n, int n_cols) {
   return v;
 }
 
-// The largest finite magnitude of a column's piece as bf16 bits; bit 15 marks a
-// NaN or an infinity among its values.
-constexpr uint32_t kBad = 0x80008000u;
-__device__ inline uint32_t pk_max(uint32_t m, uint32_t v) {
-  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m), __builtin_bit_cast(u16x2, v)));
+// Two bf16 magnitudes held as signed 16-bit numbers, 0x80 above their bits: what
+// is not finite is negative then and loses to every other.
+constexpr uint32_t kLeast = 0x00800080u;
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t larger2(uint32_t m, uint32_t v) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(i16x2, m), __builtin_bit_cast(i16x2, v)));
+}
+__device__ inline uint32_t larger(uint32_t m, uint32_t v) {        // v: two bf16 values
+  const i16x2 w = __builtin_bit_cast(i16x2, v & 0x7fff7fffu) + i16x2{0x80, 0x80};
+  return larger2(m, __builtin_bit_cast(uint32_t, w));
+}
+template <int CTRL>
+__device__ inline uint32_t moved(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp((int)kLeast, (int)v, CTRL, 0xf, 0xf, false); }
+
+// A token's scale byte from the largest magnitude as held above.  Up to 2^120: no
+// activation saturates.
+__device__ inline uint32_t column_scale(uint32_t held) {
+  const uint32_t top = held - 0x80u;
+  const int e = (int)(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+  return (uint32_t)max(e, 3);
+}
+
+// Eight values as codes; the conversion makes NaN of what is not finite.
+__device__ inline fp8_u32x2 column_codes(u32x4 v, const float (&inv)[8]) {
+  fp8_u32x2 c = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float lo = __uint_as_float(v[k] << 16) * inv[2 * k], hi = __uint_as_float(v[k] & 0xffff0000u) * inv[2 * k + 1];
+    c[k >> 1] = (k & 1) ? (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)c[k >> 1], true)
+                        : (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)c[k >> 1], false);
+  }
+  return c;
 }
 
 // Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece, four
@@ -88,8 +115,8 @@ __global__ __launch_bounds__(256) void fp8_colmax_kernel(Fp8Args a, uint16_t* __
   constexpr int U = 4;
   const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
-  u32x4 m = {0u, 0u, 0u, 0u};
-  if (n < a.n_cols && r0 < r1) {
+  u32x4 m = {kLeast, kLeast, kLeast, kLeast};
+  if (n < a.n_cols)
     for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * U) {
       u32x4 v[U];
 #pragma unroll
@@ -97,75 +124,43 @@ __global__ __launch_bounds__(256) void fp8_colmax_kernel(Fp8Args a, uint16_t* __
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = pk_max(m[k], v[u][k] & 0x7fff7fffu);
+        for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
     }
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) bad |= (m[k] & 0xffffu) >= 0x7f80u || m[k] >= 0x7f800000u;
-    if (bad) {                                 // again, without what is not finite
-      const u32x4 all = m;
-      m = u32x4{0u, 0u, 0u, 0u};
-      for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
-        const u32x4 v = load_row8(a.x + r * a.ldx, n, a.n_cols);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = fp8_max_finite(m[k], v[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        m[k] |= ((all[k] & 0xffffu) >= 0x7f80u ? 0x8000u : 0u) | (all[k] >= 0x7f800000u ? 0x80000000u : 0u);
-    }
-  }
   sh[threadIdx.x] = m;
   __syncthreads();
   if (threadIdx.x < 32 && n < a.n_cols) {
-    u32x4 flags = m & kBad, top = m & ~kBad;
     for (int k = 1; k < 8; ++k)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t v = sh[32 * k + threadIdx.x][u];
-        flags[u] |= v & kBad;
-        top[u] = pk_max(top[u], v & ~kBad);
-      }
-    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = flags | top;
+      for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], sh[32 * k + threadIdx.x][u]);
+    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = m;
   }
 }
 
 __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint16_t* __restrict__ part, int chunks,
                                                           uint8_t* __restrict__ x8, uint8_t* __restrict__ xs) {
-  __shared__ u32x4 sh[2][256];
+  __shared__ u32x4 sh[256];
   constexpr int U = 4;
   const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
-  u32x4 flags = {0u, 0u, 0u, 0u}, top = {0u, 0u, 0u, 0u};
-  if (n < a.n_cols) {
+  u32x4 m = {kLeast, kLeast, kLeast, kLeast};
+  if (n < a.n_cols)
 #pragma unroll 4
     for (int k = threadIdx.x >> 5; k < chunks; k += 8) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(part + (int64_t)k * a.ld8 + n);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        flags[u] |= v[u] & kBad;
-        top[u] = pk_max(top[u], v[u] & ~kBad);
-      }
+      for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], v[u]);
     }
-  }
-  sh[0][threadIdx.x] = top;
-  sh[1][threadIdx.x] = flags;
+  sh[threadIdx.x] = m;
   __syncthreads();
   for (int k = 0; k < 8; ++k)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      top[u] = pk_max(top[u], sh[0][32 * k + c8][u]);
-      flags[u] |= sh[1][32 * k + c8][u];
-    }
+    for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], sh[32 * k + c8][u]);
   uint32_t e[8];
   float inv[8];
-  bool plain = true;                           // every value of the eight columns is finite and below the saturation
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const uint32_t t = (top[u >> 1] >> (16 * (u & 1))) & 0xffffu;
-    e[u] = fp8_scale_of(t);
+    e[u] = column_scale((m[u >> 1] >> (16 * (u & 1))) & 0xffffu);
     inv[u] = fp8_inverse(e[u]);
-    plain &= e[u] < 246u && !((flags[u >> 1] >> (16 * (u & 1))) & 0x8000u);
   }
   if (n >= a.ld8) return;
   if (blockIdx.y == 0 && threadIdx.x < 32)
@@ -176,21 +171,8 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
     for (int u = 0; u < U; ++u)
       v[u] = n < a.n_cols ? load_row8(a.x + (int64_t)min(r + 8 * u, r1 - 1) * a.ldx, n, a.n_cols) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      fp8_u32x2 c = {0u, 0u};
-      if (plain) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float lo = __uint_as_float(v[u][k] << 16) * inv[2 * k], hi = __uint_as_float(v[u][k] & 0xffff0000u) * inv[2 * k + 1];
-          c[k >> 1] = (k & 1) ? (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)c[k >> 1], true)
-                              : (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, (int)c[k >> 1], false);
-        }
-      } else {
-        c[0] = fp8_codes<true>(fp8_codes<false>(0u, v[u][0], inv[0], inv[1]), v[u][1], inv[2], inv[3]);
-        c[1] = fp8_codes<true>(fp8_codes<false>(0u, v[u][2], inv[4], inv[5]), v[u][3], inv[6], inv[7]);
-      }
-      if (r + 8 * u < r1) *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)(r + 8 * u) * a.ld8 + n) = c;
-    }
+    for (int u = 0; u < U; ++u)
+      if (r + 8 * u < r1) *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)(r + 8 * u) * a.ld8 + n) = column_codes(v[u], inv);
   }
 }
 
@@ -502,6 +484,235 @@ __global__ __launch_bounds__(kPreThreads, 2) void fp8_prefill_kernel(Fp8Args a, 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few tokens an expert: a read of the packed weight, one launch.  The codes of a
+// segment's tokens (up to 16 of an expert) are held in LDS whole, [channel]
+// [token], rounded there by every workgroup for itself; the transposed LDS read
+// takes an address a lane, so the channels that a tile keeps are gathered there
+// and every global load is at an address known beforehand.  An item is 16 F
+// rows of a segment; a workgroup takes a contiguous range of items, its waves
+// deal the K-blocks among themselves, and their sums meet in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kDecThreads = 512, kDecWaves = kDecThreads / 64;
+constexpr int kDecSlab = 147 * 1024;               // bytes of LDS for the codes and a row of zeros
+
+template <int F>
+struct DecOperand {
+  fp8_u32x2 v[F];
+  uint32_t m[F], scale[F];
+  int index;
+};
+
+struct DecSource {
+  const uint8_t *val_d, *val_s, *meta, *idx_d, *idx_s, *scale_d, *scale_s;
+  int tile, row, first, end;
+};
+
+// Eight of X's values from element `from` on, of which the first is wanted at
+// `from + past`.
+__device__ inline u32x4 shifted_row(u32x4 v, int past) {
+  if (past & 4) v[0] = v[2], v[1] = v[3];
+  if (past & 2) v[0] = v[1], v[1] = v[2], v[2] = v[3];
+  if (past & 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = v[k] >> 16 | (k < 3 ? v[k + 1] << 16 : 0u);
+  return v;
+}
+
+// The codes of columns n0 .. n0 + width - 1 (8 or 16; what lies past the last
+// column is some other column's, which nothing reads) into the slab, the scale
+// bytes into `scales`.  X is read twice, the second time from L2: once for the
+// largest magnitudes, once to round.  A thread takes chunks of eight elements,
+// kHeld at a time: eight columns of a channel - at width 16 the waves of the
+// upper half the upper eight, so that a wave's maxima and scales are scalars -
+// or, where X is one column without padding (`flat`), eight channels.
+constexpr int kHeld = 8;
+__device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int width, bool flat, uint8_t* slab, uint32_t* red,
+                                           uint8_t* scales) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int group = kDecThreads * 8 / width, half = (int)threadIdx.x >= group;   // threads of a set of eight columns
+  const int first = threadIdx.x - half * group, chunks = flat ? (a.cin + 7) / 8 : a.cin;
+  const int64_t end = (int64_t)(a.cin - 1) * a.ldx + a.n_cols;       // elements of X: eight or more
+  auto load = [&](int q) {
+    const int64_t at = flat ? (int64_t)min(q, chunks - 1) * 8 : (int64_t)min(q, chunks - 1) * a.ldx + n0 + 8 * half;
+    const int64_t from = min(at, end - 8);
+    return shifted_row(*reinterpret_cast<const any_u32x4*>(a.x + from), (int)min(at - from, (int64_t)7));
+  };
+  u32x4 m = {kLeast, kLeast, kLeast, kLeast};
+#pragma nounroll
+  for (int q = first; q < chunks; q += kHeld * group) {
+    u32x4 v[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) v[u] = load(q + u * group);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
+  }
+  // over the wave, then over the waves of the half
+  uint32_t top[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r = m[k];
+    r = larger2(r, moved<0x111>(r));
+    r = larger2(r, moved<0x112>(r));
+    r = larger2(r, moved<0x114>(r));
+    r = larger2(r, moved<0x118>(r));
+    r = larger2(r, moved<0x142>(r));
+    r = larger2(r, moved<0x143>(r));
+    top[k] = (uint32_t)__builtin_amdgcn_readlane((int)r, 63);
+  }
+  if (lane == 0) *reinterpret_cast<u32x4*>(red + 4 * wave) = u32x4{top[0], top[1], top[2], top[3]};
+  __syncthreads();
+  uint32_t r = red[lane & 31];                     // wave lane / 4, dword lane % 4
+  if (width == 16 && ((lane >> 4) & 1) != half) r = kLeast;
+  r = larger2(r, (uint32_t)__shfl_xor((int)r, 4));
+  r = larger2(r, (uint32_t)__shfl_xor((int)r, 8));
+  r = larger2(r, (uint32_t)__shfl_xor((int)r, 16));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top[k] = (uint32_t)__builtin_amdgcn_readlane((int)r, k);
+  if (flat) {                                      // one column
+    uint32_t t = larger2(larger2(top[0], top[1]), larger2(top[2], top[3]));
+    t = max(t & 0xffffu, t >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = t | t << 16;
+  }
+  float inv[8];
+  uint32_t e[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    e[u] = column_scale((top[u >> 1] >> (16 * (u & 1))) & 0xffffu);
+    inv[u] = fp8_inverse(e[u]);
+  }
+  if (first == 0)
+    *reinterpret_cast<fp8_u32x2*>(scales + 8 * half) =
+        fp8_u32x2{e[0] | e[1] << 8 | e[2] << 16 | e[3] << 24, e[4] | e[5] << 8 | e[6] << 16 | e[7] << 24};
+#pragma nounroll
+  for (int q = first; q < chunks; q += kHeld * group) {
+    u32x4 v[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) v[u] = load(q + u * group);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int c = q + u * group;
+      if (c >= chunks) break;
+      const fp8_u32x2 code = column_codes(v[u], inv);
+      if (!flat) {
+        *reinterpret_cast<fp8_u32x2*>(slab + c * width + 8 * half) = code;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (8 * c + k < a.cin) slab[(8 * c + k) * 8] = (uint8_t)(code[k >> 2] >> (8 * (k & 3)));
+      }
+    }
+  }
+  if (first == 0) *reinterpret_cast<fp8_u32x2*>(slab + a.cin * width + 8 * half) = fp8_u32x2{0u, 0u};
+}
+
+// Width: columns of a segment, 8 or 16.  Every instruction of the prologue is
+// issued by every wave, and a compute unit's waves share its issue slots: of 4,
+// 8 and 16 waves, 8 (with 16 a single token took 26 us).
+template <int F>
+__global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int width) {
+  constexpr int kDepth = 4;
+  __shared__ __attribute__((aligned(16))) uint8_t slab[kDecSlab];
+  __shared__ union {
+    float red[kDecWaves * kRed];
+    uint32_t top[kDecWaves * 4];
+  } sh;
+  __shared__ int pre[HINM_MAX_EXPERTS + 1];
+  __shared__ uint8_t scales[16];
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
+  const int nd = a.nkb_d, ns = a.nkb_s, nblk = nd + ns, n_rb = a.cout / (16 * F);
+  const int64_t all = (int64_t)plan_blocks(a, width, pre) * n_rb;
+  const int64_t i0 = blockIdx.x * all / gridDim.x;
+  const int items = (int)((blockIdx.x + 1) * all / gridDim.x - i0);
+  int held = -1, n0 = 0, hi = 0, rb = 0;
+  float xs = 1.f;
+  f32x4 acc[F];
+  // where an item lies: segment and row block
+  auto seg_of = [&](int i) { return (int)((i0 + i) / n_rb); };
+  const int pitch = width;
+  const bool flat = !a.starts && a.ldx == 1;       // one column
+  stream<DecOperand<F>, DecSource, kDepth, kDecWaves>(
+      items,
+      [&](int i) -> DecSource {
+        const int sg = seg_of(i), e = find_expert(a, pre, sg), r16 = (int)(i0 + i - (int64_t)sg * n_rb) * F;
+        const int t = r16 * 16 / a.rows;
+        return {a.val_d + e * a.b_val_d, a.val_s + e * a.b_val_s, a.meta + e * a.b_meta, a.idx_d + e * a.b_idx_d,
+                a.idx_s + e * a.b_idx_s, a.scale_d + e * a.b_scale_d, a.scale_s + e * a.b_scale_s,
+                t, r16 * 16 - t * a.rows, wave, nblk};
+      },
+      [&](const DecSource& s, int b, DecOperand<F>& o) {
+        const bool dense = b < nd;
+        const int k = dense ? b : b - nd, nkb = dense ? nd : ns;
+        const int64_t kb = (int64_t)s.tile * nkb + k, row = kb * a.rows + s.row;
+        o.index = at<int>(pick(dense, s.idx_d, s.idx_s) + kb * (dense ? 128 : 256), dense ? 4 * (lane & 31) : 4 * lane);
+        const uint8_t* val = pick(dense, s.val_d, s.val_s) + row * 32;
+        const uint8_t* meta = pick(dense, val, s.meta + row * 8);  // a dense block has none and reads its values' bytes
+        const uint8_t* scale = pick(dense, s.scale_d, s.scale_s) + ((int64_t)s.tile * ((nkb + 3) / 4) + k / 4) * a.rows + s.row;
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          o.v[f] = at<fp8_u32x2>(val, 32 * i16 + 8 * kc + 512 * f);
+          o.scale[f] = at<uint8_t>(scale, 16 * f + i16);
+          o.m[f] = at<uint16_t>(meta, 8 * i16 + 2 * kc + 128 * f);
+        }
+      },
+      [&](int b, const DecOperand<F>& o) {
+        // the lane's share of the transposed reads: eight tokens of position 8 kc + i16 / 2, and 32 further on (past a
+        // row of eight the same ones again: columns that nothing reads)
+        const int s8 = 8 * min(i16 & 1, pitch / 8 - 1), p = 8 * kc + (i16 >> 1);
+        const bool dense = b < nd;
+        const int row = ((uint32_t)o.index < (uint32_t)a.cin ? o.index : a.cin) * pitch;
+        fp8_u32x2 raw[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int pos = p + 32 * u;
+          // a dense block is multiplied as a 2:4 block whose groups keep positions 0 and 1: column 2 q + u at 4 q + u
+          raw[u] = tr_read8(slab + __shfl(row, dense ? 2 * (pos >> 2) + (pos & 1) : pos) + s8);
+        }
+        const bf16x8 lo8 = __builtin_bit_cast(bf16x8, fp8_expand(raw[0], xs)), hi8 = __builtin_bit_cast(bf16x8, fp8_expand(raw[1], xs));
+        const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const bf16x8 av = __builtin_bit_cast(bf16x8, fp8_expand(o.v[f], fp8_scale(o.scale[f])));
+          acc[f] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av, bv, acc[f], dense ? 0x4444 : (int)o.m[f], 0, 0);
+        }
+      },
+      [&](int i) {
+        const int sg = seg_of(i);
+        rb = (int)(i0 + i - (int64_t)sg * n_rb);
+        if (sg != held) {
+          const int e = find_expert(a, pre, sg);
+          int lo;
+          range_of(a, e, lo, hi);
+          n0 = lo + (sg - (a.starts ? pre[e] : 0)) * width;
+          __syncthreads();
+          load_codes(a, n0, width, flat, slab, sh.top, scales);
+          __syncthreads();
+          xs = fp8_scale(scales[i16 & (width - 1)]);
+          held = sg;
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+      },
+      [&](int) {
+        // 256 / width rows a round: 16 or 32
+#pragma nounroll
+        for (int r0 = 0; r0 < 16 * F; r0 += 256 / width) {
+          put_sums<F>(sh.red, acc, r0, width);
+          __syncthreads();
+          // element threadIdx.x / 2, waves 4 (threadIdx.x % 2) .. + 3
+          const float* q = sh.red + (threadIdx.x & 1) * 4 * kRed + (threadIdx.x >> 1);
+          float s = (q[0] + q[kRed]) + (q[2 * kRed] + q[3 * kRed]);
+          s += quad1(s);
+          const int e = threadIdx.x >> 1, row = r0 + e / width, n = n0 + e % width;
+          if ((threadIdx.x & 1) == 0 && n < hi && row < 16 * F) a.y[((int64_t)rb * 16 * F + row) * a.ldy + n] = to_bf16(s);
+          __syncthreads();
+        }
+      });
+}
+
 int check_cols(int64_t n_cols) {
   if (n_cols < 0) return fail(HINM_ESHAPE, "%lld columns", (long long)n_cols);
   if (n_cols > (1 << 24)) return fail(HINM_ESHAPE, "%lld columns exceed 2^24", (long long)n_cols);
@@ -536,7 +747,18 @@ int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   return avg <= 64 || (avg > 110 && avg <= 170) ? 128 : 256;
 }
 
-// Workspace: arrival counters and the partial sums of kMaxWgs workgroups, where
+// Columns of a decode segment, 8 or 16, or 0 where the many-token kernel is
+// taken: as many as an expert has on average and as fit in LDS, in up to two
+// segments.
+int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols, int64_t ldx) {
+  const int64_t avg = (n_cols + n_experts - 1) / n_experts;
+  const int fit = (int64_t)(p.cin + 1) * 16 <= kDecSlab ? 16 : (int64_t)(p.cin + 1) * 8 <= kDecSlab ? 8 : 0;
+  if (fit == 0 || (int64_t)(p.cin - 1) * ldx + n_cols < 8 || p.n_dense + p.n_24 == 0) return 0;
+  const int width = avg <= 8 ? 8 : fit;
+  return avg <= 2 * width ? width : 0;
+}
+
+// Workspace: none for few tokens.  Arrival counters and the partial sums of kMaxWgs workgroups, where
 // a launch may split; then the rounded activations of one window of columns (at
 // most 2^30 bytes, a multiple of 256 columns), their scales and the pieces'
 // largest magnitudes.
@@ -547,7 +769,7 @@ struct Workspace {
 };
 Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   Workspace w{};
-  if (n_cols == 0) return w;
+  if (n_cols == 0 || decode_width(p, n_experts, n_cols, n_cols)) return w;
   w.window = std::min(n_cols, std::max<int64_t>(256, ((int64_t)1 << 30) / p.cin / 256 * 256));
   w.ld8 = w.window <= 128 ? 128 : ((w.window + 255) / 256 | 1) * 256;
   w.chunks = (int)std::min<int64_t>(kChunks, (p.cin + 63) / 64);
@@ -576,9 +798,9 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
     if (!hinm::aligned(b.ptr, 16)) return fail(HINM_EALIGN, "%s is not 16-byte aligned", b.name);
   }
   const Workspace w = workspace_of(p, n_experts, n_cols);
-  if (!workspace || workspace_bytes < (size_t)w.bytes)
+  if (w.bytes > 0 && (!workspace || workspace_bytes < (size_t)w.bytes))
     return fail(HINM_EWORKSPACE, "workspace of %zu bytes given, %lld needed", workspace_bytes, (long long)w.bytes);
-  if (!hinm::aligned(workspace, 256)) return fail(HINM_EALIGN, "workspace is not 256-byte aligned");
+  if (w.bytes > 0 && !hinm::aligned(workspace, 256)) return fail(HINM_EALIGN, "workspace is not 256-byte aligned");
   st = hinm::ensure_device();
   if (st) return st;
   char* const ws = static_cast<char*>(workspace);
@@ -615,6 +837,21 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
   a.rows = p.tile_rows;
   a.n_tiles = p.n_tiles;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
+  if (const int width = decode_width(p, n_experts, n_cols, n_cols)) {
+    a.n_cols = (int)n_cols;
+    a.x = static_cast<const uint16_t*>(x);
+    a.y = static_cast<uint16_t*>(y);
+    // rows an item: those that leave the busiest of 256 workgroups the least to do, an item costing half a fragment
+    // more than its rows
+    const int64_t segs = n_experts == 1 ? (n_cols + width - 1) / width : std::min<int64_t>(n_experts, n_cols);
+    auto cost = [&](int f) { return ((segs * (p.cout / (16 * f)) + kCus - 1) / kCus) * (2 * f + 1); };
+    const int f = cost(1) < cost(2) && cost(1) < cost(4) ? 1 : cost(2) < cost(4) ? 2 : 4;
+    if (f == 4) hipLaunchKernelGGL(fp8_decode_kernel<4>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
+    else if (f == 2) hipLaunchKernelGGL(fp8_decode_kernel<2>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
+    else hipLaunchKernelGGL(fp8_decode_kernel<1>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? HINM_OK : fail(HINM_EHIP, "8-bit product launch: %s", hipGetErrorString(e));
+  }
   uint16_t* const tops = reinterpret_cast<uint16_t*>(ws + w.part);
   float* const part = reinterpret_cast<float*>(ws + hinm::kWsCounterBytes);
   unsigned* const counters = reinterpret_cast<unsigned*>(ws);

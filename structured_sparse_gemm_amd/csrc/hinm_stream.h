@@ -12,6 +12,10 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 template <class T>
 __device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpret_cast<const T*>(base + offset); }
 
+// a or b, both evaluated: a choice between two members in place would become
+// one between their addresses, and put the struct on the stack.
+__device__ inline const uint8_t* pick(bool c, const uint8_t* a, const uint8_t* b) { return c ? a : b; }
+
 // While DEPTH of a wave's blocks are multiplied the next DEPTH blocks' operands
 // are on their way, across the items' ends too.  For item i:
 //   open(i)       names the wave's blocks, first, first + NW, ... below end, and
@@ -26,7 +30,7 @@ __device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpr
 // launch fetches every instruction from memory once, at some 2 cycles a byte,
 // and the kernels that use this last only a few times as long.
 template <class Operand, class Source, int DEPTH, int NW, class Open, class Load, class Multiply, class Begin, class Finish>
-__device__ inline void stream(int items, Open open, Load load, Multiply multiply, Begin begin, Finish finish) {
+__device__ __forceinline__ void stream(int items, Open open, Load load, Multiply multiply, Begin begin, Finish finish) {
   if (items <= 0) return;
   Operand o[DEPTH];
   int block[DEPTH];                // the operands' blocks; -1: none

@@ -21,12 +21,12 @@ E4M3 = e4m3_table()
 GRID = E4M3[:127]
 
 
-def scale_byte(top: float) -> int:
-    """The smallest E8M0 byte of 3 .. 246 at which top does not exceed 448."""
-    for e in range(3, 247):
+def scale_byte(top: float, last: int = 246) -> int:
+    """The smallest E8M0 byte of 3 .. last at which top does not exceed 448."""
+    for e in range(3, last + 1):
         if top <= 448.0 * 2.0 ** (e - 127):
             return e
-    return 246
+    return last
 
 
 def round_codes(v: np.ndarray, e: int):
@@ -69,7 +69,7 @@ def columns(x: np.ndarray) -> np.ndarray:
     """Activations [channels, tokens] as the values that their codes stand for, one scale a token."""
     out = np.zeros(x.shape)
     for n in range(x.shape[1]):
-        out[:, n] = round_codes(x[:, n], scale_byte(finite_top(x[:, n])))[1]
+        out[:, n] = round_codes(x[:, n], scale_byte(finite_top(x[:, n]), 247))[1]
     return out
 
 
