@@ -221,8 +221,6 @@ __device__ inline void lds_load(u32x4 buffer, uint32_t lds, uint32_t offset) {
 __device__ inline void lds_load(const uint8_t* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(src) : "memory");
 }
-// A barrier that waits for this wave's LDS operations, not for its loads.
-__device__ inline void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // An item: row block rb of tile t of an expert, blocks d0 .. d0 + nd - 1 of its
 // dense region and k0 .. k0 + ns - 1 of its 2:4 region, each region from its
@@ -494,7 +492,9 @@ __global__ __launch_bounds__(kPreThreads, 2) void fp8_prefill_kernel(Fp8Args a, 
 // deal the K-blocks among themselves, and their sums meet in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kDecThreads = 512, kDecWaves = kDecThreads / 64;
-constexpr int kDecSlab = 147 * 1024;               // bytes of LDS for the codes and a row of zeros
+constexpr int kDecLds = 159488;      // bytes for the codes, a row of zeros and the waves' sums
+constexpr int dec_red_bytes(int f) { return kDecWaves * (256 * f + 8) * 4; }   // the 8: reads free of bank conflicts
+constexpr bool dec_fits(int64_t cin, int width, int f) { return (cin + 1) * width + dec_red_bytes(f) <= kDecLds; }
 
 template <int F>
 struct DecOperand {
@@ -519,64 +519,75 @@ __device__ inline u32x4 shifted_row(u32x4 v, int past) {
   return v;
 }
 
-// The codes of columns n0 .. n0 + width - 1 (8 or 16; what lies past the last
-// column is some other column's, which nothing reads) into the slab, the scale
-// bytes into `scales`.  X is read twice, the second time from L2: once for the
-// largest magnitudes, once to round.  A thread takes chunks of eight elements,
-// kHeld at a time: eight columns of a channel - at width 16 the waves of the
-// upper half the upper eight, so that a wave's maxima and scales are scalars -
-// or, where X is one column without padding (`flat`), eight channels.
-constexpr int kHeld = 8;
-__device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int width, bool flat, uint8_t* slab, uint32_t* red,
-                                           uint8_t* scales) {
+// Eight columns' largest magnitudes over the workgroup's threads (two sets of
+// them where `halves`), from each thread's.
+__device__ __forceinline__ u32x4 workgroup_max(u32x4 m, bool halves, int half, uint32_t* red) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int group = kDecThreads * 8 / width, half = (int)threadIdx.x >= group;   // threads of a set of eight columns
-  const int first = threadIdx.x - half * group, chunks = flat ? (a.cin + 7) / 8 : a.cin;
-  const int64_t end = (int64_t)(a.cin - 1) * a.ldx + a.n_cols;       // elements of X: eight or more
-  auto load = [&](int q) {
-    const int64_t at = flat ? (int64_t)min(q, chunks - 1) * 8 : (int64_t)min(q, chunks - 1) * a.ldx + n0 + 8 * half;
-    const int64_t from = min(at, end - 8);
-    return shifted_row(*reinterpret_cast<const any_u32x4*>(a.x + from), (int)min(at - from, (int64_t)7));
-  };
-  u32x4 m = {kLeast, kLeast, kLeast, kLeast};
-#pragma nounroll
-  for (int q = first; q < chunks; q += kHeld * group) {
-    u32x4 v[kHeld];
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u) v[u] = load(q + u * group);
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
-  }
-  // over the wave, then over the waves of the half
-  uint32_t top[4];
+  u32x4 top;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t r = m[k];
-    r = larger2(r, moved<0x111>(r));
+    r = larger2(r, moved<0x111>(r));               // within 16 lanes: by 1, 2, 4, 8
     r = larger2(r, moved<0x112>(r));
     r = larger2(r, moved<0x114>(r));
     r = larger2(r, moved<0x118>(r));
-    r = larger2(r, moved<0x142>(r));
+    r = larger2(r, moved<0x142>(r));               // lane 15 of 16 to the next 16, lane 31 to the upper 32
     r = larger2(r, moved<0x143>(r));
     top[k] = (uint32_t)__builtin_amdgcn_readlane((int)r, 63);
   }
-  if (lane == 0) *reinterpret_cast<u32x4*>(red + 4 * wave) = u32x4{top[0], top[1], top[2], top[3]};
-  __syncthreads();
+  if (lane == 0) *reinterpret_cast<u32x4*>(red + 4 * wave) = top;
+  step_barrier();
   uint32_t r = red[lane & 31];                     // wave lane / 4, dword lane % 4
-  if (width == 16 && ((lane >> 4) & 1) != half) r = kLeast;
+  if (halves && ((lane >> 4) & 1) != half) r = kLeast;
   r = larger2(r, (uint32_t)__shfl_xor((int)r, 4));
   r = larger2(r, (uint32_t)__shfl_xor((int)r, 8));
   r = larger2(r, (uint32_t)__shfl_xor((int)r, 16));
 #pragma unroll
   for (int k = 0; k < 4; ++k) top[k] = (uint32_t)__builtin_amdgcn_readlane((int)r, k);
-  if (flat) {                                      // one column
-    uint32_t t = larger2(larger2(top[0], top[1]), larger2(top[2], top[3]));
-    t = max(t & 0xffffu, t >> 16);
+  return top;
+}
+
+// The codes of a segment of `width` columns, eight from n0 and, at width 16,
+// eight from n1 on, into the slab, the scale bytes into `scales`.  A thread
+// takes eight columns of a channel at a time - at width 16 the waves of the
+// upper half the upper eight, so that a wave's maxima and scales are scalars -
+// kHeld channels in flight.  X is read for its largest magnitudes and, but for
+// the first kHeld channels a thread, which stay in registers, again from L2.
+// Of fewer than eight columns a row's load reaches into the next rows, whose
+// codes nothing uses, and the last rows' begins early and is shifted.
+constexpr int kHeld = 8;
+__device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int n1, int width, uint8_t* slab, uint32_t* red,
+                                           uint8_t* scales) {
+  const int group = kDecThreads * 8 / width, half = uniform((int)threadIdx.x >= group);
+  const int first = threadIdx.x - half * group, passes = (a.cin + kHeld * group - 1) / (kHeld * group);
+  const uint16_t* const x = a.x + (half ? n1 : n0);
+  const uint32_t ldx = (uint32_t)a.ldx;
+  const bool few = a.n_cols < 8;
+  const int64_t last = (int64_t)(a.cin - 1) * a.ldx + a.n_cols - 8;   // of few columns: where the last load begins
+  u32x4 v[kHeld];
+  auto load = [&](int pass) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top[k] = t | t << 16;
+    for (int u = 0; u < kHeld; ++u) {
+      const uint64_t at = (uint64_t)(uint32_t)min(first + (pass * kHeld + u) * group, a.cin - 1) * ldx;
+      v[u] = *reinterpret_cast<const any_u32x4*>(x + (few ? min((int64_t)at, last) : (int64_t)at));
+    }
+    if (few)
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const uint64_t at = (uint64_t)(uint32_t)min(first + (pass * kHeld + u) * group, a.cin - 1) * ldx;
+        v[u] = shifted_row(v[u], (int)max((int64_t)at - last, (int64_t)0));
+      }
+  };
+  u32x4 m = {kLeast, kLeast, kLeast, kLeast};
+#pragma nounroll
+  for (int pass = passes - 1; pass >= 0; --pass) {
+    load(pass);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
   }
+  const u32x4 top = workgroup_max(m, width == 16, half, red);
   float inv[8];
   uint32_t e[8];
 #pragma unroll
@@ -584,29 +595,58 @@ __device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int width, 
     e[u] = column_scale((top[u >> 1] >> (16 * (u & 1))) & 0xffffu);
     inv[u] = fp8_inverse(e[u]);
   }
-  if (first == 0)
+  if (first == 0) {
     *reinterpret_cast<fp8_u32x2*>(scales + 8 * half) =
         fp8_u32x2{e[0] | e[1] << 8 | e[2] << 16 | e[3] << 24, e[4] | e[5] << 8 | e[6] << 16 | e[7] << 24};
+    *reinterpret_cast<fp8_u32x2*>(slab + a.cin * width + 8 * half) = fp8_u32x2{0u, 0u};
+  }
 #pragma nounroll
-  for (int q = first; q < chunks; q += kHeld * group) {
-    u32x4 v[kHeld];
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u) v[u] = load(q + u * group);
+  for (int pass = 0;;) {
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const int c = q + u * group;
-      if (c >= chunks) break;
-      const fp8_u32x2 code = column_codes(v[u], inv);
-      if (!flat) {
-        *reinterpret_cast<fp8_u32x2*>(slab + c * width + 8 * half) = code;
-      } else {
+      const int c = first + (pass * kHeld + u) * group;
+      if (c < a.cin) *reinterpret_cast<fp8_u32x2*>(slab + c * width + 8 * half) = column_codes(v[u], inv);
+    }
+    if (++pass == passes) break;
+    load(pass);
+  }
+}
+
+// The same for one column without padding, which eight channels a load cover
+// and registers hold.
+__device__ __forceinline__ void load_token(const Fp8Args& a, uint8_t* slab, uint32_t* red, uint8_t* scales) {
+  constexpr int kChunks8 = (kDecLds / 8 + 8 * kDecThreads - 1) / (8 * kDecThreads);
+  u32x4 v[kChunks8], m = {kLeast, kLeast, kLeast, kLeast};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (8 * c + k < a.cin) slab[(8 * c + k) * 8] = (uint8_t)(code[k >> 2] >> (8 * (k & 3)));
-      }
+  for (int u = 0; u < kChunks8; ++u) {
+    const int c = 8 * (threadIdx.x + u * kDecThreads), from = min(c, a.cin - 8);
+    v[u] = shifted_row(*reinterpret_cast<const any_u32x4*>(a.x + from), min(c - from, 7));
+  }
+#pragma unroll
+  for (int u = 0; u < kChunks8; ++u)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
+  const u32x4 top = workgroup_max(m, false, 0, red);
+  uint32_t t = larger2(larger2(top[0], top[1]), larger2(top[2], top[3]));
+  t = max(t & 0xffffu, t >> 16);
+  const uint32_t e = column_scale(t);
+  const float i1 = fp8_inverse(e), inv[8] = {i1, i1, i1, i1, i1, i1, i1, i1};
+  if (threadIdx.x == 0) {
+    scales[0] = (uint8_t)e;
+    *reinterpret_cast<fp8_u32x2*>(slab + a.cin * 8) = fp8_u32x2{0u, 0u};
+  }
+#pragma unroll
+  for (int u = 0; u < kChunks8; ++u) {
+    const int c = 8 * (threadIdx.x + u * kDecThreads);
+    if (c >= a.cin) break;
+    const uint64_t code = __builtin_bit_cast(uint64_t, column_codes(v[u], inv));
+    const int turn = threadIdx.x >> 2;             // lanes that share banks begin at other channels
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = (k + turn) & 7;
+      if (c + j < a.cin) slab[(c + j) * 8] = (uint8_t)(code >> (8 * j));
     }
   }
-  if (first == 0) *reinterpret_cast<fp8_u32x2*>(slab + a.cin * width + 8 * half) = fp8_u32x2{0u, 0u};
 }
 
 // Width: columns of a segment, 8 or 16.  Every instruction of the prologue is
@@ -614,56 +654,54 @@ __device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int width, 
 // 8 and 16 waves, 8 (with 16 a single token took 26 us).
 template <int F>
 __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int width) {
-  constexpr int kDepth = 4;
-  __shared__ __attribute__((aligned(16))) uint8_t slab[kDecSlab];
-  __shared__ union {
-    float red[kDecWaves * kRed];
-    uint32_t top[kDecWaves * 4];
-  } sh;
+  constexpr int kDepth = F == 1 ? 8 : F == 2 ? 6 : 4;
+  __shared__ __attribute__((aligned(16))) uint8_t slab[kDecLds];
+  __shared__ __attribute__((aligned(16))) uint32_t top[kDecWaves * 4];
   __shared__ int pre[HINM_MAX_EXPERTS + 1];
-  __shared__ uint8_t scales[16];
+  __shared__ __attribute__((aligned(8))) uint8_t scales[16];
+  float* const red = reinterpret_cast<float*>(slab + (kDecLds - dec_red_bytes(F)));
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
-  const int nd = a.nkb_d, ns = a.nkb_s, nblk = nd + ns, n_rb = a.cout / (16 * F);
-  const int64_t all = (int64_t)plan_blocks(a, width, pre) * n_rb;
-  const int64_t i0 = blockIdx.x * all / gridDim.x;
-  const int items = (int)((blockIdx.x + 1) * all / gridDim.x - i0);
-  int held = -1, n0 = 0, hi = 0, rb = 0;
+  const int nd = a.nkb_d, ns = a.nkb_s, nblk = nd + ns;
+  const unsigned n_rb = a.cout / (16 * F), all = plan_blocks(a, width, pre) * n_rb;
+  // this workgroup's share of all items
+  auto share = [&](unsigned b) { return all / kCus * b + all % kCus * b / kCus; };
+  const unsigned i0 = share(blockIdx.x);
+  const int items = share(blockIdx.x + 1) - i0;
+  int held = -1, lo = 0, n0 = 0, n1 = 0, hi = 0, rb = 0;
   float xs = 1.f;
   f32x4 acc[F];
-  // where an item lies: segment and row block
-  auto seg_of = [&](int i) { return (int)((i0 + i) / n_rb); };
-  const int pitch = width;
-  const bool flat = !a.starts && a.ldx == 1;       // one column
   stream<DecOperand<F>, DecSource, kDepth, kDecWaves>(
       items,
       [&](int i) -> DecSource {
-        const int sg = seg_of(i), e = find_expert(a, pre, sg), r16 = (int)(i0 + i - (int64_t)sg * n_rb) * F;
-        const int t = r16 * 16 / a.rows;
+        const unsigned sg = (i0 + i) / n_rb, r16 = (i0 + i - sg * n_rb) * F, t = r16 * 16 / (unsigned)a.rows;
+        const int e = find_expert(a, pre, sg);
         return {a.val_d + e * a.b_val_d, a.val_s + e * a.b_val_s, a.meta + e * a.b_meta, a.idx_d + e * a.b_idx_d,
                 a.idx_s + e * a.b_idx_s, a.scale_d + e * a.b_scale_d, a.scale_s + e * a.b_scale_s,
-                t, r16 * 16 - t * a.rows, wave, nblk};
+                (int)t, (int)(r16 * 16 - t * a.rows), wave, nblk};
       },
       [&](const DecSource& s, int b, DecOperand<F>& o) {
         const bool dense = b < nd;
         const int k = dense ? b : b - nd, nkb = dense ? nd : ns;
-        const int64_t kb = (int64_t)s.tile * nkb + k, row = kb * a.rows + s.row;
-        o.index = at<int>(pick(dense, s.idx_d, s.idx_s) + kb * (dense ? 128 : 256), dense ? 4 * (lane & 31) : 4 * lane);
-        const uint8_t* val = pick(dense, s.val_d, s.val_s) + row * 32;
-        const uint8_t* meta = pick(dense, val, s.meta + row * 8);  // a dense block has none and reads its values' bytes
-        const uint8_t* scale = pick(dense, s.scale_d, s.scale_s) + ((int64_t)s.tile * ((nkb + 3) / 4) + k / 4) * a.rows + s.row;
+        // 32-bit offsets from an expert's buffers
+        const uint32_t kb = s.tile * nkb + k, row = kb * a.rows + s.row;
+        const uint32_t group = (s.tile * ((nkb + 3) / 4) + k / 4) * a.rows + s.row;
+        const uint8_t *val = pick(dense, s.val_d, s.val_s), *scale = pick(dense, s.scale_d, s.scale_s);
+        // a dense block has no metadata and reads its values' first bytes
+        const uint8_t* meta = pick(dense, s.val_d, s.meta);
+        o.index = at<int>(pick(dense, s.idx_d, s.idx_s), dense ? kb * 128 + 4 * (lane & 31) : kb * 256 + 4 * lane);
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-          o.v[f] = at<fp8_u32x2>(val, 32 * i16 + 8 * kc + 512 * f);
-          o.scale[f] = at<uint8_t>(scale, 16 * f + i16);
-          o.m[f] = at<uint16_t>(meta, 8 * i16 + 2 * kc + 128 * f);
+          o.v[f] = at<fp8_u32x2>(val, row * 32 + 32 * i16 + 8 * kc + 512 * f);
+          o.scale[f] = at<uint8_t>(scale, group + 16 * f + i16);
+          o.m[f] = at<uint16_t>(meta, row * 8 + 8 * i16 + 2 * kc + 128 * f);
         }
       },
       [&](int b, const DecOperand<F>& o) {
-        // the lane's share of the transposed reads: eight tokens of position 8 kc + i16 / 2, and 32 further on (past a
-        // row of eight the same ones again: columns that nothing reads)
-        const int s8 = 8 * min(i16 & 1, pitch / 8 - 1), p = 8 * kc + (i16 >> 1);
+        // the lane's share of the transposed reads: eight tokens of position 8 kc + i16 / 2, and 32 further on (at width
+        // 8 the same ones again: columns that nothing reads)
+        const int s8 = width == 16 ? 8 * (i16 & 1) : 0, p = 8 * kc + (i16 >> 1);
         const bool dense = b < nd;
-        const int row = ((uint32_t)o.index < (uint32_t)a.cin ? o.index : a.cin) * pitch;
+        const int row = ((uint32_t)o.index < (uint32_t)a.cin ? o.index : a.cin) * width;
         fp8_u32x2 raw[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -680,16 +718,18 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
         }
       },
       [&](int i) {
-        const int sg = seg_of(i);
-        rb = (int)(i0 + i - (int64_t)sg * n_rb);
-        if (sg != held) {
+        const unsigned sg = (i0 + i) / n_rb;
+        rb = i0 + i - sg * n_rb;
+        if ((int)sg != held) {
           const int e = find_expert(a, pre, sg);
-          int lo;
           range_of(a, e, lo, hi);
-          n0 = lo + (sg - (a.starts ? pre[e] : 0)) * width;
-          __syncthreads();
-          load_codes(a, n0, width, flat, slab, sh.top, scales);
-          __syncthreads();
+          lo += (sg - (a.starts ? pre[e] : 0)) * width;
+          // eight columns each that X has, and of which some may be others'
+          n0 = max(min(lo, a.n_cols - 8), 0);
+          n1 = max(min(lo + 8, a.n_cols - 8), 0);
+          if (!a.starts && a.ldx == 1) load_token(a, slab, top, scales);
+          else load_codes(a, n0, n1, width, slab, top, scales);
+          step_barrier();
           xs = fp8_scale(scales[i16 & (width - 1)]);
           held = sg;
         }
@@ -697,19 +737,24 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
         for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
       },
       [&](int) {
-        // 256 / width rows a round: 16 or 32
-#pragma nounroll
-        for (int r0 = 0; r0 < 16 * F; r0 += 256 / width) {
-          put_sums<F>(sh.red, acc, r0, width);
-          __syncthreads();
-          // element threadIdx.x / 2, waves 4 (threadIdx.x % 2) .. + 3
-          const float* q = sh.red + (threadIdx.x & 1) * 4 * kRed + (threadIdx.x >> 1);
-          float s = (q[0] + q[kRed]) + (q[2 * kRed] + q[3 * kRed]);
-          s += quad1(s);
-          const int e = threadIdx.x >> 1, row = r0 + e / width, n = n0 + e % width;
-          if ((threadIdx.x & 1) == 0 && n < hi && row < 16 * F) a.y[((int64_t)rb * 16 * F + row) * a.ldy + n] = to_bf16(s);
-          __syncthreads();
+        // lane's sums of wave w, fragment f: red[w][f][lane]
+        constexpr int kPitch = dec_red_bytes(F) / 4 / kDecWaves, kParts = kDecWaves / F;
+#pragma unroll
+        for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(red + wave * kPitch + 256 * f + 4 * lane) = acc[f];
+        step_barrier();
+        const int part = threadIdx.x % kParts, g = threadIdx.x / kParts, f = g >> 6, l = g & 63;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < F; ++w) s += *reinterpret_cast<const f32x4*>(red + (part * F + w) * kPitch + 4 * g);
+        const int j = l & 15, n = (j < 8 ? n0 : n1 - 8) + j, from = lo + (j & 8), row = rb * 16 * F + 16 * f + 4 * (l >> 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v = s[q] + quad1(s[q]);
+          if (kParts >= 4) v += quad2(v);
+          if (kParts == 8) v += octet(v);
+          if (q % kParts == part && j < width && n >= from && n < hi && n < from + 8) a.y[(int64_t)(row + q) * a.ldy + n] = to_bf16(v);
         }
+        step_barrier();
       });
 }
 
@@ -733,6 +778,7 @@ int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n
   if (p.bytes_val_dense >= lim || p.bytes_val_24 >= lim || p.bytes_idx_dense >= lim || p.bytes_idx_24 >= lim)
     return fail(HINM_ESHAPE, "each weight's buffers must be below 2^31 bytes");
   if (p.cin > (1 << 22)) return fail(HINM_ESHAPE, "cin=%d exceeds 2^22", p.cin);
+  if (ldx >= lim) return fail(HINM_ESHAPE, "ldx=%lld must be below 2^31", (long long)ldx);
   if (n_cols == 0) return HINM_OK;
   if (!x || !y) return fail(HINM_EINVAL, "x and y must be non-NULL");
   if (!hinm::aligned(x, 2) || !hinm::aligned(y, 2)) return fail(HINM_EALIGN, "x and y must be 2-byte aligned");
@@ -750,10 +796,10 @@ int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
 // Columns of a decode segment, 8 or 16, or 0 where the many-token kernel is
 // taken: as many as an expert has on average and as fit in LDS, in up to two
 // segments.
-int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols, int64_t ldx) {
+int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
-  const int fit = (int64_t)(p.cin + 1) * 16 <= kDecSlab ? 16 : (int64_t)(p.cin + 1) * 8 <= kDecSlab ? 8 : 0;
-  if (fit == 0 || (int64_t)(p.cin - 1) * ldx + n_cols < 8 || p.n_dense + p.n_24 == 0) return 0;
+  const int fit = dec_fits(p.cin, 16, 1) ? 16 : dec_fits(p.cin, 8, 1) ? 8 : 0;
+  if (fit == 0 || p.cin < 8 || p.n_dense + p.n_24 == 0 || n_cols * (p.cout / 16) >= (int64_t)1 << 31) return 0;
   const int width = avg <= 8 ? 8 : fit;
   return avg <= 2 * width ? width : 0;
 }
@@ -769,7 +815,7 @@ struct Workspace {
 };
 Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   Workspace w{};
-  if (n_cols == 0 || decode_width(p, n_experts, n_cols, n_cols)) return w;
+  if (n_cols == 0 || decode_width(p, n_experts, n_cols)) return w;
   w.window = std::min(n_cols, std::max<int64_t>(256, ((int64_t)1 << 30) / p.cin / 256 * 256));
   w.ld8 = w.window <= 128 ? 128 : ((w.window + 255) / 256 | 1) * 256;
   w.chunks = (int)std::min<int64_t>(kChunks, (p.cin + 63) / 64);
@@ -837,15 +883,17 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
   a.rows = p.tile_rows;
   a.n_tiles = p.n_tiles;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
-  if (const int width = decode_width(p, n_experts, n_cols, n_cols)) {
+  if (const int width = decode_width(p, n_experts, n_cols)) {
     a.n_cols = (int)n_cols;
     a.x = static_cast<const uint16_t*>(x);
     a.y = static_cast<uint16_t*>(y);
     // rows an item: those that leave the busiest of 256 workgroups the least to do, an item costing half a fragment
     // more than its rows
     const int64_t segs = n_experts == 1 ? (n_cols + width - 1) / width : std::min<int64_t>(n_experts, n_cols);
-    auto cost = [&](int f) { return ((segs * (p.cout / (16 * f)) + kCus - 1) / kCus) * (2 * f + 1); };
-    const int f = cost(1) < cost(2) && cost(1) < cost(4) ? 1 : cost(2) < cost(4) ? 2 : 4;
+    auto cost = [&](int f) {
+      return dec_fits(p.cin, width, f) ? ((segs * (p.cout / (16 * f)) + kCus - 1) / kCus) * (2 * f + 1) : INT64_MAX;
+    };
+    const int f = cost(1) <= cost(2) && cost(1) <= cost(4) ? 1 : cost(2) <= cost(4) ? 2 : 4;
     if (f == 4) hipLaunchKernelGGL(fp8_decode_kernel<4>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
     else if (f == 2) hipLaunchKernelGGL(fp8_decode_kernel<2>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
     else hipLaunchKernelGGL(fp8_decode_kernel<1>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);

@@ -9,6 +9,9 @@ namespace {
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// A barrier that waits for this wave's LDS operations, not for its loads.
+__device__ inline void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 template <class T>
 __device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpret_cast<const T*>(base + offset); }
 
@@ -65,24 +68,11 @@ __device__ __forceinline__ void stream(int items, Open open, Load load, Multiply
   }
 }
 
-// Sums over a workgroup's waves of their products' rows r0 .. r0 + 256 / width - 1
-// (of 16 F) in `width` columns.  Each wave puts its own, at a pitch that keeps
-// the reads free of bank conflicts; acc[f][q] is row 16 f + 4 (lane / 16) + q,
-// column lane % 16.
-constexpr int kRed = 260;
-template <int F>
-__device__ inline void put_sums(float* red, const f32x4 (&acc)[F], int r0, int width) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15;
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-    if (16 * f >= r0 && 16 * f < r0 + 256 / width && col < width)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) red[wave * kRed + (16 * f - r0 + 4 * (lane >> 4) + q) * width + col] = acc[f][q];
-}
-
 // The value of lane ^ 1 or ^ 2.
 __device__ inline float quad1(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xf, 0xf, true)); }
 __device__ inline float quad2(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xf, 0xf, true)); }
+// The value of a lane of the other four of eight, where four hold the same.
+__device__ inline float octet(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xf, 0xf, true)); }
 
 }  // namespace
 
