@@ -521,8 +521,8 @@ __device__ inline u32x4 shifted_row(u32x4 v, int past) {
 
 // Eight columns' largest magnitudes over the workgroup's threads (two sets of
 // them where `halves`), from each thread's.
-__device__ __forceinline__ u32x4 workgroup_max(u32x4 m, bool halves, int half, uint32_t* red) {
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+__device__ __forceinline__ u32x4 workgroup_max(int tid, u32x4 m, bool halves, int half, uint32_t* red) {
+  const int lane = tid & 63, wave = uniform(tid >> 6);
   u32x4 top;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -556,10 +556,11 @@ __device__ __forceinline__ u32x4 workgroup_max(u32x4 m, bool halves, int half, u
 // Of fewer than eight columns a row's load reaches into the next rows, whose
 // codes nothing uses, and the last rows' begins early and is shifted.
 constexpr int kHeld = 8;
+static_assert(kDecThreads == 512 && kHeld == 8);     // the shifts below
 __device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int n1, int width, uint8_t* slab, uint32_t* red,
                                            uint8_t* scales) {
-  const int group = kDecThreads * 8 / width, half = uniform((int)threadIdx.x >= group);
-  const int first = threadIdx.x - half * group, passes = (a.cin + kHeld * group - 1) / (kHeld * group);
+  const int tid = own_thread(), shift = width == 16 ? 8 : 9, group = 1 << shift, half = uniform(tid >> shift);
+  const int first = tid - half * group, passes = (a.cin + kHeld * group - 1) >> (shift + 3);
   const uint16_t* const x = a.x + (half ? n1 : n0);
   const uint32_t ldx = (uint32_t)a.ldx;
   const bool few = a.n_cols < 8;
@@ -587,7 +588,7 @@ __device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int n1, int
 #pragma unroll
       for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
   }
-  const u32x4 top = workgroup_max(m, width == 16, half, red);
+  const u32x4 top = workgroup_max(tid, m, width == 16, half, red);
   float inv[8];
   uint32_t e[8];
 #pragma unroll
@@ -616,31 +617,32 @@ __device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int n1, int
 // and registers hold.
 __device__ __forceinline__ void load_token(const Fp8Args& a, uint8_t* slab, uint32_t* red, uint8_t* scales) {
   constexpr int kChunks8 = (kDecLds / 8 + 8 * kDecThreads - 1) / (8 * kDecThreads);
+  const int tid = own_thread();
   u32x4 v[kChunks8], m = {kLeast, kLeast, kLeast, kLeast};
 #pragma unroll
   for (int u = 0; u < kChunks8; ++u) {
-    const int c = 8 * (threadIdx.x + u * kDecThreads), from = min(c, a.cin - 8);
+    const int c = 8 * (tid + u * kDecThreads), from = min(c, a.cin - 8);
     v[u] = shifted_row(*reinterpret_cast<const any_u32x4*>(a.x + from), min(c - from, 7));
   }
 #pragma unroll
   for (int u = 0; u < kChunks8; ++u)
 #pragma unroll
     for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
-  const u32x4 top = workgroup_max(m, false, 0, red);
+  const u32x4 top = workgroup_max(tid, m, false, 0, red);
   uint32_t t = larger2(larger2(top[0], top[1]), larger2(top[2], top[3]));
   t = max(t & 0xffffu, t >> 16);
   const uint32_t e = column_scale(t);
   const float i1 = fp8_inverse(e), inv[8] = {i1, i1, i1, i1, i1, i1, i1, i1};
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     scales[0] = (uint8_t)e;
     *reinterpret_cast<fp8_u32x2*>(slab + a.cin * 8) = fp8_u32x2{0u, 0u};
   }
 #pragma unroll
   for (int u = 0; u < kChunks8; ++u) {
-    const int c = 8 * (threadIdx.x + u * kDecThreads);
+    const int c = 8 * (tid + u * kDecThreads);
     if (c >= a.cin) break;
     const uint64_t code = __builtin_bit_cast(uint64_t, column_codes(v[u], inv));
-    const int turn = threadIdx.x >> 2;             // lanes that share banks begin at other channels
+    const int turn = tid >> 2;             // lanes that share banks begin at other channels
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int j = (k + turn) & 7;
@@ -742,7 +744,8 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
 #pragma unroll
         for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(red + wave * kPitch + 256 * f + 4 * lane) = acc[f];
         step_barrier();
-        const int part = threadIdx.x % kParts, g = threadIdx.x / kParts, f = g >> 6, l = g & 63;
+        const int tid = own_thread();
+        const int part = tid % kParts, g = tid / kParts, f = g >> 6, l = g & 63;
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < F; ++w) s += *reinterpret_cast<const f32x4*>(red + (part * F + w) * kPitch + 4 * g);

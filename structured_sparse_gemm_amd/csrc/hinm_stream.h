@@ -12,6 +12,15 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 // A barrier that waits for this wave's LDS operations, not for its loads.
 __device__ inline void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// The thread's number, as a value that the compiler takes for new: what is
+// computed from it stays where it is used, and out of the code ahead of a loop
+// that uses it once.
+__device__ inline int own_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 template <class T>
 __device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpret_cast<const T*>(base + offset); }
 
