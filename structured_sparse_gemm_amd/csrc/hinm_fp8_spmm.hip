@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kPreThreads, 2) void fp8_prefill_kernel(Fp8Args a, 
 // deal the K-blocks among themselves, and their sums meet in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kDecThreads = 512, kDecWaves = kDecThreads / 64;
-constexpr int kDecLds = 159488;      // bytes for the codes, a row of zeros and the waves' sums
+constexpr int kDecLds = 159360;      // bytes for the codes, a row of zeros and the waves' sums
 constexpr int dec_red_bytes(int f) { return kDecWaves * (256 * f + 8) * 4; }   // the 8: reads free of bank conflicts
 constexpr bool dec_fits(int64_t cin, int width, int f) { return (cin + 1) * width + dec_red_bytes(f) <= kDecLds; }
 
@@ -508,6 +508,43 @@ struct DecSource {
   int tile, row, first, end;
 };
 
+// The activations of a segment: `width` columns, eight from n0 and, at width 16,
+// eight from n1 on, of which columns lo .. hi - 1 are the segment's.
+struct Segment {
+  int n0, n1, lo, hi;
+};
+
+// X's values are kept in registers, kHeld loads a thread, from `load_x`, which
+// comes ahead of the weight's first loads, to `round_x`: one pass of
+// kHeld * 512 loads of sixteen bytes.  A load is eight columns of a channel -
+// at width 16 neighbouring lanes take the two halves of a channel, which share
+// cache lines - or, where X is one column without padding (TOKEN), eight
+// channels.  Of fewer than eight columns a row's load reaches into the next
+// rows, whose codes nothing uses, and the last rows' begins early and is shifted.
+constexpr int kChannelLoads = 16;
+template <bool TOKEN>
+constexpr int kHeld = TOKEN ? (kDecLds / 8 + 8 * kDecThreads - 1) / (8 * kDecThreads) : kChannelLoads;
+static_assert(kDecThreads == 512 && kChannelLoads == 16);          // the shifts below
+
+template <bool TOKEN>
+__device__ __forceinline__ void load_x(const Fp8Args& a, const Segment& sg, int width, int pass, u32x4 (&v)[kHeld<TOKEN>]) {
+  const int tid = own_thread();
+  if constexpr (TOKEN) {
+#pragma unroll
+    for (int u = 0; u < kHeld<TOKEN>; ++u) v[u] = *reinterpret_cast<const any_u32x4*>(a.x + min(8 * (tid + u * kDecThreads), a.cin - 8));
+    return;
+  }
+  const int half = width == 16 ? tid & 1 : 0, shift = width == 16 ? 8 : 9, first = width == 16 ? tid >> 1 : tid;
+  const int n0 = sg.n0, n1 = sg.n1;
+  const uint16_t* const x = a.x + (half ? n1 : n0);
+  const int64_t last = a.n_cols < 8 ? (int64_t)(a.cin - 1) * a.ldx + a.n_cols - 8 : INT64_MAX;
+#pragma unroll
+  for (int u = 0; u < kHeld<TOKEN>; ++u) {
+    const int c = min(first + ((pass * kChannelLoads + u) << shift), a.cin - 1);
+    v[u] = *reinterpret_cast<const any_u32x4*>(x + min((int64_t)((uint64_t)(uint32_t)c * (uint32_t)a.ldx), last));
+  }
+}
+
 // Eight of X's values from element `from` on, of which the first is wanted at
 // `from + past`.
 __device__ inline u32x4 shifted_row(u32x4 v, int past) {
@@ -519,164 +556,151 @@ __device__ inline u32x4 shifted_row(u32x4 v, int past) {
   return v;
 }
 
-// Eight columns' largest magnitudes over the workgroup's threads (two sets of
-// them where `halves`), from each thread's.
-__device__ __forceinline__ u32x4 workgroup_max(int tid, u32x4 m, bool halves, int half, uint32_t* red) {
-  const int lane = tid & 63, wave = uniform(tid >> 6);
-  u32x4 top;
+// Their codes into the slab, [channel][width] and a row of zeros, and the
+// columns' scale bytes into `scales`.  Where one pass does not hold the columns,
+// all but the last are read once more, from L2.
+template <bool TOKEN>
+__device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int width, u32x4 (&v)[kHeld<TOKEN>], uint8_t* slab,
+                                        uint32_t* red, uint8_t* scales) {
+  const int tid = own_thread(), lane = tid & 63, passes = TOKEN ? 1 : (a.cin + (width == 16 ? 4095 : 8191)) >> (width == 16 ? 12 : 13);
+  const int half = width == 16 ? tid & 1 : 0, shift = width == 16 ? 8 : 9, first = width == 16 ? tid >> 1 : tid;
+  auto shift_last = [&](int pass) {
+    if constexpr (TOKEN) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t r = m[k];
-    r = larger2(r, moved<0x111>(r));               // within 16 lanes: by 1, 2, 4, 8
-    r = larger2(r, moved<0x112>(r));
-    r = larger2(r, moved<0x114>(r));
-    r = larger2(r, moved<0x118>(r));
-    r = larger2(r, moved<0x142>(r));               // lane 15 of 16 to the next 16, lane 31 to the upper 32
-    r = larger2(r, moved<0x143>(r));
-    top[k] = (uint32_t)__builtin_amdgcn_readlane((int)r, 63);
-  }
-  if (lane == 0) *reinterpret_cast<u32x4*>(red + 4 * wave) = top;
-  step_barrier();
-  uint32_t r = red[lane & 31];                     // wave lane / 4, dword lane % 4
-  if (halves && ((lane >> 4) & 1) != half) r = kLeast;
-  r = larger2(r, (uint32_t)__shfl_xor((int)r, 4));
-  r = larger2(r, (uint32_t)__shfl_xor((int)r, 8));
-  r = larger2(r, (uint32_t)__shfl_xor((int)r, 16));
-#pragma unroll
-  for (int k = 0; k < 4; ++k) top[k] = (uint32_t)__builtin_amdgcn_readlane((int)r, k);
-  return top;
-}
-
-// The codes of a segment of `width` columns, eight from n0 and, at width 16,
-// eight from n1 on, into the slab, the scale bytes into `scales`.  A thread
-// takes eight columns of a channel at a time - at width 16 the waves of the
-// upper half the upper eight, so that a wave's maxima and scales are scalars -
-// kHeld channels in flight.  X is read for its largest magnitudes and, but for
-// the first kHeld channels a thread, which stay in registers, again from L2.
-// Of fewer than eight columns a row's load reaches into the next rows, whose
-// codes nothing uses, and the last rows' begins early and is shifted.
-constexpr int kHeld = 8;
-static_assert(kDecThreads == 512 && kHeld == 8);     // the shifts below
-__device__ __forceinline__ void load_codes(const Fp8Args& a, int n0, int n1, int width, uint8_t* slab, uint32_t* red,
-                                           uint8_t* scales) {
-  const int tid = own_thread(), shift = width == 16 ? 8 : 9, group = 1 << shift, half = uniform(tid >> shift);
-  const int first = tid - half * group, passes = (a.cin + kHeld * group - 1) >> (shift + 3);
-  const uint16_t* const x = a.x + (half ? n1 : n0);
-  const uint32_t ldx = (uint32_t)a.ldx;
-  const bool few = a.n_cols < 8;
-  const int64_t last = (int64_t)(a.cin - 1) * a.ldx + a.n_cols - 8;   // of few columns: where the last load begins
-  u32x4 v[kHeld];
-  auto load = [&](int pass) {
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const uint64_t at = (uint64_t)(uint32_t)min(first + (pass * kHeld + u) * group, a.cin - 1) * ldx;
-      v[u] = *reinterpret_cast<const any_u32x4*>(x + (few ? min((int64_t)at, last) : (int64_t)at));
-    }
-    if (few)
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u) {
-        const uint64_t at = (uint64_t)(uint32_t)min(first + (pass * kHeld + u) * group, a.cin - 1) * ldx;
-        v[u] = shifted_row(v[u], (int)max((int64_t)at - last, (int64_t)0));
+      for (int u = 0; u < kHeld<TOKEN>; ++u) {
+        const int c = 8 * (tid + u * kDecThreads);
+        v[u] = shifted_row(v[u], min(max(c - (a.cin - 8), 0), 7));
       }
+    } else if (a.n_cols < 8) {
+      const int64_t last = (int64_t)(a.cin - 1) * a.ldx + a.n_cols - 8;
+#pragma unroll
+      for (int u = 0; u < kHeld<TOKEN>; ++u) {
+        const int c = min(first + ((pass * kChannelLoads + u) << shift), a.cin - 1);
+        v[u] = shifted_row(v[u], (int)max((int64_t)((uint64_t)(uint32_t)c * (uint32_t)a.ldx) - last, (int64_t)0));
+      }
+    }
   };
   u32x4 m = {kLeast, kLeast, kLeast, kLeast};
-#pragma nounroll
-  for (int pass = passes - 1; pass >= 0; --pass) {
-    load(pass);
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
-  }
-  const u32x4 top = workgroup_max(tid, m, width == 16, half, red);
-  float inv[8];
-  uint32_t e[8];
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    e[u] = column_scale((top[u >> 1] >> (16 * (u & 1))) & 0xffffu);
-    inv[u] = fp8_inverse(e[u]);
-  }
-  if (first == 0) {
-    *reinterpret_cast<fp8_u32x2*>(scales + 8 * half) =
-        fp8_u32x2{e[0] | e[1] << 8 | e[2] << 16 | e[3] << 24, e[4] | e[5] << 8 | e[6] << 16 | e[7] << 24};
-    *reinterpret_cast<fp8_u32x2*>(slab + a.cin * width + 8 * half) = fp8_u32x2{0u, 0u};
-  }
+  shift_last(0);
 #pragma nounroll
   for (int pass = 0;;) {
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const int c = first + (pass * kHeld + u) * group;
+    for (int u = 0; u < kHeld<TOKEN>; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
+    if (++pass == passes) break;
+    load_x<TOKEN>(a, sg, width, pass, v);
+    shift_last(pass);
+  }
+  // the largest of a wave's lanes (of equal parity at width 16), then of the waves: red[wave][half][4]
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r = m[k];
+    if (width == 8) r = larger2(r, moved<0x121>(r));
+    r = larger2(r, moved<0x122>(r));
+    r = larger2(r, moved<0x124>(r));
+    r = larger2(r, moved<0x128>(r));
+    r = larger2(r, (uint32_t)__shfl_xor((int)r, 16));
+    m[k] = larger2(r, (uint32_t)__shfl_xor((int)r, 32));
+  }
+  if constexpr (TOKEN) {                                     // one column
+    uint32_t t = larger2(larger2(m[0], m[1]), larger2(m[2], m[3]));
+    t = larger2(t, t >> 16 | t << 16);
+    m = u32x4{t, t, t, t};
+  }
+  if (lane < 2) *reinterpret_cast<u32x4*>(red + 8 * (tid >> 6) + 4 * lane) = m;
+  step_barrier();
+  uint32_t r = red[lane];
+  r = larger2(r, moved<0x128>(r));
+  r = larger2(r, (uint32_t)__shfl_xor((int)r, 16));
+  r = larger2(r, (uint32_t)__shfl_xor((int)r, 32));
+  const uint32_t e0 = column_scale(r & 0xffffu), e1 = column_scale(r >> 16);
+  if (tid < 8) *reinterpret_cast<uint16_t*>(scales + 2 * tid) = (uint16_t)(e0 | e1 << 8);
+  const uint32_t i0 = __float_as_uint(fp8_inverse(e0)), i1 = __float_as_uint(fp8_inverse(e1));
+  float inv[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint32_t from = u & 1 ? i1 : i0;
+    const int lo = __builtin_amdgcn_readlane((int)from, u >> 1), hi = __builtin_amdgcn_readlane((int)from, 4 + (u >> 1));
+    inv[u] = __int_as_float(half ? hi : lo);
+  }
+  if (tid < width / 8) *reinterpret_cast<fp8_u32x2*>(slab + a.cin * width + 8 * tid) = fp8_u32x2{0u, 0u};
+  if constexpr (TOKEN) {
+#pragma unroll
+    for (int u = 0; u < kHeld<TOKEN>; ++u) {
+      const int c = 8 * (tid + u * kDecThreads);
+      if (c >= a.cin) break;
+      const uint64_t code = __builtin_bit_cast(uint64_t, column_codes(v[u], inv));
+      const int turn = tid >> 2;                   // lanes that share banks begin at other channels
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = (k + turn) & 7;
+        if (c + j < a.cin) slab[(c + j) * 8] = (uint8_t)(code >> (8 * j));
+      }
+    }
+    return;
+  }
+#pragma nounroll
+  for (int pass = passes - 1;;) {
+#pragma unroll
+    for (int u = 0; u < kHeld<TOKEN>; ++u) {
+      const int c = first + ((pass * kChannelLoads + u) << shift);
       if (c < a.cin) *reinterpret_cast<fp8_u32x2*>(slab + c * width + 8 * half) = column_codes(v[u], inv);
     }
-    if (++pass == passes) break;
-    load(pass);
+    if (--pass < 0) break;
+    load_x<TOKEN>(a, sg, width, pass, v);
+    shift_last(pass);
   }
 }
 
-// The same for one column without padding, which eight channels a load cover
-// and registers hold.
-__device__ __forceinline__ void load_token(const Fp8Args& a, uint8_t* slab, uint32_t* red, uint8_t* scales) {
-  constexpr int kChunks8 = (kDecLds / 8 + 8 * kDecThreads - 1) / (8 * kDecThreads);
-  const int tid = own_thread();
-  u32x4 v[kChunks8], m = {kLeast, kLeast, kLeast, kLeast};
-#pragma unroll
-  for (int u = 0; u < kChunks8; ++u) {
-    const int c = 8 * (tid + u * kDecThreads), from = min(c, a.cin - 8);
-    v[u] = shifted_row(*reinterpret_cast<const any_u32x4*>(a.x + from), min(c - from, 7));
-  }
-#pragma unroll
-  for (int u = 0; u < kChunks8; ++u)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
-  const u32x4 top = workgroup_max(tid, m, false, 0, red);
-  uint32_t t = larger2(larger2(top[0], top[1]), larger2(top[2], top[3]));
-  t = max(t & 0xffffu, t >> 16);
-  const uint32_t e = column_scale(t);
-  const float i1 = fp8_inverse(e), inv[8] = {i1, i1, i1, i1, i1, i1, i1, i1};
-  if (tid == 0) {
-    scales[0] = (uint8_t)e;
-    *reinterpret_cast<fp8_u32x2*>(slab + a.cin * 8) = fp8_u32x2{0u, 0u};
-  }
-#pragma unroll
-  for (int u = 0; u < kChunks8; ++u) {
-    const int c = 8 * (tid + u * kDecThreads);
-    if (c >= a.cin) break;
-    const uint64_t code = __builtin_bit_cast(uint64_t, column_codes(v[u], inv));
-    const int turn = tid >> 2;             // lanes that share banks begin at other channels
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int j = (k + turn) & 7;
-      if (c + j < a.cin) slab[(c + j) * 8] = (uint8_t)(code >> (8 * j));
-    }
-  }
-}
-
-// Width: columns of a segment, 8 or 16.  Every instruction of the prologue is
-// issued by every wave, and a compute unit's waves share its issue slots: of 4,
-// 8 and 16 waves, 8 (with 16 a single token took 26 us).
-template <int F>
-__global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int width) {
+// Width: columns of a segment, 8 or 16.  The segments share the compute units
+// evenly, and a segment's workgroups its row blocks: to round a segment's
+// activations costs a workgroup as much as two to four items (a range of items
+// that ran on into the next segment did it twice: 8 experts 60 us).  Every
+// instruction of that prologue is issued by every wave, and a compute unit's
+// waves share its issue slots: of 4, 8 and 16 waves, 8 (16: a token 26 us).
+template <int F, bool TOKEN>
+__global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int columns) {
+  const int width = TOKEN ? 8 : columns;
   constexpr int kDepth = F == 1 ? 8 : F == 2 ? 6 : 4;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kDecLds];
-  __shared__ __attribute__((aligned(16))) uint32_t top[kDecWaves * 4];
+  __shared__ __attribute__((aligned(16))) uint32_t top[kDecWaves * 8];
   __shared__ int pre[HINM_MAX_EXPERTS + 1];
   __shared__ __attribute__((aligned(8))) uint8_t scales[16];
   float* const red = reinterpret_cast<float*>(slab + (kDecLds - dec_red_bytes(F)));
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
   const int nd = a.nkb_d, ns = a.nkb_s, nblk = nd + ns;
-  const unsigned n_rb = a.cout / (16 * F), all = plan_blocks(a, width, pre) * n_rb;
-  // this workgroup's share of all items
-  auto share = [&](unsigned b) { return all / kCus * b + all % kCus * b / kCus; };
-  const unsigned i0 = share(blockIdx.x);
-  const int items = share(blockIdx.x + 1) - i0;
-  int held = -1, lo = 0, n0 = 0, n1 = 0, hi = 0, rb = 0;
+  const unsigned n_rb = a.cout / (16 * F), segs = plan_blocks(a, width, pre), wg = blockIdx.x;
+  if (segs == 0) return;
+  // this workgroup's segments and, where it shares one, its row blocks
+  const unsigned sg0 = wg * segs / kCus;           // segs < 2^15
+  unsigned rb0 = 0, items;
+  if (segs >= kCus) {
+    items = ((wg + 1) * segs / kCus - sg0) * n_rb;
+  } else {
+    const unsigned first = (sg0 * kCus + segs - 1) / segs, n = ((sg0 + 1) * kCus + segs - 1) / segs - first, j = wg - first;
+    rb0 = n_rb / n * j + n_rb % n * j / n;
+    items = n_rb / n * (j + 1) + n_rb % n * (j + 1) / n - rb0;
+  }
+  int held = -1, coming = -1, rb = 0;
+  Segment now{}, next{};
+  u32x4 v[kHeld<TOKEN>];
   float xs = 1.f;
   f32x4 acc[F];
   stream<DecOperand<F>, DecSource, kDepth, kDecWaves>(
-      items,
+      (int)items,
       [&](int i) -> DecSource {
-        const unsigned sg = (i0 + i) / n_rb, r16 = (i0 + i - sg * n_rb) * F, t = r16 * 16 / (unsigned)a.rows;
+        const unsigned s = (rb0 + i) / n_rb, r16 = (rb0 + i - s * n_rb) * F, t = r16 * 16 / (unsigned)a.rows, sg = sg0 + s;
         const int e = find_expert(a, pre, sg);
+        if ((int)sg != coming) {
+          coming = sg;
+          range_of(a, e, next.lo, next.hi);
+          next.lo += (sg - (a.starts ? pre[e] : 0)) * width;
+          // eight columns each that X has, and of which some may be others'
+          next.n0 = max(min(next.lo, a.n_cols - 8), 0);
+          next.n1 = max(min(next.lo + 8, a.n_cols - 8), 0);
+          load_x<TOKEN>(a, next, width, 0, v);
+        }
         return {a.val_d + e * a.b_val_d, a.val_s + e * a.b_val_s, a.meta + e * a.b_meta, a.idx_d + e * a.b_idx_d,
                 a.idx_s + e * a.b_idx_s, a.scale_d + e * a.b_scale_d, a.scale_s + e * a.b_scale_s,
                 (int)t, (int)(r16 * 16 - t * a.rows), wave, nblk};
@@ -720,20 +744,14 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
         }
       },
       [&](int i) {
-        const unsigned sg = (i0 + i) / n_rb;
-        rb = i0 + i - sg * n_rb;
-        if ((int)sg != held) {
-          const int e = find_expert(a, pre, sg);
-          range_of(a, e, lo, hi);
-          lo += (sg - (a.starts ? pre[e] : 0)) * width;
-          // eight columns each that X has, and of which some may be others'
-          n0 = max(min(lo, a.n_cols - 8), 0);
-          n1 = max(min(lo + 8, a.n_cols - 8), 0);
-          if (!a.starts && a.ldx == 1) load_token(a, slab, top, scales);
-          else load_codes(a, n0, n1, width, slab, top, scales);
+        const unsigned s = (rb0 + i) / n_rb;
+        rb = rb0 + i - s * n_rb;
+        if ((int)(sg0 + s) != held) {
+          held = sg0 + s;
+          now = next;
+          round_x<TOKEN>(a, now, width, v, slab, top, scales);
           step_barrier();
           xs = fp8_scale(scales[i16 & (width - 1)]);
-          held = sg;
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -749,13 +767,13 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < F; ++w) s += *reinterpret_cast<const f32x4*>(red + (part * F + w) * kPitch + 4 * g);
-        const int j = l & 15, n = (j < 8 ? n0 : n1 - 8) + j, from = lo + (j & 8), row = rb * 16 * F + 16 * f + 4 * (l >> 4);
+        const int j = l & 15, n0 = now.n0, n1 = now.n1, n = (j < 8 ? n0 : n1 - 8) + j, from = now.lo + (j & 8), row = rb * 16 * F + 16 * f + 4 * (l >> 4);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float v = s[q] + quad1(s[q]);
           if (kParts >= 4) v += quad2(v);
           if (kParts == 8) v += octet(v);
-          if (q % kParts == part && j < width && n >= from && n < hi && n < from + 8) a.y[(int64_t)(row + q) * a.ldy + n] = to_bf16(v);
+          if (q % kParts == part && j < width && n >= from && n < now.hi && n < from + 8) a.y[(int64_t)(row + q) * a.ldy + n] = to_bf16(v);
         }
         step_barrier();
       });
@@ -894,12 +912,13 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
     // more than its rows
     const int64_t segs = n_experts == 1 ? (n_cols + width - 1) / width : std::min<int64_t>(n_experts, n_cols);
     auto cost = [&](int f) {
-      return dec_fits(p.cin, width, f) ? ((segs * (p.cout / (16 * f)) + kCus - 1) / kCus) * (2 * f + 1) : INT64_MAX;
+      const int64_t n_rb = p.cout / (16 * f), share = std::max<int64_t>(kCus / segs, 1);
+      return dec_fits(p.cin, width, f) ? (n_rb + share - 1) / share * (2 * f + 1) : INT64_MAX;
     };
     const int f = cost(1) <= cost(2) && cost(1) <= cost(4) ? 1 : cost(2) <= cost(4) ? 2 : 4;
-    if (f == 4) hipLaunchKernelGGL(fp8_decode_kernel<4>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
-    else if (f == 2) hipLaunchKernelGGL(fp8_decode_kernel<2>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
-    else hipLaunchKernelGGL(fp8_decode_kernel<1>, dim3(kCus), dim3(kDecThreads), 0, stream, a, width);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(kCus), dim3(kDecThreads), 0, stream, a, width); };
+    if (!starts && ldx == 1) f == 4 ? go(fp8_decode_kernel<4, true>) : f == 2 ? go(fp8_decode_kernel<2, true>) : go(fp8_decode_kernel<1, true>);
+    else f == 4 ? go(fp8_decode_kernel<4, false>) : f == 2 ? go(fp8_decode_kernel<2, false>) : go(fp8_decode_kernel<1, false>);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? HINM_OK : fail(HINM_EHIP, "8-bit product launch: %s", hipGetErrorString(e));
   }
