@@ -66,14 +66,6 @@ __device__ inline void range_of(const Fp8Args& a, int e, int& lo, int& hi) {
 // ---------------------------------------------------------------------------
 constexpr int kChunks = 64;          // pieces of the channels
 
-// Eight columns of a row, zeros past the last one.
-__device__ inline u32x4 load_row8(const uint16_t* row, int n, int n_cols) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (n + 8 <= n_cols) return *reinterpret_cast<const any_u32x4*>(row + n);
-  for (int u = 0; u < 8 && n + u < n_cols; ++u) v[u >> 1] |= (uint32_t)row[n + u] << (16 * (u & 1));
-  return v;
-}
-
 // Two bf16 magnitudes held as signed 16-bit numbers, 0x80 above their bits: what
 // is not finite is negative then and loses to every other.
 constexpr uint32_t kLeast = 0x00800080u;
@@ -108,53 +100,69 @@ __device__ inline fp8_u32x2 column_codes(u32x4 v, const float (&inv)[8]) {
   return c;
 }
 
-// Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece, four
-// loads a thread in flight.
+// Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece, whose
+// rows (up to 8 a thread) are all in flight at once: four at a time, and loads
+// under a condition, took 25 us for 4096 x 2047, this 6.  A thread's columns are
+// the window's last eight where it has no eight more, so that two threads may
+// write the same values; of a window of fewer than eight columns one thread
+// reads and writes single ones.
+constexpr int kRowsHeld = 8;
+__device__ __forceinline__ void load_rows(const Fp8Args& a, int n, int r0, int r1, u32x4 (&v)[kRowsHeld]) {
+  const int first = r0 + (threadIdx.x >> 5);
+#pragma unroll
+  for (int u = 0; u < kRowsHeld; ++u) {
+    const uint16_t* const row = a.x + (int64_t)min(first + 8 * u, r1 - 1) * a.ldx + n;
+    if (a.n_cols >= 8) {
+      v[u] = *reinterpret_cast<const any_u32x4*>(row);
+    } else {
+      v[u] = u32x4{0u, 0u, 0u, 0u};
+      for (int k = 0; k < a.n_cols; ++k) v[u][k >> 1] |= (uint32_t)row[k] << (16 * (k & 1));
+    }
+  }
+}
+
 __global__ __launch_bounds__(256) void fp8_colmax_kernel(Fp8Args a, uint16_t* __restrict__ part) {
   __shared__ u32x4 sh[256];
-  constexpr int U = 4;
-  const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
+  const int n = max(min((int)(blockIdx.x * 256 + 8 * (threadIdx.x & 31)), a.n_cols - 8), 0);
   u32x4 m = {kLeast, kLeast, kLeast, kLeast};
-  if (n < a.n_cols)
-    for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * U) {
-      u32x4 v[U];
+  for (int r = r0; r < r1; r += 8 * kRowsHeld) {
+    u32x4 v[kRowsHeld];
+    load_rows(a, n, r, r1, v);
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = load_row8(a.x + (int64_t)min(r + 8 * u, r1 - 1) * a.ldx, n, a.n_cols);
+    for (int u = 0; u < kRowsHeld; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
-    }
+      for (int k = 0; k < 4; ++k) m[k] = larger(m[k], v[u][k]);
+  }
   sh[threadIdx.x] = m;
   __syncthreads();
-  if (threadIdx.x < 32 && n < a.n_cols) {
+  if (threadIdx.x < 32) {
     for (int k = 1; k < 8; ++k)
 #pragma unroll
       for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], sh[32 * k + threadIdx.x][u]);
-    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = m;
+    *reinterpret_cast<any_u32x4*>(part + (int64_t)blockIdx.y * a.ld8 + n) = m;
   }
 }
 
 __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint16_t* __restrict__ part, int chunks,
                                                           uint8_t* __restrict__ x8, uint8_t* __restrict__ xs) {
+  typedef fp8_u32x2 any_u32x2 __attribute__((aligned(1)));
   __shared__ u32x4 sh[256];
-  constexpr int U = 4;
-  const int c8 = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * c8;
   const int r0 = (int)((int64_t)blockIdx.y * a.cin / gridDim.y), r1 = (int)((int64_t)(blockIdx.y + 1) * a.cin / gridDim.y);
-  u32x4 m = {kLeast, kLeast, kLeast, kLeast};
-  if (n < a.n_cols)
-#pragma unroll 4
-    for (int k = threadIdx.x >> 5; k < chunks; k += 8) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(part + (int64_t)k * a.ld8 + n);
+  const int n = max(min((int)(blockIdx.x * 256 + 8 * (threadIdx.x & 31)), a.n_cols - 8), 0);
+  u32x4 v[kRowsHeld], m = {kLeast, kLeast, kLeast, kLeast};
+  load_rows(a, n, r0, r1, v);
+#pragma unroll 8
+  for (int k = threadIdx.x >> 5; k < chunks; k += 8) {
+    const u32x4 t = *reinterpret_cast<const any_u32x4*>(part + (int64_t)k * a.ld8 + n);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], v[u]);
-    }
+    for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], t[u]);
+  }
   sh[threadIdx.x] = m;
   __syncthreads();
   for (int k = 0; k < 8; ++k)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], sh[32 * k + c8][u]);
+    for (int u = 0; u < 4; ++u) m[u] = larger2(m[u], sh[32 * k + (threadIdx.x & 31)][u]);
   uint32_t e[8];
   float inv[8];
 #pragma unroll
@@ -162,17 +170,16 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
     e[u] = column_scale((m[u >> 1] >> (16 * (u & 1))) & 0xffffu);
     inv[u] = fp8_inverse(e[u]);
   }
-  if (n >= a.ld8) return;
   if (blockIdx.y == 0 && threadIdx.x < 32)
     for (int u = 0; u < 8; ++u) xs[n + u] = (uint8_t)e[u];
-  for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8 * U) {
-    u32x4 v[U];
+  for (int r = r0;;) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      v[u] = n < a.n_cols ? load_row8(a.x + (int64_t)min(r + 8 * u, r1 - 1) * a.ldx, n, a.n_cols) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r + 8 * u < r1) *reinterpret_cast<fp8_u32x2*>(x8 + (int64_t)(r + 8 * u) * a.ld8 + n) = column_codes(v[u], inv);
+    for (int u = 0; u < kRowsHeld; ++u) {
+      const int row = r + (threadIdx.x >> 5) + 8 * u;
+      if (row < r1) *reinterpret_cast<any_u32x2*>(x8 + (int64_t)row * a.ld8 + n) = column_codes(v[u], inv);
+    }
+    if ((r += 8 * kRowsHeld) >= r1) break;
+    load_rows(a, n, r, r1, v);
   }
 }
 
