@@ -552,17 +552,6 @@ __device__ __forceinline__ void load_x(const Fp8Args& a, const Segment& sg, int 
   }
 }
 
-// Eight of X's values from element `from` on, of which the first is wanted at
-// `from + past`.
-__device__ inline u32x4 shifted_row(u32x4 v, int past) {
-  if (past & 4) v[0] = v[2], v[1] = v[3];
-  if (past & 2) v[0] = v[1], v[1] = v[2], v[2] = v[3];
-  if (past & 1)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = v[k] >> 16 | (k < 3 ? v[k + 1] << 16 : 0u);
-  return v;
-}
-
 // Their codes into the slab, [channel][width] and a row of zeros, and the
 // columns' scale bytes into `scales`.  Where one pass does not hold the columns,
 // all but the last are read once more, from L2.
@@ -660,12 +649,9 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
   }
 }
 
-// Width: columns of a segment, 8 or 16.  The segments share the compute units
-// evenly, and a segment's workgroups its row blocks: to round a segment's
-// activations costs a workgroup as much as two to four items (a range of items
-// that ran on into the next segment did it twice: 8 experts 60 us).  Every
-// instruction of that prologue is issued by every wave, and a compute unit's
-// waves share its issue slots: of 4, 8 and 16 waves, 8 (16: a token 26 us).
+// Width: columns of a segment, 8 or 16.  Every instruction of the prologue is
+// issued by every wave, and a compute unit's waves share its issue slots: of 4,
+// 8 and 16 waves, 8 (16: a token 26 us).
 template <int F, bool TOKEN>
 __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int columns) {
   const int width = TOKEN ? 8 : columns;
@@ -677,27 +663,17 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
   float* const red = reinterpret_cast<float*>(slab + (kDecLds - dec_red_bytes(F)));
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
   const int nd = a.nkb_d, ns = a.nkb_s, nblk = nd + ns;
-  const unsigned n_rb = a.cout / (16 * F), segs = plan_blocks(a, width, pre), wg = blockIdx.x;
-  if (segs == 0) return;
-  // this workgroup's segments and, where it shares one, its row blocks
-  const unsigned sg0 = wg * segs / kCus;           // segs < 2^15
-  unsigned rb0 = 0, items;
-  if (segs >= kCus) {
-    items = ((wg + 1) * segs / kCus - sg0) * n_rb;
-  } else {
-    const unsigned first = (sg0 * kCus + segs - 1) / segs, n = ((sg0 + 1) * kCus + segs - 1) / segs - first, j = wg - first;
-    rb0 = n_rb / n * j + n_rb % n * j / n;
-    items = n_rb / n * (j + 1) + n_rb % n * (j + 1) / n - rb0;
-  }
+  const unsigned n_rb = a.cout / (16 * F);
+  const Share mine = share_of(plan_blocks(a, width, pre), n_rb);
   int held = -1, coming = -1, rb = 0;
   Segment now{}, next{};
   u32x4 v[kHeld<TOKEN>];
   float xs = 1.f;
   f32x4 acc[F];
   stream<DecOperand<F>, DecSource, kDepth, kDecWaves>(
-      (int)items,
+      (int)mine.n,
       [&](int i) -> DecSource {
-        const unsigned s = (rb0 + i) / n_rb, r16 = (rb0 + i - s * n_rb) * F, t = r16 * 16 / (unsigned)a.rows, sg = sg0 + s;
+        const unsigned sg = (mine.first + i) / n_rb, r16 = (mine.first + i - sg * n_rb) * F, t = r16 * 16 / (unsigned)a.rows;
         const int e = find_expert(a, pre, sg);
         if ((int)sg != coming) {
           coming = sg;
@@ -751,10 +727,10 @@ __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int 
         }
       },
       [&](int i) {
-        const unsigned s = (rb0 + i) / n_rb;
-        rb = rb0 + i - s * n_rb;
-        if ((int)(sg0 + s) != held) {
-          held = sg0 + s;
+        const unsigned sg = (mine.first + i) / n_rb;
+        rb = mine.first + i - sg * n_rb;
+        if ((int)sg != held) {
+          held = sg;
           now = next;
           round_x<TOKEN>(a, now, width, v, slab, top, scales);
           step_barrier();

@@ -2,23 +2,26 @@
 // kernels (formulas at hinm_moe_layer).
 //
 // A few tokens make a layer a read of the chosen experts' packed weights, so
-// both kernels are built around that stream.  The activations of a segment -
-// up to 16 of an expert's tokens - are held in LDS whole, [channel][token], so
-// that the channels a tile keeps are gathered there: the transposed LDS read
-// takes an address a lane, which is the channel's row.  The gather therefore
-// costs no memory access and no staging, every global load of a wave (index
-// words, values, metadata) is at an address known beforehand, and 16 waves a
-// compute unit each keep their own K-blocks in flight.
+// both kernels are built around that stream: every wave keeps its own K-blocks
+// in flight.
 //
 //   up kernel    every workgroup works out the routing from the logits, then
-//                takes (segment, 64 rows of the inner channels): eight waves
-//                the gate's K-blocks, eight the up projection's; the sums meet
-//                in LDS and become h, which goes to the workspace laid out as
-//                the down kernel's LDS rows.
+//                takes (segment, 32 rows of the inner channels); a segment is
+//                up to 16 of an expert's tokens.  Their activations are held in
+//                LDS whole, [channel][token], and the channels that a tile
+//                keeps gathered there: the transposed LDS read takes an address
+//                a lane, which is the channel's row.  Four waves take the
+//                gate's K-blocks, four the up projection's; the sums meet in
+//                LDS and become h, which goes to the workspace by channels.
 //   down kernel  a workgroup takes 64 rows of Y and a share of all segments'
-//                K-blocks; each segment's sums are multiplied by the router's
-//                weights and added to the tokens' in LDS, and the shares meet
-//                in the workspace.
+//                K-blocks.  h has more channels than X and two columns a token,
+//                too much for LDS, so a wave gathers a block's rows of h from
+//                L2, by indices that it read a turn before, and turns them
+//                through LDS of its own.  A segment's sums are multiplied by
+//                the router's weights and added to the tokens' in LDS, and the
+//                shares meet in the workspace.  (With h in LDS a segment held
+//                two tokens of 11008 channels, and 8 experts of 8 tokens each
+//                took 145 us, four reads of each expert's weight.)
 //
 // h is a matrix operand and so bf16, but rounded once it would cost the output
 // as much as its own rounding (relative error of the layer 0.0024, against
@@ -29,25 +32,28 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "hinm_device.h"
 #include "hinm_fp8.h"
 #include "hinm_internal.h"
 #include "hinm_mx4.h"
 #include "hinm_ragged.h"
+#include "hinm_stream.h"
 
 using hinm::fail;
 
 namespace {
 
-constexpr int kWaves = 16;                         // of a workgroup; one workgroup a compute unit
+constexpr int kWaves = 8;                          // of a workgroup; one workgroup a compute unit (16: slower, see stream())
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTokens = HINM_MOE_MAX_TOKENS;
 constexpr int kPairs = kTokens * HINM_MAX_TOP_K;   // (token, expert) pairs at most; a segment holds at least one
 constexpr int kSlab = 131328;                      // bytes of LDS for a segment's activations and a row of zeros
 constexpr int kMaxChannels = 16384;                // of four columns, with the row of zeros
 static_assert((kMaxChannels + 1) * 8 <= kSlab, "four columns of the most channels fit");
-constexpr int kRed = 260;                          // floats between the waves' sums: 256, and conflict-free reads
+// Floats between the waves' sums of F fragments, the 8 for reads free of bank conflicts.
+constexpr int sums_pitch(int f) { return 256 * f + 8; }
 
 // One stack of packed weights; strides are bytes of one expert.
 struct MoeStack {
@@ -56,11 +62,11 @@ struct MoeStack {
   int rows, nkb_d, nkb_s, cin, cout;
 };
 
-// A segment: n of an expert's tokens from the rank0-th on.
+// A segment: n of an expert's tokens, from the rank0-th on.
 struct Seg {
-  uint16_t expert, slot;           // slot: of its first token
-  uint8_t n, rank0, count, pad;    // count: tokens of the expert
-  uint16_t down;                   // the expert's first segment of the down kernel
+  uint32_t mask;                   // the tokens
+  uint16_t expert, down;           // down: the expert's first segment of the down kernel
+  uint8_t n, rank0;
 };
 
 // What the up kernel leaves for the down kernel: its segments as expert, first
@@ -77,11 +83,11 @@ struct MoeArgs {
   const uint16_t* x;
   uint16_t* y;
   Table* table;
-  uint16_t* h;                     // [segment][inner channels][tokens]
+  uint16_t* h;                     // [segment][inner channels and a row of zeros][wide]
   float* part;
   unsigned* counters;
   int64_t ldl, ldx, ldy, h_seg;    // h_seg: elements between segments
-  int logits_fp32, n_tokens, n_experts, top_k, renormalize, up_cap, down_cap;
+  int logits_fp32, n_tokens, n_experts, top_k, renormalize, up_cap, wide;   // wide: twice a segment's tokens there
   MoeStack gate, up, down;
 };
 
@@ -123,18 +129,21 @@ struct Source {
   int first, end;                  // the wave's blocks: first, first + nw, ... below end
 };
 
-__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 __device__ inline Source source_of(const MoeStack& w, const Item& it, int v) {
-  const int t = it.rows16 * 16 / w.rows;
+  const int t = (unsigned)(it.rows16 * 16) / (unsigned)w.rows;
   const int64_t e = it.expert;
   return {w.val_d + e * w.b_val_d, w.val_s + e * w.b_val_s, w.meta + e * w.b_meta, w.idx_d + e * w.b_idx_d,
           w.idx_s + e * w.b_idx_s, w.scale_d + e * w.b_scale_d, w.scale_s + e * w.b_scale_s,
           t, it.rows16 * 16 - t * w.rows, it.b0 + v, it.b1};
 }
 
-template <class T>
-__device__ inline T at(const uint8_t* base, uint32_t offset) { return *reinterpret_cast<const T*>(base + offset); }
+// Block b's indices: a lane's position (of a dense block's 32, twice).
+__device__ inline int load_index(const MoeStack& w, const Source& s, int b) {
+  const uint32_t lane = threadIdx.x & 63;
+  const bool dense = b < w.nkb_d;
+  const uint32_t kb = dense ? s.tile * w.nkb_d + b : s.tile * w.nkb_s + b - w.nkb_d;
+  return at<int>(pick(dense, s.idx_d, s.idx_s), dense ? kb * 128 + 4 * (lane & 31) : kb * 256 + 4 * lane);
+}
 
 // Block b's operands.  The block's place is scalar and the lane's share a
 // constant; a dense block has no metadata and reads its values' bytes instead.
@@ -142,65 +151,54 @@ template <int VALUES, int F>
 __device__ inline void load_block(const MoeStack& w, const Source& s, int b, Operand<VALUES, F>& o) {
   const uint32_t lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
   const bool dense = b < w.nkb_d;
-  const int k = dense ? b : b - w.nkb_d;
-  const int64_t kb = (int64_t)s.tile * (dense ? w.nkb_d : w.nkb_s) + k;
-  o.index = dense ? at<int>(s.idx_d + kb * 128, 4 * (lane & 31)) : at<int>(s.idx_s + kb * 256, 4 * lane);
+  const uint32_t k = dense ? b : b - w.nkb_d, nkb = dense ? w.nkb_d : w.nkb_s, kb = s.tile * nkb + k;   // offsets below 2^31
+  const uint8_t *val = pick(dense, s.val_d, s.val_s), *scale = pick(dense, s.scale_d, s.scale_s), *meta = pick(dense, val, s.meta);
   if constexpr (VALUES == HINM_VALUES_MX4) {
-    const int64_t u = kb * (w.rows / 64) + s.row / 64;
-    const uint8_t* val = (dense ? s.val_d : s.val_s) + u * 1024;
+    const uint32_t u = kb * (w.rows / 64) + s.row / 64;
     const uint32_t f0 = (uint32_t)(s.row >> 4) & 3;          // 0 or 2 with two fragments
-    o.scale = at<uint32_t>((dense ? s.scale_d : s.scale_s) + u * 64, 4 * i16) >> (8 * f0);
-    const uint8_t* meta = dense ? val : s.meta + u * 512;
+    o.scale = at<uint32_t>(scale, u * 64 + 4 * i16) >> (8 * f0);
     if constexpr (F == 4) {
-      const u32x4 v = at<u32x4>(val, 256 * kc + 16 * i16);
-      const u32x2 m = at<u32x2>(meta, 128 * kc + 8 * i16);
+      const u32x4 v = at<u32x4>(val, u * 1024 + 256 * kc + 16 * i16);
+      const u32x2 m = at<u32x2>(meta, u * 512 + 128 * kc + 8 * i16);
       for (int f = 0; f < 4; ++f) o.v[f] = v[f];
       o.m[0] = m[0];
       o.m[1] = m[1];
     } else {
-      const u32x2 v = at<u32x2>(val, 256 * kc + 16 * i16 + 4 * f0);
+      const u32x2 v = at<u32x2>(val, u * 1024 + 256 * kc + 16 * i16 + 4 * f0);
       o.v[0] = v[0];
       o.v[1] = v[1];
-      o.m[0] = at<uint32_t>(meta, 128 * kc + 8 * i16 + 2 * f0);
+      o.m[0] = at<uint32_t>(meta, u * 512 + 128 * kc + 8 * i16 + 2 * f0);
     }
   } else {
     constexpr int kRow = VALUES == HINM_VALUES_FP8 ? 32 : 64;      // bytes of a row
-    const int64_t row = kb * w.rows + s.row;
-    const uint8_t* val = (dense ? s.val_d : s.val_s) + row * kRow;
-    const uint8_t* meta = dense ? val : s.meta + row * 8;
-    const int64_t group = (int64_t)s.tile * (((dense ? w.nkb_d : w.nkb_s) + 3) / 4) + k / 4;
-    const uint8_t* scale = (dense ? s.scale_d : s.scale_s) + group * w.rows + s.row;
+    const uint32_t row = kb * w.rows + s.row, group = (s.tile * ((nkb + 3) / 4) + k / 4) * w.rows + s.row;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       if constexpr (VALUES == HINM_VALUES_FP8) {
-        o.v[f] = at<u32x2>(val, 32 * i16 + 8 * kc + 512 * f);
-        o.scale[f] = at<uint8_t>(scale, 16 * f + i16);
+        o.v[f] = at<u32x2>(val, row * kRow + 32 * i16 + 8 * kc + 512 * f);
+        o.scale[f] = at<uint8_t>(scale, group + 16 * f + i16);
       } else {
-        o.v[f] = at<u32x4>(val, 64 * i16 + 16 * kc + 1024 * f);
+        o.v[f] = at<u32x4>(val, row * kRow + 64 * i16 + 16 * kc + 1024 * f);
       }
-      o.m[f] = at<uint16_t>(meta, 8 * i16 + 2 * kc + 128 * f);
+      o.m[f] = at<uint16_t>(meta, row * 8 + 8 * i16 + 2 * kc + 128 * f);
     }
   }
 }
 
-// acc += the block's rows x 16 columns of the slab: rows of `pitch` bytes,
-// zeros in row cin.
-template <int VALUES, int F>
-__device__ inline void multiply_block(const MoeStack& w, int b, const Operand<VALUES, F>& o, const uint8_t* slab,
-                                      int pitch, f32x4 (&acc)[F]) {
+// acc += the block's rows x 16 columns, of which row(position) is the LDS row.
+// The lane's share of the transposed reads: 8 bytes of columns 4 s .. 4 s + 3
+// (past a short row the first ones again: columns that nothing reads) of
+// positions 8 kc + i16 / 4 + {0, 4, 32, 36}.  A dense block is multiplied as a
+// 2:4 block whose groups keep positions 0 and 1: column 2 q + u at 4 q + u.
+template <int VALUES, int F, class Row>
+__device__ inline void multiply_block(bool dense, const Operand<VALUES, F>& o, int pitch, Row row, f32x4 (&acc)[F]) {
   const int lane = threadIdx.x & 63, i16 = lane & 15, kc = lane >> 4;
-  // The lane's share of the transposed reads: 8 bytes of columns 4 s .. 4 s + 3
-  // (past a short row the first ones again: columns that nothing reads) of
-  // positions 8 kc + i16 / 4 + {0, 4, 32, 36}.
   const int s8 = 8 * min(i16 & 3, pitch / 8 - 1), p0 = 8 * kc + (i16 >> 2);
-  const bool dense = b < w.nkb_d;
-  const int row = (o.index < 0 || o.index >= w.cin ? w.cin : o.index) * pitch;
   v4i16 q[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int p = p0 + 4 * (k & 1) + 32 * (k >> 1);
-    // a dense block is multiplied as a 2:4 block whose groups keep positions 0 and 1: column 2 q + u at 4 q + u
-    q[k] = tr_read_b(slab + __shfl(row, dense ? 2 * (p >> 2) + (p & 1) : p) + s8);
+    q[k] = tr_read_b(row(dense ? 2 * (p >> 2) + (p & 1) : p) + s8);
   }
   const bf16x8 lo8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
   const bf16x8 hi8 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(q[2], q[3], 0, 1, 2, 3, 4, 5, 6, 7));
@@ -221,83 +219,6 @@ __device__ inline void multiply_block(const MoeStack& w, int b, const Operand<VA
     }
     acc[f] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av, bv, acc[f], dense ? 0x4444 : sidx, 0, 0);
   }
-}
-
-// The wave's share - blocks v, v + NW, ... - of `items` items, in one stream:
-// while a pair of blocks is multiplied the next pair's operands are on their
-// way, across the items' ends too.  item_of(i) names an item (with one block at
-// least) without reading memory, begin(i) makes
-// its activations ready (in step for the whole workgroup) and returns their
-// pitch, and finish(i, acc) takes its sums (in step, too).  One loop body for
-// the first loads, the products and the items' ends: a launch reads every
-// instruction from memory once, and these kernels last some ten times that.
-template <int VALUES, int F, int NW, class ItemOf, class Begin, class Finish>
-__device__ inline void stream(const MoeStack& w, int items, int v, const uint8_t* slab, ItemOf item_of, Begin begin,
-                              Finish finish) {
-  if (items <= 0) return;
-  Operand<VALUES, F> o[2];
-  int block[2] = {-1, -1};         // the operands' blocks; -1: none
-  Source src{};
-  int ahead = -1, pairs = 0;       // the item that loads are at, and its pairs left
-  int pitch = 8;
-  f32x4 acc[F];
-#pragma unroll
-  for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma nounroll
-  while (true) {
-    const bool enter = pairs == 0;
-    if (enter) {
-      pairs = 1;
-      if (++ahead < items) {
-        src = source_of(w, item_of(ahead), v);
-        pairs = max(1, (src.end - src.first + 2 * NW - 1) / (2 * NW));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (block[k] >= 0) multiply_block<VALUES, F>(w, block[k], o[k], slab, pitch, acc);
-      // past its end an item's last block is read again: a load that only sometimes happens would make every wait one
-      // for all loads in flight
-      const int b = min(src.first, src.end - 1);
-      load_block<VALUES, F>(w, src, b, o[k]);
-      block[k] = src.first < src.end ? b : -1;
-      src.first += NW;
-    }
-    --pairs;
-    if (enter) {
-      if (ahead > 0) finish(ahead - 1, acc);
-      if (ahead >= items) return;
-      pitch = begin(ahead);
-#pragma unroll
-      for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  }
-}
-
-// The waves' sums of the rows r0 .. r0 + 256 / width - 1 (of 16 F) in `width`
-// columns: put by each wave, summed over four waves by each thread, which has
-// element threadIdx.x / 4 and waves 4 (threadIdx.x % 4) .. + 3.
-template <int F>
-__device__ inline void put_sums(float* red, const f32x4 (&acc)[F], int r0, int width) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15;
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-    if (16 * f >= r0 && 16 * f < r0 + 256 / width && col < width)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) red[wave * kRed + (16 * f - r0 + 4 * (lane >> 4) + q) * width + col] = acc[f][q];
-}
-__device__ inline float four_sums(const float* red) {
-  const float* p = red + (threadIdx.x & 3) * 4 * kRed + (threadIdx.x >> 2);
-  return (p[0] + p[kRed]) + (p[2 * kRed] + p[3 * kRed]);
-}
-// The value of lane ^ 1 or ^ 2.
-__device__ inline float quad1(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xf, 0xf, true)); }
-__device__ inline float quad2(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xf, 0xf, true)); }
-
-// A segment's scalars.
-__device__ inline Seg uniform_seg(const Seg& s) {
-  return {(uint16_t)uniform(s.expert), (uint16_t)uniform(s.slot), (uint8_t)uniform(s.n), (uint8_t)uniform(s.rank0),
-          (uint8_t)uniform(s.count), 0, (uint16_t)uniform(s.down)};
 }
 
 // ---------------------------------------------------------------------------
@@ -393,10 +314,10 @@ __device__ inline void route_token(const MoeArgs& a, RouteScratch& r, int n) {
   }
 }
 
-// The up kernel's segments and their tokens by slot go to `seg` and `token`,
-// their number to n_seg; down (one workgroup's): the table for the down kernel.
-__device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_seg, Seg* seg, uint16_t* token, Table* down) {
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+// The up kernel's segments go to `seg`, their number to n_seg; down (one
+// workgroup's): the table for the down kernel.
+__device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_seg, Seg* seg, Table* down) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), down_cap = a.wide / 2;
   for (int e = threadIdx.x; e < a.n_experts; e += kThreads) r.mask[e] = 0u;
   __syncthreads();
   for (int n = wave; n < a.n_tokens; n += kWaves) {
@@ -413,7 +334,7 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
     for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
       const int e = e0 + lane;
       const int c = e < a.n_experts ? __popc(r.mask[e]) : 0;
-      const int nu = (c + a.up_cap - 1) / a.up_cap, nd = (c + a.down_cap - 1) / a.down_cap;
+      const int nu = (c + a.up_cap - 1) / a.up_cap, nd = (c + down_cap - 1) / down_cap;
       const uint32_t own = (uint32_t)c | (uint32_t)nu << 10 | (uint32_t)nd << 20;
       uint32_t all = own;
       for (int d = 1; d < 64; d *= 2) {
@@ -423,12 +344,17 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
       const uint32_t at = before + all - own;
       const int s0 = at & 1023, u0 = at >> 10 & 1023, d0 = at >> 20;
       if (e < a.n_experts) r.start[e] = (uint16_t)s0;
-      for (int q = 0; q < nu; ++q)
-        seg[u0 + q] = {(uint16_t)e, (uint16_t)(s0 + q * a.up_cap), (uint8_t)min(a.up_cap, c - q * a.up_cap),
-                       (uint8_t)(q * a.up_cap), (uint8_t)c, 0, (uint16_t)d0};
+      uint32_t rest = nu ? r.mask[e] : 0u;
+      for (int q = 0; q < nu; ++q) {
+        const int n = min(a.up_cap, c - q * a.up_cap);
+        uint32_t after = rest;
+        for (int j = 0; j < n; ++j) after &= after - 1u;
+        seg[u0 + q] = {rest & ~after, (uint16_t)e, (uint16_t)d0, (uint8_t)n, (uint8_t)(q * a.up_cap)};
+        rest = after;
+      }
       if (down)
         for (int q = 0; q < nd; ++q)
-          down->seg[d0 + q] = (uint32_t)e | (uint32_t)(s0 + q * a.down_cap) << 10 | (uint32_t)min(a.down_cap, c - q * a.down_cap) << 20;
+          down->seg[d0 + q] = (uint32_t)e | (uint32_t)(s0 + q * down_cap) << 10 | (uint32_t)min(down_cap, c - q * down_cap) << 20;
       before += __shfl(all, 63);
     }
     if (lane == 0) {
@@ -437,246 +363,324 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
     }
   }
   __syncthreads();
-  if ((int)threadIdx.x < a.n_tokens * a.top_k) {
+  if (down && (int)threadIdx.x < a.n_tokens * a.top_k) {
     const int e = r.id[threadIdx.x], n = threadIdx.x / a.top_k;
     if (e >= 0) {
       const int slot = r.start[e] + __popc(r.mask[e] & ((1u << n) - 1u));
-      token[slot] = (uint16_t)n;
-      if (down) {
-        down->token[slot] = (uint16_t)n;
-        down->weight[slot] = r.weight[threadIdx.x];
-      }
+      down->token[slot] = (uint16_t)n;
+      down->weight[slot] = r.weight[threadIdx.x];
     }
   }
   __syncthreads();
 }
 
-// A segment's tokens from X into the slab, [channel][column], and the row of
-// zeros.  A thread reads eight tokens of a channel at once and writes those of
-// the segment, four channels in flight.
-__device__ inline void load_tokens(const MoeArgs& a, const Seg& seg, const uint16_t* token, uint16_t* slab) {
-  const int cin = a.up.cin, width = row_columns(seg.n);
-  uint32_t mask = 0;
-  for (int j = 0; j < seg.n; ++j) mask |= 1u << token[seg.slot + j];
-  mask = (uint32_t)uniform((int)mask);
-  const int64_t end = (int64_t)(cin - 1) * a.ldx + a.n_tokens;       // elements of X
-  constexpr int U = 4;
-  int col = 0;
-  for (int g = 0; g < 32; g += 8) {
-    const uint32_t some = (mask >> g) & 255u;
-    if (!some) continue;
-    for (int c0 = threadIdx.x; c0 < cin; c0 += U * kThreads) {
-      u32x4 v[U];
-      int past[U];                 // elements that the load begins before its own, at the end of X
+// X's values of eight tokens, g .. g + 7 (of fewer than eight the rows' first
+// ones, and the last rows' loads begin early; where fewer follow g, the last
+// eight), of channels c0 .. c0 + 8 * 512 - 1.
+constexpr int kHeld = 8;
+__device__ inline int first_token(const MoeArgs& a, int g) { return a.n_tokens < 8 ? 0 : min(g, a.n_tokens - 8); }
+__device__ __forceinline__ void load_x(const MoeArgs& a, int g, int c0, u32x4 (&v)[kHeld]) {
+  const int tid = own_thread();
+  const uint16_t* const x = a.x + first_token(a, g);
+  const int64_t last = a.n_tokens < 8 ? (int64_t)(a.up.cin - 1) * a.ldx + a.n_tokens - 8 : INT64_MAX;   // 64 elements or more
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = (int64_t)min(c0 + u * kThreads, cin - 1) * a.ldx + g;
-        const int64_t from = min(at, end - 8);     // X has 64 elements or more
-        past[u] = (int)(at - from);
-        v[u] = *reinterpret_cast<const any_u32x4*>(a.x + from);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (past[u] & 4) v[u][0] = v[u][2], v[u][1] = v[u][3];
-        if (past[u] & 2) v[u][0] = v[u][1], v[u][1] = v[u][2], v[u][2] = v[u][3];
-        if (past[u] & 1)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[u][k] = v[u][k] >> 16 | (k < 3 ? v[u][k + 1] << 16 : 0u);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * kThreads;
-        if (c >= cin) continue;
-        int j = col;
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if ((some >> t) & 1u) slab[c * width + j++] = (uint16_t)(v[u][t >> 1] >> (16 * (t & 1)));
-      }
-    }
-    col += __popc(some);
+  for (int u = 0; u < kHeld; ++u) {
+    const uint32_t c = min(c0 + tid + u * kThreads, a.up.cin - 1);
+    v[u] = *reinterpret_cast<const any_u32x4*>(x + min((int64_t)((uint64_t)c * (uint32_t)a.ldx), last));
   }
-  if ((int)threadIdx.x < width) slab[cin * width + threadIdx.x] = 0;
+}
+// Those of the tokens `mask` into the slab, from column col on.
+__device__ __forceinline__ void put_x(const MoeArgs& a, uint32_t mask, int g, int c0, int col, int width, u32x4 (&v)[kHeld],
+                                      uint16_t* slab) {
+  const int tid = own_thread();
+  const uint32_t some = ((mask >> g) & 255u) << (g - first_token(a, g));
+  if (a.n_tokens < 8) {
+    const int64_t last = (int64_t)(a.up.cin - 1) * a.ldx + a.n_tokens - 8;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const uint32_t c = min(c0 + tid + u * kThreads, a.up.cin - 1);
+      v[u] = shifted_row(v[u], (int)max((int64_t)((uint64_t)c * (uint32_t)a.ldx) - last, (int64_t)0));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const int c = c0 + tid + u * kThreads;
+    if (c >= a.up.cin) break;
+    int j = col;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if ((some >> t) & 1u) slab[c * width + j++] = (uint16_t)(v[u][t >> 1] >> (16 * (t & 1)));
+  }
 }
 
-// Items are (segment, 32 rows of the inner channels), a contiguous range of
-// them a workgroup: of 64 rows, the 344 items of a token's two experts of 11008
-// channels left the busiest of 256 workgroups two.
+// Items are (segment, 32 rows of the inner channels): of 64 rows, the 344 items
+// of a token's two experts of 11008 channels left the busiest of 256 workgroups
+// two.
 template <int VALUES>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
-  constexpr int F = 2, R = 16 * F;
+  constexpr int F = 2, R = 16 * F, kPitch = sums_pitch(F), kDepth = VALUES == HINM_VALUES_BF16 ? 4 : 6;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
   __shared__ __attribute__((aligned(16))) union {
-    float red[kWaves * kRed];
+    float red[kWaves * kPitch];
     RouteScratch route;
   } sh;
   __shared__ int n_seg;
   __shared__ Seg segs[kPairs];
-  __shared__ uint16_t token[kPairs];
-  route_tokens(a, sh.route, &n_seg, segs, token, blockIdx.x == 0 ? a.table : nullptr);
+  u32x4 v[kHeld];
+  // the first loads of up to eight tokens' activations need no routing
+  bool early = a.n_tokens <= 8;
+  if (early) load_x(a, 0, 0, v);
+  route_tokens(a, sh.route, &n_seg, segs, blockIdx.x == 0 ? a.table : nullptr);
 
-  const int wave = uniform(threadIdx.x >> 6);
-  const int n_rb = a.up.cout / R, all = uniform(n_seg) * n_rb;     // at most 512 * 512
-  const int i0 = (int)((int64_t)blockIdx.x * all / kCus), i1 = (int)((int64_t)(blockIdx.x + 1) * all / kCus);
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const unsigned n_rb = a.up.cout / R;
+  const Share mine = share_of(uniform(n_seg), n_rb);               // at most 512 * 512 items
   const MoeStack& w = wave < kWaves / 2 ? a.gate : a.up;
-  int held = -1;
+  const int nd = w.nkb_d;
+  int held = -1, coming = -1, rb = 0, pitch = 8;
   Seg seg{};                       // of the item at hand
-  int rb = 0;
-  stream<VALUES, F, kWaves / 2>(
-      w, i1 - i0, wave % (kWaves / 2), slab,
-      [&](int i) -> Item {
-        const int sg = (i0 + i) / n_rb;
-        return {uniform(segs[sg].expert), (i0 + i - sg * n_rb) * F, 0, w.nkb_d + w.nkb_s};
+  f32x4 acc[F];
+  auto seg_at = [&](unsigned sg) -> Seg {
+    const Seg t = segs[sg];
+    return {(uint32_t)uniform(t.mask), (uint16_t)uniform(t.expert), (uint16_t)uniform(t.down), (uint8_t)uniform(t.n), (uint8_t)uniform(t.rank0)};
+  };
+  auto group_of = [](uint32_t mask) { return __builtin_ctz(mask) & ~7; };
+  stream<Operand<VALUES, F>, Source, kDepth, kWaves / 2>(
+      (int)mine.n,
+      [&](int i) -> Source {
+        const unsigned sg = (mine.first + i) / n_rb;
+        const Seg next = seg_at(sg);
+        if ((int)sg != coming) {
+          coming = sg;
+          if (!early) load_x(a, group_of(next.mask), 0, v);
+          early = false;
+        }
+        return source_of(w, {next.expert, (int)(mine.first + i - sg * n_rb) * F, 0, nd + w.nkb_s}, wave % (kWaves / 2));
+      },
+      [&](const Source& s, int b, Operand<VALUES, F>& o) {
+        o.index = load_index(w, s, b);
+        load_block<VALUES, F>(w, s, b, o);
+      },
+      [&](int b, const Operand<VALUES, F>& o) {
+        const int row = ((uint32_t)o.index < (uint32_t)w.cin ? o.index : w.cin) * pitch;
+        multiply_block<VALUES, F>(b < nd, o, pitch, [&](int p) { return slab + __shfl(row, p); }, acc);
       },
       [&](int i) {
-        const int sg = (i0 + i) / n_rb;
-        rb = i0 + i - sg * n_rb;
-        if (sg != held) {
-          seg = uniform_seg(segs[sg]);
-          __syncthreads();
-          load_tokens(a, seg, token, reinterpret_cast<uint16_t*>(slab));
-          __syncthreads();
+        const unsigned sg = (mine.first + i) / n_rb;
+        rb = mine.first + i - sg * n_rb;
+        if ((int)sg != held) {
           held = sg;
-        }
-        return 2 * row_columns(seg.n);
-      },
-      [&](int, f32x4 (&acc)[F]) {
-        const int width = row_columns(seg.n);
+          seg = seg_at(sg);
+          const int width = row_columns(seg.n);
+          pitch = 2 * width;
+          uint32_t left = seg.mask;
+          int col = 0, g = group_of(left);
 #pragma nounroll
-        for (int r0 = 0; r0 < R; r0 += 256 / width) {
-          put_sums<F>(sh.red, acc, r0, width);
-          __syncthreads();
-          // of four adjacent threads the first two have the gate's sum, the others the up projection's
-          float g = four_sums(sh.red);
-          g += quad1(g);
-          const float u = quad2(g);
-          const int e = threadIdx.x >> 2, row = r0 + e / width, col = e % width;
-          if ((threadIdx.x & 3) == 0 && col < seg.n && row < R) {
-            // where the down kernel's segment of this token has it
-            const int rank = seg.rank0 + col, q = rank / a.down_cap;
-            const int wide = row_columns(2 * min(a.down_cap, seg.count - q * a.down_cap));
-            const float h = g / (1.f + expf(-g)) * u;
-            const uint16_t hi = to_bf16(h);
-            uint16_t* dst = a.h + (seg.down + q) * a.h_seg + (int64_t)(rb * R + row) * wide + rank - q * a.down_cap;
-            dst[0] = hi;
-            dst[wide / 2] = to_bf16(h - __uint_as_float((uint32_t)hi << 16));
+          for (int c0 = 0;;) {
+            put_x(a, left, g, c0, col, width, v, reinterpret_cast<uint16_t*>(slab));
+            c0 += kHeld * kThreads;
+            if (c0 >= a.up.cin) {
+              col += __popc((left >> g) & 255u);
+              left &= ~(255u << g);
+              if (!left) break;
+              g = group_of(left);
+              c0 = 0;
+            }
+            load_x(a, g, c0, v);
           }
-          __syncthreads();
+          const int tid = own_thread();
+          if (tid < width) reinterpret_cast<uint16_t*>(slab)[a.up.cin * width + tid] = 0;
+          step_barrier();
         }
+#pragma unroll
+        for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+      },
+      [&](int) {
+        // a lane's sums of wave w, fragment f: red[w][f][lane]; of four adjacent threads the first two sum the gate's
+        // waves, the others the up projection's, and each makes one row's h
+#pragma unroll
+        for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(sh.red + wave * kPitch + 256 * f + 4 * lane) = acc[f];
+        step_barrier();
+        const int tid = own_thread(), part = tid & 3, t = tid >> 2;
+        const f32x4 s = *reinterpret_cast<const f32x4*>(sh.red + 2 * part * kPitch + 4 * t) +
+                        *reinterpret_cast<const f32x4*>(sh.red + (2 * part + 1) * kPitch + 4 * t);
+        float own = 0.f, other = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x = s[q] + quad1(s[q]), y = quad2(x);
+          if (q == part) own = x, other = y;
+        }
+        const float g = part < 2 ? own : other, u = part < 2 ? other : own;
+        const int col = t & 15, row = 16 * (t >> 6) + 4 * ((t >> 4) & 3) + part;
+        if (col < seg.n) {
+          // where the down kernel's segment of this token has it
+          const int rank = seg.rank0 + col, cap = a.wide / 2, q = rank / cap;
+          const float h = g / (1.f + expf(-g)) * u;
+          const uint16_t hi = to_bf16(h);
+          uint16_t* const dst = a.h + (seg.down + q) * a.h_seg + rank - q * cap;
+          uint16_t* const at = dst + (rb * R + row) * a.wide;
+          at[0] = hi;
+          at[cap] = to_bf16(h - __uint_as_float((uint32_t)hi << 16));
+          if (rb == 0 && row == 0) dst[a.up.cout * a.wide] = dst[a.up.cout * a.wide + cap] = 0;
+        }
+        step_barrier();
       });
 }
 
-template <int VALUES>
+// A workgroup's K-blocks are a contiguous range of those of all segments, its
+// items the parts of it in one segment.  In a turn of kDepth blocks a wave
+// multiplies those whose rows and values it asked for a turn before, asks for
+// the rows and values of the next ones, by indices that it asked for a turn
+// before, and for the indices of those after.  No load is under a condition:
+// waits are for a known number of loads.
+template <int VALUES, int WIDE>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
-  constexpr int F = 4;
-  __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
-  __shared__ float red[kWaves * kRed];
-  __shared__ float out[64 * kTokens];
+  constexpr int F = 4, kPitch = sums_pitch(F), kDepth = 4, kRow = 2 * WIDE, kSlot = 64 * kRow;
+  typedef std::conditional_t<WIDE == 4, u32x2, u32x4> Piece;
+  constexpr int kPieces = kRow / sizeof(Piece);
+  __shared__ __attribute__((aligned(16))) uint8_t slots[kWaves * 2 * kSlot];
+  __shared__ __attribute__((aligned(16))) float red[kWaves * kPitch];
+  __shared__ float out[64 * kTokens];              // [row][token]
   __shared__ Table table;
   __shared__ int s_last;
-  static_assert(sizeof(Table) % 4 == 0 && sizeof(Table) / 4 <= 2 * kThreads, "the table is two words a thread");
-#pragma unroll
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   for (int q = threadIdx.x; q < (int)sizeof(Table) / 4; q += kThreads)
     reinterpret_cast<uint32_t*>(&table)[q] = reinterpret_cast<const uint32_t*>(a.table)[q];
   __syncthreads();
-  const int wave = uniform(threadIdx.x >> 6);
-  const int n_rb = a.down.cout / 64, nblk = a.down.nkb_d + a.down.nkb_s, n_seg = uniform(table.n_seg);
-  const int units = n_seg * nblk;
+  const MoeStack& w = a.down;
+  const int n_rb = w.cout / 64, nd = w.nkb_d, nblk = nd + w.nkb_s, n_seg = uniform(table.n_seg), units = n_seg * nblk;
   // shares of a row block's K-blocks: as many as leave no compute unit idle, and a block for each wave
   const int splits = max(1, min(kCus / n_rb, units / kWaves));
+  uint8_t* const slot = slots + wave * 2 * kSlot;
 #pragma nounroll
   for (int item = blockIdx.x; item < n_rb * splits; item += kCus) {
     const int rb = item / splits, split = item % splits;
-    // whole segments in turn (an expert's are adjacent: they share its weights in the caches), then an even share of
-    // the remaining ones' blocks
-    const int rounds = n_seg / splits, rest = (n_seg - rounds * splits) * nblk, r0 = rounds * splits * nblk;
-    const int u0 = r0 + split * rest / splits, u1 = r0 + (split + 1) * rest / splits;
-    const int s0 = u0 / nblk, parts = u0 < u1 ? (u1 - 1) / nblk - s0 + 1 : 0;
-    for (int q = threadIdx.x; q < 64 * kTokens; q += kThreads) out[q] = 0.f;
-    auto seg_of = [&](int i) { return i < rounds ? i * splits + split : s0 + i - rounds; };
-    int n = 0, slot = 0;           // tokens of the segment at hand, and the first one's slot
-    stream<VALUES, F, kWaves>(
-        a.down, rounds + parts, wave, slab,
-        [&](int i) -> Item {
-          const int sg = seg_of(i);
-          return {uniform(table.seg[sg] & 1023), rb * F, i < rounds ? 0 : max(0, u0 - sg * nblk),
-                  i < rounds ? nblk : min(nblk, u1 - sg * nblk)};
-        },
-        [&](int i) {
-          const int sg = seg_of(i), word = uniform((int)table.seg[sg]);
-          slot = word >> 10 & 1023;
-          n = word >> 20;
-          const int pitch = 2 * row_columns(2 * n);
-          const u32x4* src = reinterpret_cast<const u32x4*>(a.h + sg * a.h_seg);
-          const int words = a.down.cin * pitch / 16;         // cin is a multiple of 64
-          __syncthreads();
-          constexpr int U = 4;
+    const int u0 = split * units / splits, u1 = (split + 1) * units / splits;      // below 2^20 * splits
+    const int s0 = n_seg ? u0 / nblk : 0, parts = u0 < u1 ? (u1 - 1) / nblk - s0 + 1 : 0;
+    for (int q = threadIdx.x; q < 64 * a.n_tokens; q += kThreads) out[q] = 0.f;
+    step_barrier();
+    auto source = [&](int i) {
+      const int sg = s0 + i;
+      return source_of(w, {uniform(table.seg[sg] & 1023), rb * F, max(0, u0 - sg * nblk), min(nblk, u1 - sg * nblk)}, wave);
+    };
+    auto turns_of = [&](const Source& s) { return max(1, (s.end - s.first + kDepth * kWaves - 1) / (kDepth * kWaves)); };
+    f32x4 acc[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto finish = [&](int i) {
+      const int word = uniform((int)table.seg[s0 + i]), first = word >> 10 & 1023, n = word >> 20;
+#pragma unroll
+      for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(red + wave * kPitch + 256 * f + 4 * lane) = acc[f];
+      step_barrier();
+      const int tid = own_thread(), part = tid & 1, t = tid >> 1;    // four waves' sums of fragment t / 64, lane t % 64
+      f32x4 s = *reinterpret_cast<const f32x4*>(red + 4 * part * kPitch + 4 * t);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) s += *reinterpret_cast<const f32x4*>(red + (4 * part + k) * kPitch + 4 * t);
+      const int col = t & 15, row = 16 * (t >> 6) + 4 * ((t >> 4) & 3);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x = s[q] + quad1(s[q]);
+        x += __shfl_down(x, WIDE);                 // the token's other column, WIDE / 2 further on
+        if ((q & 1) == part && col < n) out[(row + q) * a.n_tokens + table.token[first + col]] += table.weight[first + col] * x;
+        acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      step_barrier();
+    };
+    if (parts > 0) {
+      Operand<VALUES, F> o[kDepth];
+      Piece rows[kDepth][kPieces];
+      int index[kDepth], asked[kDepth], block[kDepth];       // blocks; ~b: block b, not to be multiplied
+      int seg_i = 0;                                         // the item that indices are asked of
+      Source src = source(0), from;
+      int turns = turns_of(src), ends = -1, last = -1;       // items that the turns of rows and of products end
+      const uint8_t* h_src = reinterpret_cast<const uint8_t*>(a.h + s0 * a.h_seg);
+      const uint8_t* h_from = h_src;
+      auto ask = [&](int k) {
+        const int b = min(src.first, src.end - 1);
+        index[k] = load_index(w, src, b);
+        asked[k] = src.first < src.end ? b : ~b;
+        src.first += kWaves;
+      };
+      // ends the turn of indices: which item it ends, and on to the next one
+      auto turn = [&] {
+        from = src;
+        h_from = h_src;
+        ends = -1;
+        if (--turns > 0) return;
+        turns = 1;
+        if (seg_i < parts) ends = seg_i;
+        if (++seg_i < parts) {
+          src = source(seg_i);
+          turns = turns_of(src);
+          h_src += 2 * a.h_seg;
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < kDepth; ++k) {
+        ask(k);
+        block[k] = -1;
+      }
+      turn();
 #pragma nounroll
-          for (int q0 = threadIdx.x; q0 < words; q0 += U * kThreads) {
-            u32x4 v[U];
+      while (true) {
+        const int ended = last;
+        last = ends;
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = src[min(q0 + u * kThreads, words - 1)];
+        for (int k = 0; k < kDepth; ++k) {
+          if (block[k] >= 0) {
+            uint8_t* const to = slot + (k & 1) * kSlot;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-              if (q0 + u * kThreads < words) reinterpret_cast<u32x4*>(slab)[q0 + u * kThreads] = v[u];
+            for (int u = 0; u < kPieces; ++u) *reinterpret_cast<Piece*>(to + lane * kRow + u * sizeof(Piece)) = rows[k][u];
+            multiply_block<VALUES, F>(block[k] < nd, o[k], kRow, [&](int p) { return to + p * kRow; }, acc);
           }
-          if ((int)threadIdx.x < pitch / 2) reinterpret_cast<uint16_t*>(slab)[a.down.cin * (pitch / 2) + threadIdx.x] = 0;
-          __syncthreads();
-          return pitch;
-        },
-        [&](int, f32x4 (&acc)[F]) {
-          const int width = row_columns(2 * n);
-#pragma nounroll
-          for (int r = 0; r < 64; r += 256 / width) {
-            put_sums<F>(red, acc, r, width);
-            __syncthreads();
-            float s = four_sums(red);
-            s += quad1(s);
-            s += quad2(s);
-            s += __shfl_xor(s, 2 * width);                   // the other of the token's two columns
-            const int e = threadIdx.x >> 2, row = r + e / width, col = e % width;
-            if ((threadIdx.x & 3) == 0 && col < n) out[row * kTokens + table.token[slot + col]] += table.weight[slot + col] * s;
-            __syncthreads();
-          }
-        });
-    __syncthreads();
-    constexpr int N = 64 * kTokens / kThreads;     // outputs a thread
-    float v[N];
+          block[k] = asked[k];
+          const int b = asked[k] < 0 ? ~asked[k] : asked[k];
+          const uint32_t row = (uint32_t)index[k] < (uint32_t)w.cin ? index[k] : w.cin;
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = out[k * kThreads + threadIdx.x];
-    bool last = true;
+          for (int u = 0; u < kPieces; ++u) rows[k][u] = at<Piece>(h_from, row * kRow + u * sizeof(Piece));
+          load_block<VALUES, F>(w, from, b, o[k]);
+          ask(k);
+        }
+        turn();
+        if (ended >= 0) {
+          finish(ended);
+          if (ended == parts - 1) break;
+        }
+      }
+    }
+    const int outs = 64 * a.n_tokens;
+    bool leave = false;
+    float* const part0 = a.part + (int64_t)rb * splits * 64 * kTokens;
     if (splits > 1) {
-      float* my = a.part + (int64_t)item * 64 * kTokens + threadIdx.x;
-#pragma unroll
-      for (int k = 0; k < N; ++k) __hip_atomic_store(my + k * kThreads, v[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      float* const my = part0 + (int64_t)split * 64 * kTokens;
+      for (int q = threadIdx.x; q < outs; q += kThreads) __hip_atomic_store(my + q, out[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
       if (threadIdx.x == 0) s_last = arrive(a.counters + rb, splits);
       __syncthreads();
-      last = s_last;
-      if (last) {
-        const float* p0 = a.part + (int64_t)rb * splits * 64 * kTokens + threadIdx.x;
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = 0.f;
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s)
-#pragma unroll
-          for (int k = 0; k < N; ++k)
-            v[k] += __hip_atomic_load(p0 + (int64_t)s * 64 * kTokens + k * kThreads, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      leave = !s_last;
     }
-    if (last)
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int q = k * kThreads + threadIdx.x, row = q / kTokens, col = q % kTokens;
-        if (col < a.n_tokens) a.y[((int64_t)rb * 64 + row) * a.ldy + col] = to_bf16(v[k]);
+    if (!leave)
+      for (int q = threadIdx.x; q < outs; q += kThreads) {
+        float v = splits > 1 ? 0.f : out[q];
+        if (splits > 1)
+#pragma unroll 4
+          for (int s = 0; s < splits; ++s)
+            v += __hip_atomic_load(part0 + (int64_t)s * 64 * kTokens + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const unsigned row = (unsigned)q / (unsigned)a.n_tokens, col = q - row * a.n_tokens;
+        a.y[((int64_t)rb * 64 + row) * a.ldy + col] = to_bf16(v);
       }
     __syncthreads();
   }
 }
 
-// Columns a segment holds at most: as many as fit in LDS.  A token takes one in
-// the up kernel and two in the down kernel.
+// Tokens that a segment of the up kernel holds at most: as many as fit in LDS.
 int columns_of(int channels) { return (channels + 1) * 32 <= kSlab ? 16 : (channels + 1) * 16 <= kSlab ? 8 : 4; }
+
+// Columns of h, twice the tokens of a segment of the down kernel: of 16 its
+// products use what there is, but of up to two tokens rows of 8 bytes are fewer
+// loads.
+int wide_of(int64_t n_tokens) { return n_tokens <= 2 ? 4 : 16; }
 
 struct Workspace {
   int64_t table, part, h, h_seg, bytes;            // offsets; h_seg in elements
@@ -684,13 +688,13 @@ struct Workspace {
 Workspace workspace_of(int hidden, int inter, int32_t n_experts, int64_t n_tokens, int32_t top_k) {
   Workspace w{};
   if (n_tokens == 0) return w;
-  const int64_t pairs = n_tokens * top_k, columns = columns_of(inter);
-  const int64_t segs = std::min(pairs, std::min<int64_t>(n_experts, pairs) + pairs / (columns / 2));
+  const int64_t pairs = n_tokens * top_k, wide = wide_of(n_tokens);
+  const int64_t segs = std::min(pairs, std::min<int64_t>(n_experts, pairs) + pairs / (wide / 2));
   w.table = hinm::kWsCounterBytes;
   w.part = w.table + (int64_t)((sizeof(Table) + 255) / 256 * 256);
   const int64_t items = std::max<int64_t>(kCus, hidden / 64);
   w.h = w.part + items * 64 * kTokens * 4;
-  w.h_seg = (int64_t)inter * columns;
+  w.h_seg = (int64_t)(inter + 1) * wide;
   w.bytes = w.h + (segs * w.h_seg * 2 + 255) / 256 * 256;
   return w;
 }
@@ -782,7 +786,8 @@ int plan_of(const char* whose, const void* stack, const hinm_plan_t*& p) {
 template <int VALUES>
 void launch(const MoeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(moe_up_kernel<VALUES>, dim3(kCus), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL(moe_down_kernel<VALUES>, dim3(kCus), dim3(kThreads), 0, stream, a);
+  if (a.wide == 4) hipLaunchKernelGGL((moe_down_kernel<VALUES, 4>), dim3(kCus), dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((moe_down_kernel<VALUES, 16>), dim3(kCus), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -821,6 +826,7 @@ extern "C" int hinm_moe_layer(const void* logits, int32_t logits_type, int64_t l
   if (ldl < n_tokens || ldx < n_tokens || ldy < n_tokens)
     return fail(HINM_ESHAPE, "ldl=%lld, ldx=%lld and ldy=%lld must be >= the %lld tokens", (long long)ldl, (long long)ldx,
                 (long long)ldy, (long long)n_tokens);
+  if (ldx >= (int64_t)1 << 31) return fail(HINM_ESHAPE, "ldx=%lld must be below 2^31", (long long)ldx);
   if (n_tokens == 0) return HINM_OK;
   if (!logits || !x_bf16 || !y_bf16) return fail(HINM_EINVAL, "logits, x and y must be non-NULL");
   if (!hinm::aligned(logits, logits_type == HINM_FP32 ? 4 : 2) || !hinm::aligned(x_bf16, 2) || !hinm::aligned(y_bf16, 2))
@@ -854,7 +860,7 @@ extern "C" int hinm_moe_layer(const void* logits, int32_t logits_type, int64_t l
   a.top_k = top_k;
   a.renormalize = renormalize != 0;
   a.up_cap = columns_of(pu->cin);
-  a.down_cap = columns_of(pu->cout) / 2;
+  a.wide = wide_of(n_tokens);
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
   if (values == HINM_VALUES_BF16) launch<HINM_VALUES_BF16>(a, stream);
   else if (values == HINM_VALUES_MX4) launch<HINM_VALUES_MX4>(a, stream);

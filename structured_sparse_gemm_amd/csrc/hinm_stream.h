@@ -4,6 +4,7 @@
 #define HINM_STREAM_H_
 
 #include "hinm_device.h"
+#include "hinm_ragged.h"
 
 namespace {
 
@@ -38,9 +39,7 @@ __device__ inline const uint8_t* pick(bool c, const uint8_t* a, const uint8_t* b
 //   multiply(b, o) adds its products;
 //   begin(i), finish(i): before its first and after its last product, in step
 //                 for the whole workgroup.
-// One loop body serves the first loads, the products and the items' ends: a
-// launch fetches every instruction from memory once, at some 2 cycles a byte,
-// and the kernels that use this last only a few times as long.
+// One loop body serves the first loads, the products and the items' ends.
 template <class Operand, class Source, int DEPTH, int NW, class Open, class Load, class Multiply, class Begin, class Finish>
 __device__ __forceinline__ void stream(int items, Open open, Load load, Multiply multiply, Begin begin, Finish finish) {
   if (items <= 0) return;
@@ -75,6 +74,39 @@ __device__ __forceinline__ void stream(int items, Open open, Load load, Multiply
       begin(ahead);
     }
   }
+}
+
+// A workgroup's share of the items (segment, row block), of kCus workgroups: a
+// contiguous range.  Up to 32 segments share the workgroups out among
+// themselves, since to ready a segment's activations costs as much as several
+// items, and a range that runs on into the next segment does it twice (8
+// experts of 11008 x 4096, 16 tokens each: 60 us, against 43); of more the
+// shares would differ by more than that (100 segments: 2 or 3 workgroups each).
+struct Share {
+  unsigned first, n;               // items: number segment * n_rb + row block
+};
+__device__ inline Share share_of(unsigned segs, unsigned n_rb) {
+  const unsigned wg = blockIdx.x;
+  if (segs == 0) return {0, 0};
+  if (segs > 32) {
+    const unsigned all = segs * n_rb;
+    auto upto = [&](unsigned b) { return all / kCus * b + all % kCus * b / kCus; };
+    return {upto(wg), upto(wg + 1) - upto(wg)};
+  }
+  const unsigned sg = wg * segs / kCus;
+  const unsigned first = (sg * kCus + segs - 1) / segs, n = ((sg + 1) * kCus + segs - 1) / segs - first;
+  auto upto = [&](unsigned j) { return n_rb / n * j + n_rb % n * j / n; };
+  return {sg * n_rb + upto(wg - first), upto(wg - first + 1) - upto(wg - first)};
+}
+
+// Eight of X's bf16 values of which the first is wanted at element `past`, of 0 .. 7.
+__device__ inline u32x4 shifted_row(u32x4 v, int past) {
+  if (past & 4) v[0] = v[2], v[1] = v[3];
+  if (past & 2) v[0] = v[1], v[1] = v[2], v[2] = v[3];
+  if (past & 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = v[k] >> 16 | (k < 3 ? v[k + 1] << 16 : 0u);
+  return v;
 }
 
 // The value of lane ^ 1 or ^ 2.
