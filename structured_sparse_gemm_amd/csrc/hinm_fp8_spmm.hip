@@ -655,6 +655,7 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
 template <int F, bool TOKEN>
 __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int columns) {
   const int width = TOKEN ? 8 : columns;
+  touch(a);
   constexpr int kDepth = F == 1 ? 8 : F == 2 ? 6 : 4;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kDecLds];
   __shared__ __attribute__((aligned(16))) uint32_t top[kDecWaves * 8];

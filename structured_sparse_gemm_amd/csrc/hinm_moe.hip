@@ -244,6 +244,9 @@ __device__ inline float logit_of(uint32_t key) { return __uint_as_float((int)key
 // broadcasts between them), and the wave's sum.
 template <int CTRL>
 __device__ inline uint32_t shifted(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false); }
+// Of those broadcasts, lanes of the rows of 16 in ROWS alone.
+template <int CTRL, int ROWS>
+__device__ inline uint32_t to_row(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false); }
 __device__ inline uint32_t wave_max(uint32_t v) {
   v = max(v, shifted<0x111>(v));
   v = max(v, shifted<0x112>(v));
@@ -260,9 +263,9 @@ __device__ inline float wave_sum(float v) {
 
 // Token n's experts and weights; NL keys a lane, expert 64 i + lane.
 template <int NL>
-__device__ inline void route_token(const MoeArgs& a, RouteScratch& r, int n) {
+__device__ __forceinline__ void load_logits(const MoeArgs& a, int n, uint32_t (&raw)[NL]) {
   const int lane = threadIdx.x & 63;
-  uint32_t raw[NL];
+  n = min(n, a.n_tokens - 1);
   if (a.logits_fp32) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) raw[i] = static_cast<const uint32_t*>(a.logits)[min(64 * i + lane, a.n_experts - 1) * a.ldl + n];
@@ -270,6 +273,10 @@ __device__ inline void route_token(const MoeArgs& a, RouteScratch& r, int n) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) raw[i] = static_cast<const uint16_t*>(a.logits)[min(64 * i + lane, a.n_experts - 1) * a.ldl + n];
   }
+}
+template <int NL>
+__device__ __forceinline__ void route_token(const MoeArgs& a, RouteScratch& r, int n, const uint32_t (&raw)[NL]) {
+  const int lane = threadIdx.x & 63;
   uint32_t key[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) key[i] = 64 * i + lane < a.n_experts ? key_of(__uint_as_float(a.logits_fp32 ? raw[i] : raw[i] << 16)) : 0u;
@@ -315,17 +322,27 @@ __device__ inline void route_token(const MoeArgs& a, RouteScratch& r, int n) {
 }
 
 // The up kernel's segments go to `seg`, their number to n_seg; down (one
-// workgroup's): the table for the down kernel.
-__device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_seg, Seg* seg, Table* down) {
+// workgroup's): the table for the down kernel.  meanwhile() runs while the
+// first logits come.
+template <class Meanwhile>
+__device__ __forceinline__ void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_seg, Seg* seg, Table* down, Meanwhile meanwhile) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), down_cap = a.wide / 2;
   for (int e = threadIdx.x; e < a.n_experts; e += kThreads) r.mask[e] = 0u;
-  __syncthreads();
-  for (int n = wave; n < a.n_tokens; n += kWaves) {
-    if (a.n_experts <= 64) route_token<1>(a, r, n);
-    else if (a.n_experts <= 256) route_token<4>(a, r, n);
-    else route_token<HINM_MAX_EXPERTS / 64>(a, r, n);
-  }
-  __syncthreads();
+  auto tokens = [&](auto count) {
+    constexpr int NL = decltype(count)::value;
+    uint32_t raw[NL];
+    load_logits<NL>(a, wave, raw);
+    meanwhile();
+    step_barrier();                                // the masks are clear
+    for (int n = wave; n < a.n_tokens; n += kWaves) {
+      if (n != wave) load_logits<NL>(a, n, raw);
+      route_token<NL>(a, r, n, raw);
+    }
+  };
+  if (a.n_experts <= 64) tokens(std::integral_constant<int, 1>{});
+  else if (a.n_experts <= 256) tokens(std::integral_constant<int, 4>{});
+  else tokens(std::integral_constant<int, HINM_MAX_EXPERTS / 64>{});
+  step_barrier();
   // slots by expert and token, and the segments of both kernels; the three running counts (each at most kPairs) share
   // a word
   if (wave == 0) {
@@ -336,11 +353,13 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
       const int c = e < a.n_experts ? __popc(r.mask[e]) : 0;
       const int nu = (c + a.up_cap - 1) / a.up_cap, nd = (c + down_cap - 1) / down_cap;
       const uint32_t own = (uint32_t)c | (uint32_t)nu << 10 | (uint32_t)nd << 20;
-      uint32_t all = own;
-      for (int d = 1; d < 64; d *= 2) {
-        const uint32_t v = __shfl_up(all, d);
-        if (lane >= d) all += v;
-      }
+      uint32_t all = own;                          // over the lanes up to this one
+      all += shifted<0x111>(all);
+      all += shifted<0x112>(all);
+      all += shifted<0x114>(all);
+      all += shifted<0x118>(all);
+      all += to_row<0x142, 0xa>(all);
+      all += to_row<0x143, 0xc>(all);
       const uint32_t at = before + all - own;
       const int s0 = at & 1023, u0 = at >> 10 & 1023, d0 = at >> 20;
       if (e < a.n_experts) r.start[e] = (uint16_t)s0;
@@ -355,14 +374,14 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
       if (down)
         for (int q = 0; q < nd; ++q)
           down->seg[d0 + q] = (uint32_t)e | (uint32_t)(s0 + q * down_cap) << 10 | (uint32_t)min(down_cap, c - q * down_cap) << 20;
-      before += __shfl(all, 63);
+      before += (uint32_t)__builtin_amdgcn_readlane((int)all, 63);
     }
     if (lane == 0) {
       *n_seg = before >> 10 & 1023;
       if (down) down->n_seg = before >> 20;
     }
   }
-  __syncthreads();
+  step_barrier();
   if (down && (int)threadIdx.x < a.n_tokens * a.top_k) {
     const int e = r.id[threadIdx.x], n = threadIdx.x / a.top_k;
     if (e >= 0) {
@@ -371,7 +390,7 @@ __device__ inline void route_tokens(const MoeArgs& a, RouteScratch& r, int* n_se
       down->weight[slot] = r.weight[threadIdx.x];
     }
   }
-  __syncthreads();
+  step_barrier();
 }
 
 // X's values of eight tokens, g .. g + 7 (of fewer than eight the rows' first
@@ -394,23 +413,22 @@ __device__ __forceinline__ void put_x(const MoeArgs& a, uint32_t mask, int g, in
                                       uint16_t* slab) {
   const int tid = own_thread();
   const uint32_t some = ((mask >> g) & 255u) << (g - first_token(a, g));
-  if (a.n_tokens < 8) {
-    const int64_t last = (int64_t)(a.up.cin - 1) * a.ldx + a.n_tokens - 8;
+  uint16_t* at[kHeld];                             // past the last channel that one again, and its values
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const uint32_t c = min(c0 + tid + u * kThreads, a.up.cin - 1);
-      v[u] = shifted_row(v[u], (int)max((int64_t)((uint64_t)c * (uint32_t)a.ldx) - last, (int64_t)0));
+  for (int u = 0; u < kHeld; ++u) {
+    const int c = min(c0 + tid + u * kThreads, a.up.cin - 1);
+    at[u] = slab + c * width + col;
+    if (a.n_tokens < 8) {
+      const int64_t past = (int64_t)((uint64_t)(uint32_t)c * (uint32_t)a.ldx) - ((int64_t)(a.up.cin - 1) * a.ldx + a.n_tokens - 8);
+      if (__ballot(past > 0)) v[u] = shifted_row(v[u], (int)max(past, (int64_t)0));
     }
   }
 #pragma unroll
-  for (int u = 0; u < kHeld; ++u) {
-    const int c = c0 + tid + u * kThreads;
-    if (c >= a.up.cin) break;
-    int j = col;
+  for (int t = 0; t < 8; ++t)
+    if ((some >> t) & 1u) {
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if ((some >> t) & 1u) slab[c * width + j++] = (uint16_t)(v[u][t >> 1] >> (16 * (t & 1)));
-  }
+      for (int u = 0; u < kHeld; ++u) *at[u]++ = (uint16_t)(v[u][t >> 1] >> (16 * (t & 1)));
+    }
 }
 
 // Items are (segment, 32 rows of the inner channels): of 64 rows, the 344 items
@@ -426,11 +444,13 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
   } sh;
   __shared__ int n_seg;
   __shared__ Seg segs[kPairs];
+  touch(a);
   u32x4 v[kHeld];
   // the first loads of up to eight tokens' activations need no routing
   bool early = a.n_tokens <= 8;
-  if (early) load_x(a, 0, 0, v);
-  route_tokens(a, sh.route, &n_seg, segs, blockIdx.x == 0 ? a.table : nullptr);
+  route_tokens(a, sh.route, &n_seg, segs, blockIdx.x == 0 ? a.table : nullptr, [&] {
+    if (early) load_x(a, 0, 0, v);
+  });
 
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const unsigned n_rb = a.up.cout / R;
@@ -543,6 +563,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   __shared__ float out[64 * kTokens];              // [row][token]
   __shared__ Table table;
   __shared__ int s_last;
+  touch(a);
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   for (int q = threadIdx.x; q < (int)sizeof(Table) / 4; q += kThreads)
     reinterpret_cast<uint32_t*>(&table)[q] = reinterpret_cast<const uint32_t*>(a.table)[q];

@@ -13,6 +13,18 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 // A barrier that waits for this wave's LDS operations, not for its loads.
 __device__ inline void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Reads a word of every 64 bytes of a kernel's arguments, so that they are in
+// the scalar cache when they are wanted: they come from the host's memory, some
+// two thousand cycles for each part that is read for the first time, all at
+// once here.
+template <class Args>
+__device__ __forceinline__ void touch(const Args& a) {
+  uint32_t x = 0;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Args) + 63) / 64; ++i) x ^= reinterpret_cast<const uint32_t*>(&a)[16 * i];
+  asm volatile("" ::"s"(x));
+}
+
 // The thread's number, as a value that the compiler takes for new: what is
 // computed from it stays where it is used, and out of the code ahead of a loop
 // that uses it once.
