@@ -238,39 +238,68 @@ struct Work {
 };
 
 template <int NT>
-__device__ inline void multiply_weight(const Fp8Args& a, const Work w, uint8_t* lds, u32x4 rx, int n0,
-                                       const float (&xs)[Pre<NT>::NTB], f32x16 (&acc)[2][Pre<NT>::NTB]) {
+__device__ __forceinline__ void multiply_weight(const Fp8Args& a, const Work w, uint8_t* lds, u32x4 rx, int n0,
+                                                const float (&xs)[Pre<NT>::NTB], f32x16 (&acc)[2][Pre<NT>::NTB]) {
   using C = Pre<NT>;
   constexpr int NJ = 16 / C::RPL;              // X loads of a wave for 64 positions
   const int lane = threadIdx.x & 63, nb = w.nd + w.ns;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t* const ring = lds + kTiles * C::TILE;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)lds, ring0 = lds0 + kTiles * C::TILE;
+  // offsets in the rings move on by a step
+  auto next_tile = [](uint32_t& t) { t = t == (kTiles - 1) * C::TILE ? 0u : t + C::TILE; };
+  auto next_slot = [](uint32_t& t) { t = t == (kRing - 1) * kSlot ? 0u : t + kSlot; };
 
-  // Block b's bytes of the weight into its slot: waves 0 and 1 (and 3 again) half of the values each, wave 2 in lanes
-  // 0 .. 31 metadata (a dense block has none and reads values), 32 .. 35 scales, the others indices, the last sixteen
-  // bytes again where there are no more.
-  auto load_weight = [&](int b) {
-    const uint32_t slot = ring0 + (uint32_t)(b % kRing) * kSlot;
-    b = min(b, nb - 1);                        // past the end the last block again: waits are for known numbers of loads
-    const bool dense = b < w.nd;
-    int k = dense ? b + w.turn_d : b - w.nd + w.turn_s;
-    k = dense ? w.d0 + (k < w.nd ? k : k - w.nd) : w.k0 + (k < w.ns ? k : k - w.ns);
+  // The weight's blocks in the order of the loop, into a slot each: waves 0 and 1 (and 3 again) half of the values each,
+  // wave 2 in lanes 0 .. 31 metadata (a dense block has none and reads values), 32 .. 35 scales, the others indices, the
+  // last sixteen bytes again where there are no more.  A lane's address moves on by its stride; up to four runs of
+  // adjacent blocks, two a region, begin anew.  Past the end the last block is read again: waits are for known numbers
+  // of loads.
+  const uint32_t into = ring0 + (wave == 2 ? kMeta : 1024u * (wave == 1));
+  const uint8_t* src = nullptr;
+  uint32_t stride = 0, stride4 = 0;            // stride4: from the last block of four that share scales
+  uint32_t slot_w = 0;
+  int run = -1, left = 0, kw = 0;              // of the run; the block's number in its region
+  auto begin_run = [&] {
+    int first = 0;
+    do {
+      ++run;
+      const int n = run < 2 ? w.nd : w.ns, turn = run < 2 ? w.turn_d : w.turn_s;
+      first = (run & 1) ? 0 : turn;
+      left = (run & 1) ? turn : n - turn;
+    } while (left == 0);                       // some run follows: a block is left
+    const bool dense = run < 2;
+    kw = (dense ? w.d0 : w.k0) + first;
     const int nkb = dense ? a.nkb_d : a.nkb_s;
-    const int64_t kb = (int64_t)w.tile * nkb + k, row = kb * a.rows + w.rb * 64;
-    const uint8_t* val = (dense ? w.val_d : w.val_s) + row * 32;
-    if (wave != 2) {
-      lds_load(val + 1024 * (wave & 1) * (wave < 2) + 16 * lane, slot + 1024u * (wave & 1) * (wave < 2));
-    } else {
-      const int64_t group = (int64_t)w.tile * ((nkb + 3) / 4) + k / 4;
-      const uint8_t* scale = (dense ? w.scale_d : w.scale_s) + group * a.rows + w.rb * 64;
-      const uint8_t* index = (dense ? w.idx_d : w.idx_s) + kb * (dense ? 128 : 256);
-      const uint8_t* src = dense ? val : w.meta + row * 8;
-      uint32_t off = 16u * lane;
-      if (lane >= 32) src = scale, off -= 512u;
-      if (lane >= 36) src = index, off = 16u * min(lane - 36, dense ? 7 : 15);
-      lds_load(src + off, slot + kMeta);
+    const int64_t kb = (int64_t)w.tile * nkb + kw, row = kb * a.rows + w.rb * 64;
+    src = (dense ? w.val_d : w.val_s) + row * 32 + 1024 * (wave == 1) + 16 * lane;
+    stride = stride4 = a.rows * 32;
+    if (wave == 2) {
+      if (!dense) src = w.meta + row * 8 + 16 * lane, stride = stride4 = a.rows * 8;
+      if (lane >= 36) {
+        src = (dense ? w.idx_d : w.idx_s) + kb * (dense ? 128 : 256) + 16 * min(lane - 36, dense ? 7 : 15);
+        stride = stride4 = dense ? 128 : 256;
+      } else if (lane >= 32) {
+        src = (dense ? w.scale_d : w.scale_s) + ((int64_t)w.tile * ((nkb + 3) / 4) + kw / 4) * a.rows + w.rb * 64 + 16 * (lane - 32);
+        stride = 0;
+        stride4 = a.rows;
+      }
     }
+  };
+  int blocks = nb;                             // not asked for yet
+  auto load_weight = [&] {
+    if (blocks > 0) {
+      if (left == 0) {
+        begin_run();
+      } else {
+        src += (kw & 3) == 3 ? stride4 : stride;
+        ++kw;
+      }
+      --left;
+      --blocks;
+    }
+    lds_load(src, into + slot_w);
+    next_slot(slot_w);
   };
   // A wave stages 16 positions of a 2:4 block, or 8 of a dense one, RPL a load: load j those from first + RPL j on,
   // first a multiple of 8 or 16, so that turned() is the same for both.
@@ -281,21 +310,22 @@ __device__ inline void multiply_weight(const Fp8Args& a, const Work w, uint8_t* 
     const int n = n0 + 16 * (sl ^ turned<NT>(j * C::RPL + q));
     xoff[j] = n < a.ld8 ? (uint32_t)n : 0x80000000u;
   }
+  uint32_t tile_x = 0, slot_x = 0;
   auto load_x = [&](int b) {
-    const uint32_t tile = lds0 + (uint32_t)(b % kTiles) * C::TILE;
-    b = min(b, nb - 1);
-    const int* index = reinterpret_cast<const int*>(ring + (b % kRing) * kSlot + kIndex);
     auto rows = [&](auto count, int first) {
+      const int* index = reinterpret_cast<const int*>(ring + slot_x + kIndex) + first + q;
       int c[decltype(count)::value];
 #pragma unroll
-      for (int j = 0; j < decltype(count)::value; ++j) c[j] = index[first + j * C::RPL + q];
+      for (int j = 0; j < decltype(count)::value; ++j) c[j] = index[j * C::RPL];
 #pragma unroll
-      for (int j = 0; j < decltype(count)::value; ++j)
-        lds_load(rx, tile + (first + j * C::RPL) * NT,
-                 (uint32_t)c[j] < (uint32_t)a.cin ? (uint32_t)c[j] * (uint32_t)a.ld8 + xoff[j] : kOob);
+      for (int j = 0; j < decltype(count)::value; ++j)       // both factors are below 2^24
+        lds_load(rx, lds0 + tile_x + (first + j * C::RPL) * NT,
+                 (uint32_t)c[j] < (uint32_t)a.cin ? __umul24((uint32_t)c[j], (uint32_t)a.ld8) + xoff[j] : kOob);
     };
     if (b < w.nd) rows(std::integral_constant<int, NJ / 2>{}, wave * 8);
     else rows(std::integral_constant<int, NJ>{}, wave * 16);
+    next_tile(tile_x);
+    if (b < nb - 1) next_slot(slot_x);         // past the end the last block's rows again
   };
   // until all but block b's rows and `more` other loads have come
   auto wait_but = [&](int b, auto more) {
@@ -318,12 +348,13 @@ __device__ inline void multiply_weight(const Fp8Args& a, const Work w, uint8_t* 
     off24[j] = (uint32_t)(row24 * NT + 16 * (chunk ^ turned<NT>(row24)) + 8 * s8);
     off_dense[j] = (uint32_t)(row_dense * NT + 16 * (chunk ^ turned<NT>(row_dense)) + 8 * s8);
   }
+  uint32_t tile_c = 0, slot_c = 0;
   // Half h of instruction s takes the row's values 8 (2 h + s) .. + 7, so that a
   // lane's values of both instructions are 16 adjacent bytes.
-  auto compute = [&](int b) {
-    const bool dense = b < w.nd;
-    const uint8_t *xt = lds + (b % kTiles) * C::TILE, *slot = ring + (b % kRing) * kSlot;
-    const int second = dense ? 8 * NT : 16 * NT;
+  auto compute = [&](auto dense_block) {
+    constexpr bool dense = decltype(dense_block)::value;
+    constexpr int second = dense ? 8 * NT : 16 * NT;
+    const uint8_t *xt = lds + tile_c, *slot = ring + slot_c;
     // all of the block's LDS reads first: with two waves a SIMD little else hides their latency
     float scale[2];
     u32x4 v[2];
@@ -333,23 +364,22 @@ __device__ inline void multiply_weight(const Fp8Args& a, const Work w, uint8_t* 
     for (int r = 0; r < 2; ++r) {
       scale[r] = fp8_scale(slot[kScale + 32 * r + m32]);
       v[r] = *reinterpret_cast<const u32x4*>(slot + (32 * r + m32) * 32 + 16 * h);
-      m[r] = *reinterpret_cast<const uint32_t*>(slot + kMeta + (32 * r + m32) * 8 + 4 * h);
+      m[r] = dense ? 0x44444444u : *reinterpret_cast<const uint32_t*>(slot + kMeta + (32 * r + m32) * 8 + 4 * h);
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int j = 0; j < C::NTB; ++j) {
+      const uint8_t* const at = xt + (dense ? off_dense[j] : off24[j]);
 #pragma unroll
-      for (int j = 0; j < C::NTB; ++j)
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) raw[s][j][u] = tr_read8(xt + (dense ? off_dense[j] : off24[j]) + (s + 2 * u) * second);
+        for (int u = 0; u < 2; ++u) raw[s][j][u] = tr_read8(at + (s + 2 * u) * second);
+    }
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 av[2][2];
-    int sidx[2][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       av[r][0] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[r][0], v[r][1]}, scale[r]));
       av[r][1] = __builtin_bit_cast(bf16x8, fp8_expand(fp8_u32x2{v[r][2], v[r][3]}, scale[r]));
-      sidx[r][0] = dense ? 0x4444 : (int)m[r];
-      sidx[r][1] = dense ? 0x4444 : (int)(m[r] >> 16);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -360,29 +390,35 @@ __device__ inline void multiply_weight(const Fp8Args& a, const Work w, uint8_t* 
         const bf16x16 bv = __builtin_shufflevector(lo8, hi8, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          acc[r][j] = __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av[r][s], bv, acc[r][j], sidx[r][s], 0, 0);
+          acc[r][j] = __builtin_amdgcn_smfmac_f32_32x32x32_bf16(av[r][s], bv, acc[r][j], (int)(s ? m[r] >> 16 : m[r]), 0, 0);
       }
+    next_tile(tile_c);
+    next_slot(slot_c);
+  };
+  auto step = [&](int b, auto dense_block) {
+    __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
+    load_x(b + 2);
+    load_weight();
+    __builtin_amdgcn_s_setprio(0);
+    compute(dense_block);
+    wait_but(b + 2, std::integral_constant<int, 1>{});
+    step_barrier();
   };
 
   step_barrier();                              // LDS is free
   wait_vm<0>();                                // counted loads begin here
-  for (int b = 0; b < kRing - 1; ++b) load_weight(b);
+  for (int b = 0; b < kRing - 1; ++b) load_weight();
   wait_vm<kRing - 3>();                        // the indices of blocks 0 and 1
   step_barrier();
   load_x(0);
   load_x(1);
-  wait_but(min(1, nb - 1), std::integral_constant<int, 0>{});
+  wait_but(1, std::integral_constant<int, 0>{});
   step_barrier();
+  int b = 0;
 #pragma nounroll
-  for (int b = 0; b < nb; ++b) {
-    __builtin_amdgcn_s_setprio(2);             // the loads go out ahead of the other workgroup's arithmetic
-    load_x(b + 2);
-    load_weight(b + kRing - 1);
-    __builtin_amdgcn_s_setprio(0);
-    compute(b);
-    wait_but(min(b + 2, nb - 1), std::integral_constant<int, 1>{});
-    step_barrier();
-  }
+  for (; b < w.nd; ++b) step(b, std::true_type{});
+#pragma nounroll
+  for (; b < nb; ++b) step(b, std::false_type{});
   wait_vm<0>();                                // what was loaded past the end
 }
 
@@ -821,7 +857,7 @@ struct Workspace {
 Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   Workspace w{};
   if (n_cols == 0 || decode_width(p, n_experts, n_cols)) return w;
-  w.window = std::min(n_cols, std::max<int64_t>(256, ((int64_t)1 << 30) / p.cin / 256 * 256));
+  w.window = std::min({n_cols, (int64_t)1 << 23, std::max<int64_t>(256, ((int64_t)1 << 30) / p.cin / 256 * 256)});
   w.ld8 = w.window <= 128 ? 128 : ((w.window + 255) / 256 | 1) * 256;
   w.chunks = (int)std::min<int64_t>(kChunks, (p.cin + 63) / 64);
   const int nt = token_block(p, n_experts, n_cols);
