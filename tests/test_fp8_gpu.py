@@ -265,3 +265,91 @@ def test_graph_and_streams(n):
             ys.append(hinm.spmm(q, x))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in ys)
+
+
+@pytest.mark.parametrize("cin", [4096, 4100, 8192, 8196, 9428, 9432, 18860, 18864, 20000])
+def test_product_many_channels(cin):
+    """Channel counts at which LDS holds 16, 8 or no columns, and one pass of loads or more cover them."""
+    q = hinm.quantize_fp8(_packed(64, cin, 0.75, 0.55, seed=cin))
+    w = _dense(q)
+    for n in (1, 2, 7, 8, 9, 15, 16, 23, 40):
+        print(f"[fp8] channels {cin} n={n}", flush=True)
+        x = _x(cin, n, n).to(DEV)
+        y = hinm.spmm(q, x)
+        torch.cuda.synchronize()
+        _check(y, w, x, q.plan.n_dense + q.plan.n_24 // 2)
+
+
+@pytest.mark.parametrize("n", [1, 6, 8, 13, 16])
+def test_product_last_channels(n):
+    """Kept channels at the very end of X, of whose rows the loads begin early."""
+    p = _packed(64, 64, 0.0, 0.0, seed=n)
+    q = hinm.quantize_fp8(p)
+    x = torch.zeros(64, n, dtype=BF16)
+    x[-9:] = _x(9, n, n)
+    x = x.to(DEV)
+    _check(hinm.spmm(q, x), _dense(q), x, q.plan.n_dense + q.plan.n_24 // 2)
+
+
+@pytest.mark.parametrize("experts", [1, 2, 31, 33, 64, 300])
+@pytest.mark.parametrize("most", [1, 8, 19])
+def test_experts_few_tokens(experts, most):
+    """Up to 32 segments share the workgroups evenly, more in contiguous ranges; some of none."""
+    rng = np.random.default_rng(experts + most)
+    counts = rng.integers(0, most + 1, experts)
+    starts = np.cumsum(counts + rng.integers(0, 3, experts)) - counts
+    cols = int(starts[-1] + counts[-1] + 2)
+    print(f"[fp8] few tokens E={experts} counts up to {most} columns {cols}", flush=True)
+    made = [_packed(128, 260, seed=s) for s in range(min(experts, 5))]
+    q = hinm.quantize_fp8(hinm.Experts.stack([made[e % len(made)] for e in range(experts)]))
+    dense = [_dense(hinm.quantize_fp8(m)) for m in made]
+    x = _x(260, cols, cols).to(DEV)
+    out = torch.full((128, cols), 7.0, dtype=BF16, device=DEV)
+    hinm.spmm_experts(q, x, _ranges(counts.tolist(), starts.tolist(), cols), out=out)
+    torch.cuda.synchronize()
+    rest = np.ones(cols, bool)
+    for e in range(experts):
+        at = slice(int(starts[e]), int(starts[e] + counts[e]))
+        rest[at] = False
+        if counts[e]:
+            _check(out[:, at], dense[e % len(made)], x[:, at], q.plan.n_dense + q.plan.n_24 // 2)
+    assert bool((out[:, torch.from_numpy(rest).to(DEV)] == 7).all())
+
+
+@pytest.mark.parametrize("cin", [7892, 7896, 8916, 8920, 15788, 15792, 17836, 17840])
+def test_experts_many_channels(cin):
+    """Items of 64, 32 and 16 rows: the sums of more rows leave LDS less room for channels."""
+    one = _packed(256, cin, 0.75, 0.55, seed=cin)
+    q = hinm.quantize_fp8(hinm.Experts.stack([one] * 64))
+    rng = np.random.default_rng(cin)
+    counts = rng.integers(*((9, 17) if cin < 9000 else (0, 9)), 64)
+    starts = np.cumsum(counts) - counts
+    cols = int(counts.sum())
+    print(f"[fp8] experts of {cin} channels, {cols} columns", flush=True)
+    x = _x(cin, cols, cin).to(DEV)
+    out = hinm.spmm_experts(q, x, _ranges(counts.tolist(), starts.tolist(), cols))
+    torch.cuda.synchronize()
+    _check(out, _dense(hinm.quantize_fp8(one)), x, q.plan.n_dense + q.plan.n_24 // 2)
+
+
+@pytest.mark.parametrize("rows", [128, 192])
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_product_tile_heights(rows, n):
+    q = hinm.quantize_fp8(_packed(384, 700, 0.75, 0.55, seed=rows, tile_rows=rows))
+    x = _x(700, n, n).to(DEV)
+    _check(hinm.spmm(q, x), _dense(q), x, q.plan.n_dense + q.plan.n_24 // 2)
+
+
+def test_same_weight_on_two_streams():
+    """Workspaces are the stream's: long and short products on two streams at once."""
+    q = hinm.quantize_fp8(_packed(256, 1500, seed=3))
+    xs = [_x(1500, n, n).to(DEV) for n in (300, 4, 150, 1)]
+    want = [hinm.spmm(q, x).clone() for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(16):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((i % 4, hinm.spmm(q, xs[i % 4])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[k]) for k, y in got)

@@ -218,3 +218,46 @@ def test_graph_and_streams(n, k):
             ys.append(layer(x, logits, k))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in ys)
+
+
+@pytest.mark.parametrize("experts,k", [(16, 16), (40, 16), (260, 4), (520, 8)])
+def test_many_pairs(experts, k):
+    """Up to 512 pairs of a token and an expert, and more segments than share the workgroups evenly."""
+    layer = Layer(64, 64, experts, seed=experts)
+    for n in (1, 3, 32):
+        print(f"[moe] E={experts} k={k} n={n}", flush=True)
+        x, logits = _inputs(layer, n, n)
+        _check(layer(x, logits, k), *layer.want(x, logits, k))
+
+
+@pytest.mark.parametrize("values", ["bf16", "mx4", "fp8"])
+def test_many_blocks(values):
+    """Several turns of every wave, in both kernels, and shares that end inside an expert."""
+    layer = Layer(1024, 1088, 5, values=values, seed=3)
+    for n in (1, 2, 6, 21, 32):
+        print(f"[moe] blocks {values} n={n}", flush=True)
+        x, logits = _inputs(layer, n, n)
+        _check(layer(x, logits, 2), *layer.want(x, logits, 2))
+
+
+def test_tokens_of_one_column_block():
+    """Tokens 8 g .. 8 g + 7 are loaded together: an expert's tokens from one, two and all such groups."""
+    layer = Layer(128, 128, 2, seed=5)
+    x, logits = _inputs(layer, 30, 5)
+    for mine in (range(24, 30), range(6, 10), range(0, 30, 3), range(29, 30), range(7, 8)):
+        logits[0], logits[1] = 0.0, 1.0
+        logits[0, list(mine)] = 2.0
+        _check(layer(x, logits, 1), *layer.want(x, logits, 1))
+
+
+def test_layers_on_two_streams():
+    layer = Layer(128, 192, 4, seed=8)
+    ins = [_inputs(layer, n, n) for n in (1, 32, 2, 9)]
+    want = [layer(x, l, 2).clone() for x, l in ins]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(16):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((i % 4, layer(*ins[i % 4], 2)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[k]) for k, y in got)
