@@ -826,29 +826,38 @@ int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n
   return HINM_OK;
 }
 
-// Tokens a workgroup takes.  256 halves the bytes of packed values of 128 but
-// costs an expert with few columns the whole block.
+// Tokens a workgroup of the many-token kernel takes.  256 halves the bytes of
+// packed values of 128 but costs an expert with few columns the whole block, and
+// one weight of few row blocks half of its workgroups.  Measured, 128 against
+// 256: 4096x4096 at 256, 700 and 1500 tokens 29 / 31, 37 / 40, 56 / 49 us; 8
+// experts of 11008x4096 with 64, 115, 130 and 500 columns on average 86 / 116,
+// 97 / 111, 124 / 108, 275 / 215.
 int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
   if (n_experts == 1) return (p.cout / 64) * ((n_cols + 255) / 256) <= kCus ? 128 : 256;
-  return avg <= 64 || (avg > 110 && avg <= 170) ? 128 : 256;
+  return avg <= 112 ? 128 : 256;
 }
 
-// Columns of a decode segment, 8 or 16, or 0 where the many-token kernel is
-// taken: as many as an expert has on average and as fit in LDS, in up to two
-// segments.
+// Columns of a decode segment, 16, or 8 where 16 do not fit in LDS or one weight
+// has no more (of experts, some have more than eight where eight are the
+// average: 8 of 11008x4096 51 us, against 41), or 0 where the many-token kernel
+// is taken: of one weight up to four segments, of experts one on average.
+// Measured, this kernel against the other: 4096x4096 at 64 tokens 16 / 25 us, 4096x11008 (segments of 8) at 32
+// 27 / 37; 64 experts of 1408x2048 with 16 and 20 columns on average 55 / 57 and
+// 63 / 58, 8 of 4096x11008 (segments of 8) with 6, 8 and 12 53 / 68, 69 / 66 and
+// 75 / 66.
 int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
   const int fit = dec_fits(p.cin, 16, 1) ? 16 : dec_fits(p.cin, 8, 1) ? 8 : 0;
   if (fit == 0 || p.cin < 8 || p.n_dense + p.n_24 == 0 || n_cols * (p.cout / 16) >= (int64_t)1 << 31) return 0;
-  const int width = avg <= 8 ? 8 : fit;
-  return avg <= 2 * width ? width : 0;
+  const int width = n_experts == 1 && n_cols <= 8 ? 8 : fit;
+  return avg <= (n_experts == 1 ? 4 : 1) * width ? width : 0;
 }
 
-// Workspace: none for few tokens.  Arrival counters and the partial sums of kMaxWgs workgroups, where
-// a launch may split; then the rounded activations of one window of columns (at
-// most 2^30 bytes, a multiple of 256 columns), their scales and the pieces'
-// largest magnitudes.
+// Workspace: none for few tokens.  Arrival counters and the partial sums of
+// kMaxWgs workgroups, where a launch may split; then the rounded activations of
+// one window of columns (at most 2^30 bytes, a multiple of 256 columns), their
+// scales and the pieces' largest magnitudes.
 struct Workspace {
   int64_t window, ld8;               // columns of a window, their pitch
   int64_t x8, xs, part, bytes;       // offsets
@@ -928,12 +937,13 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
     a.n_cols = (int)n_cols;
     a.x = static_cast<const uint16_t*>(x);
     a.y = static_cast<uint16_t*>(y);
-    // rows an item: those that leave the busiest of 256 workgroups the least to do, an item costing half a fragment
-    // more than its rows
+    // Rows an item, 16 f: those that leave the busiest workgroup the least to do.  An item costs as much as another
+    // seven fragments of 16 rows (11008x4096 at one token, 3, 2 and 1 items of 1, 2 and 4 fragments: 14.6, 12.0 and
+    // 10.3 us; 4096x4096, one item each: 9.5, 9.8 and 10.4).
     const int64_t segs = n_experts == 1 ? (n_cols + width - 1) / width : std::min<int64_t>(n_experts, n_cols);
     auto cost = [&](int f) {
       const int64_t n_rb = p.cout / (16 * f), share = std::max<int64_t>(kCus / segs, 1);
-      return dec_fits(p.cin, width, f) ? (n_rb + share - 1) / share * (2 * f + 1) : INT64_MAX;
+      return dec_fits(p.cin, width, f) ? (n_rb + share - 1) / share * (f + 7) : INT64_MAX;
     };
     const int f = cost(1) <= cost(2) && cost(1) <= cost(4) ? 1 : cost(2) <= cost(4) ? 2 : 4;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(kCus), dim3(kDecThreads), 0, stream, a, width); };
