@@ -540,7 +540,8 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
           uint16_t* const dst = a.h + (seg.down + q) * a.h_seg + rank - q * cap;
           uint16_t* const at = dst + (rb * R + row) * a.wide;
           at[0] = hi;
-          at[cap] = to_bf16(h - __uint_as_float((uint32_t)hi << 16));
+          const float rest = h - __uint_as_float((uint32_t)hi << 16);
+          at[cap] = to_bf16(fabsf(rest) < __builtin_inff() ? rest : 0.f);      // an infinite h stays infinite
           if (rb == 0 && row == 0) dst[a.up.cout * a.wide] = dst[a.up.cout * a.wide + cap] = 0;
         }
         step_barrier();

@@ -353,3 +353,38 @@ def test_same_weight_on_two_streams():
             got.append((i % 4, hinm.spmm(q, xs[i % 4])))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[k]) for k, y in got)
+
+
+def _check_some(y, q, x, cols):
+    """Of a product with many columns, those."""
+    xs = x[:, cols]
+    _check(y[:, cols], _dense(q), xs, q.plan.n_dense + q.plan.n_24 // 2)
+
+
+def test_product_in_windows():
+    """So many columns that their rounded values are made and multiplied in two windows of 16384."""
+    q = hinm.quantize_fp8(_packed(64, 65536, 0.99, 0.985, seed=1))
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(65536, 16500, device=DEV, generator=g, dtype=BF16)
+    print("[fp8] windows, one weight", flush=True)
+    y = hinm.spmm(q, x)
+    torch.cuda.synchronize()
+    _check_some(y, q, x, [0, 1, 8191, 16383, 16384, 16385, 16499])
+
+
+def test_experts_in_windows():
+    """A range that two windows share, one in each, and a gap between the windows' last and first columns."""
+    one = _packed(64, 65536, 0.99, 0.985, seed=2)
+    q, e = hinm.quantize_fp8(hinm.Experts.stack([one] * 4)), hinm.quantize_fp8(one)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(65536, 16600, device=DEV, generator=g, dtype=BF16)
+    for starts, counts in (([0, 300, 16400, 16500], [290, 16080, 90, 100]), ([5, 8000, 16390, 16390], [7000, 8380, 0, 210])):
+        print(f"[fp8] windows, experts {starts} {counts}", flush=True)
+        out = torch.full((64, 16600), 7.0, dtype=BF16, device=DEV)
+        hinm.spmm_experts(q, x, _ranges(counts, starts, 16600), out=out)
+        torch.cuda.synchronize()
+        used = np.zeros(16600, bool)
+        for s, c in zip(starts, counts):
+            used[s:s + c] = True
+        _check_some(out, e, x, [c for c in (5, 301, 8100, 16379, 16383, 16384, 16400, 16599) if used[c]])
+        assert bool((out[:, torch.from_numpy(~used).to(DEV)] == 7).all())

@@ -261,3 +261,27 @@ def test_layers_on_two_streams():
             got.append((i % 4, layer(*ins[i % 4], 2)))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[k]) for k, y in got)
+
+
+@pytest.mark.parametrize("values", ["bf16", "mx4", "fp8"])
+def test_infinite_products(values):
+    """A token whose inner values pass bf16's range gets infinities of the right signs, or NaN where they meet; the
+    other tokens keep their results."""
+    layer = Layer(128, 64, 2, t_s=0.0, v_s=0.0, values=values, seed=9)
+    x, logits = _inputs(layer, 5, 9)
+    want = layer(x, logits, 1)
+    x[:, 2] *= 2.0 ** 70
+    with np.errstate(over="ignore", invalid="ignore"):
+        w = layer.dg, layer.du, layer.dd
+        e = int(_f64(logits)[:, 2].argmax())
+        g, u = (m[e] @ _f64(x[:, 2]) for m in w[:2])
+        h = np.where(g > 0, g, 0.0) * u                        # silu(g) of so large a g
+        hot = np.abs(h) > 2.0 ** 129                           # infinite in fp32 and bf16; others finite
+        assert hot.any() and np.all(hot | (np.abs(h) < 2.0 ** 127))
+    y = layer(x, logits, 1)
+    keep = [0, 1, 3, 4]
+    assert torch.equal(y[:, keep], want[:, keep])
+    part = w[2][e][:, hot] * np.sign(h[hot])
+    up, down = (part > 0).any(1), (part < 0).any(1)
+    got = _f64(y[:, 2])
+    assert np.all(np.isnan(got[up & down])) and np.all(got[up & ~down] == np.inf) and np.all(got[~up & down] == -np.inf)
