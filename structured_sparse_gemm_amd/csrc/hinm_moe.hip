@@ -137,12 +137,11 @@ __device__ inline Source source_of(const MoeStack& w, const Item& it, int v) {
           t, it.rows16 * 16 - t * w.rows, it.b0 + v, it.b1};
 }
 
-// Block b's indices: a lane's position (of a dense block's 32, twice).
-__device__ inline int load_index(const MoeStack& w, const Source& s, int b) {
-  const uint32_t lane = threadIdx.x & 63;
+// The index of block b's position p (of a dense block's 32, twice).
+__device__ inline int load_index(const MoeStack& w, const Source& s, int b, uint32_t p) {
   const bool dense = b < w.nkb_d;
   const uint32_t kb = dense ? s.tile * w.nkb_d + b : s.tile * w.nkb_s + b - w.nkb_d;
-  return at<int>(pick(dense, s.idx_d, s.idx_s), dense ? kb * 128 + 4 * (lane & 31) : kb * 256 + 4 * lane);
+  return at<int>(pick(dense, s.idx_d, s.idx_s), dense ? kb * 128 + 4 * (p & 31) : kb * 256 + 4 * p);
 }
 
 // Block b's operands.  The block's place is scalar and the lane's share a
@@ -478,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
         return source_of(w, {next.expert, (int)(mine.first + i - sg * n_rb) * F, 0, nd + w.nkb_s}, wave % (kWaves / 2));
       },
       [&](const Source& s, int b, Operand<VALUES, F>& o) {
-        o.index = load_index(w, s, b);
+        o.index = load_index(w, s, b, lane);
         load_block<VALUES, F>(w, s, b, o);
       },
       [&](int b, const Operand<VALUES, F>& o) {
@@ -558,7 +557,7 @@ template <int VALUES, int WIDE>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   constexpr int F = 4, kPitch = sums_pitch(F), kDepth = 4, kRow = 2 * WIDE, kSlot = 64 * kRow;
   typedef std::conditional_t<WIDE == 4, u32x2, u32x4> Piece;
-  constexpr int kPieces = kRow / sizeof(Piece);
+  constexpr int kPieces = kRow / sizeof(Piece);    // of a row, which as many adjacent lanes read: they share a cache line
   __shared__ __attribute__((aligned(16))) uint8_t slots[kWaves * 2 * kSlot];
   __shared__ __attribute__((aligned(16))) float red[kWaves * kPitch];
   __shared__ float out[64 * kTokens];              // [row][token]
@@ -611,7 +610,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
     if (parts > 0) {
       Operand<VALUES, F> o[kDepth];
       Piece rows[kDepth][kPieces];
-      int index[kDepth], asked[kDepth], block[kDepth];       // blocks; ~b: block b, not to be multiplied
+      int index[kDepth][kPieces], asked[kDepth], block[kDepth];        // blocks; ~b: block b, not to be multiplied
       int seg_i = 0;                                         // the item that indices are asked of
       Source src = source(0), from;
       int turns = turns_of(src), ends = -1, last = -1;       // items that the turns of rows and of products end
@@ -619,7 +618,8 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
       const uint8_t* h_from = h_src;
       auto ask = [&](int k) {
         const int b = min(src.first, src.end - 1);
-        index[k] = load_index(w, src, b);
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) index[k][u] = load_index(w, src, b, 64 / kPieces * u + lane / kPieces);
         asked[k] = src.first < src.end ? b : ~b;
         src.first += kWaves;
       };
@@ -652,14 +652,16 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
           if (block[k] >= 0) {
             uint8_t* const to = slot + (k & 1) * kSlot;
 #pragma unroll
-            for (int u = 0; u < kPieces; ++u) *reinterpret_cast<Piece*>(to + lane * kRow + u * sizeof(Piece)) = rows[k][u];
+            for (int u = 0; u < kPieces; ++u) *reinterpret_cast<Piece*>(to + (64 * u + lane) * sizeof(Piece)) = rows[k][u];
             multiply_block<VALUES, F>(block[k] < nd, o[k], kRow, [&](int p) { return to + p * kRow; }, acc);
           }
           block[k] = asked[k];
           const int b = asked[k] < 0 ? ~asked[k] : asked[k];
-          const uint32_t row = (uint32_t)index[k] < (uint32_t)w.cin ? index[k] : w.cin;
 #pragma unroll
-          for (int u = 0; u < kPieces; ++u) rows[k][u] = at<Piece>(h_from, row * kRow + u * sizeof(Piece));
+          for (int u = 0; u < kPieces; ++u) {
+            const uint32_t row = (uint32_t)index[k][u] < (uint32_t)w.cin ? index[k][u] : w.cin;
+            rows[k][u] = at<Piece>(h_from, row * kRow + lane % kPieces * sizeof(Piece));
+          }
           load_block<VALUES, F>(w, from, b, o[k]);
           ask(k);
         }
