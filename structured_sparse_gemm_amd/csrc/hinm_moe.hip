@@ -6,7 +6,7 @@
 // in flight.
 //
 //   up kernel    every workgroup works out the routing from the logits, then
-//                takes (segment, 32 rows of the inner channels); a segment is
+//                takes (segment, 32 or 64 inner channels); a segment is
 //                up to 16 of an expert's tokens.  Their activations are held in
 //                LDS whole, [channel][token], and the channels that a tile
 //                keeps gathered there: the transposed LDS read takes an address
@@ -430,12 +430,10 @@ __device__ __forceinline__ void put_x(const MoeArgs& a, uint32_t mask, int g, in
     }
 }
 
-// Items are (segment, 32 rows of the inner channels): of 64 rows, the 344 items
-// of a token's two experts of 11008 channels left the busiest of 256 workgroups
-// two.
-template <int VALUES>
+// Items are (segment, 16 F rows of the inner channels).
+template <int VALUES, int F>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
-  constexpr int F = 2, R = 16 * F, kPitch = sums_pitch(F), kDepth = VALUES == HINM_VALUES_BF16 ? 4 : 6;
+  constexpr int R = 16 * F, kPitch = sums_pitch(2), kDepth = VALUES == HINM_VALUES_BF16 || F == 4 ? 4 : 6;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
   __shared__ __attribute__((aligned(16))) union {
     float red[kWaves * kPitch];
@@ -515,35 +513,39 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
         for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
       },
       [&](int) {
-        // a lane's sums of wave w, fragment f: red[w][f][lane]; of four adjacent threads the first two sum the gate's
-        // waves, the others the up projection's, and each makes one row's h
+        // two fragments at a time, which is what LDS has room for: a lane's sums of wave w, fragment f to
+        // red[w][f % 2][lane]; of four adjacent threads the first two sum the gate's waves, the others the up
+        // projection's, and each makes one row's h
 #pragma unroll
-        for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(sh.red + wave * kPitch + 256 * f + 4 * lane) = acc[f];
-        step_barrier();
-        const int tid = own_thread(), part = tid & 3, t = tid >> 2;
-        const f32x4 s = *reinterpret_cast<const f32x4*>(sh.red + 2 * part * kPitch + 4 * t) +
-                        *reinterpret_cast<const f32x4*>(sh.red + (2 * part + 1) * kPitch + 4 * t);
-        float own = 0.f, other = 0.f;
+        for (int f0 = 0; f0 < F; f0 += 2) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float x = s[q] + quad1(s[q]), y = quad2(x);
-          if (q == part) own = x, other = y;
+          for (int f = 0; f < 2; ++f) *reinterpret_cast<f32x4*>(sh.red + wave * kPitch + 256 * f + 4 * lane) = acc[f0 + f];
+          step_barrier();
+          const int tid = own_thread(), part = tid & 3, t = tid >> 2;
+          const f32x4 s = *reinterpret_cast<const f32x4*>(sh.red + 2 * part * kPitch + 4 * t) +
+                          *reinterpret_cast<const f32x4*>(sh.red + (2 * part + 1) * kPitch + 4 * t);
+          float own = 0.f, other = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float x = s[q] + quad1(s[q]), y = quad2(x);
+            if (q == part) own = x, other = y;
+          }
+          const float g = part < 2 ? own : other, u = part < 2 ? other : own;
+          const int col = t & 15, row = 16 * (f0 + (t >> 6)) + 4 * ((t >> 4) & 3) + part;
+          if (col < seg.n) {
+            // where the down kernel's segment of this token has it
+            const int rank = seg.rank0 + col, cap = a.wide / 2, q = rank / cap;
+            const float h = g / (1.f + expf(-g)) * u;
+            const uint16_t hi = to_bf16(h);
+            const float rest = h - __uint_as_float((uint32_t)hi << 16);
+            uint16_t* const dst = a.h + (seg.down + q) * a.h_seg + rank - q * cap;
+            uint16_t* const at = dst + (rb * R + row) * a.wide;
+            at[0] = hi;
+            at[cap] = to_bf16(fabsf(rest) < __builtin_inff() ? rest : 0.f);      // an infinite h stays infinite
+            if (rb == 0 && row == 0) dst[a.up.cout * a.wide] = dst[a.up.cout * a.wide + cap] = 0;
+          }
+          step_barrier();
         }
-        const float g = part < 2 ? own : other, u = part < 2 ? other : own;
-        const int col = t & 15, row = 16 * (t >> 6) + 4 * ((t >> 4) & 3) + part;
-        if (col < seg.n) {
-          // where the down kernel's segment of this token has it
-          const int rank = seg.rank0 + col, cap = a.wide / 2, q = rank / cap;
-          const float h = g / (1.f + expf(-g)) * u;
-          const uint16_t hi = to_bf16(h);
-          uint16_t* const dst = a.h + (seg.down + q) * a.h_seg + rank - q * cap;
-          uint16_t* const at = dst + (rb * R + row) * a.wide;
-          at[0] = hi;
-          const float rest = h - __uint_as_float((uint32_t)hi << 16);
-          at[cap] = to_bf16(fabsf(rest) < __builtin_inff() ? rest : 0.f);      // an infinite h stays infinite
-          if (rb == 0 && row == 0) dst[a.up.cout * a.wide] = dst[a.up.cout * a.wide + cap] = 0;
-        }
-        step_barrier();
       });
 }
 
@@ -807,9 +809,22 @@ int plan_of(const char* whose, const void* stack, const hinm_plan_t*& p) {
   return hinm::check_plan(p);
 }
 
+// Fragments of 16 rows of the up kernel's items: what leaves the busiest
+// workgroup the least to do, by an item's cost of its own, in half fragments.
+// Measured with two and with four (8 experts of 11008x4096, top 2): bf16 at 1
+// and 32 tokens 46 / 50 and 178 / 178 us, 8 bits 41.5 / 42.8 and 151 / 147, 4
+// bits 38 / 36 and 112 / 100.
+int fragments_of(const MoeArgs& a, int values) {
+  const int64_t segs = std::min<int64_t>(a.n_experts, (int64_t)a.n_tokens * a.top_k);
+  const int own = values == HINM_VALUES_BF16 ? 0 : values == HINM_VALUES_FP8 ? 3 : 6;
+  auto cost = [&](int f) { return (segs * (a.up.cout / (16 * f)) + kCus - 1) / kCus * (2 * f + own); };
+  return cost(2) <= cost(4) ? 2 : 4;
+}
+
 template <int VALUES>
 void launch(const MoeArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(moe_up_kernel<VALUES>, dim3(kCus), dim3(kThreads), 0, stream, a);
+  if (fragments_of(a, VALUES) == 2) hipLaunchKernelGGL((moe_up_kernel<VALUES, 2>), dim3(kCus), dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((moe_up_kernel<VALUES, 4>), dim3(kCus), dim3(kThreads), 0, stream, a);
   if (a.wide == 4) hipLaunchKernelGGL((moe_down_kernel<VALUES, 4>), dim3(kCus), dim3(kThreads), 0, stream, a);
   else hipLaunchKernelGGL((moe_down_kernel<VALUES, 16>), dim3(kCus), dim3(kThreads), 0, stream, a);
 }
