@@ -102,7 +102,8 @@ __device__ inline fp8_u32x2 column_codes(u32x4 v, const float (&inv)[8]) {
 
 // Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece, whose
 // rows (up to 8 a thread) are all in flight at once: four at a time, and loads
-// under a condition, took 25 us for 4096 x 2047, this 6.  A thread's columns are
+// under a condition, took 25 and 23 us for 11008 x 2047 values, this 11 and 17,
+// 4.2 and 4.0 TB/s.  A thread's columns are
 // the window's last eight where it has no eight more, so that two threads may
 // write the same values; of a window of fewer than eight columns one thread
 // reads and writes single ones.
@@ -197,7 +198,11 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
 // thousand cycles away (with __syncthreads(), which waits for all loads into
 // LDS, 4096x11008 at 2047 tokens took 87 us, and 67 without the rows or without
 // the products).  Hence the loads are inline assembly, which the compiler does
-// not wait for, and the barrier waits for LDS operations alone.
+// not wait for, and the barrier waits for LDS operations alone.  What a step
+// issues beside its 48 conversions and 8 products bounds it next: with the
+// addresses of the weight's blocks worked out anew in every step, and one loop
+// for both kinds of blocks, 96 us, with addresses that move on 79 (587 TFLOP/s
+// of kept products).
 //
 // Tile layout: position p's row of NT bytes, its 16-byte chunk c at chunk
 // c ^ turned(p), so that a 32-lane half of a transposed read covers every bank
@@ -217,7 +222,7 @@ __device__ inline int turned(int p) { return NT == 256 ? 2 * (p & 7) : 2 * ((p >
 
 // A slot of the weight's ring: 64 rows' values of a block, then what one load
 // brings: metadata, scales and indices.
-constexpr int kTiles = 3, kRing = 5, kSlot = 3072, kMeta = 2048, kScale = kMeta + 512, kIndex = kScale + 64;
+constexpr int kTiles = 3, kRing = 5, kMeta = 2048, kScale = kMeta + 512, kIndex = kScale + 64, kSlot = kMeta + 1024;
 
 // Sixteen bytes a lane into LDS at `lds` + 16 lane: from a buffer (past its end
 // zeros; sc0 as in load_lds16), and from an address.
@@ -842,10 +847,10 @@ int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
 // has no more (of experts, some have more than eight where eight are the
 // average: 8 of 11008x4096 51 us, against 41), or 0 where the many-token kernel
 // is taken: of one weight up to four segments, of experts one on average.
-// Measured, this kernel against the other: 4096x4096 at 64 tokens 16 / 25 us, 4096x11008 (segments of 8) at 32
-// 27 / 37; 64 experts of 1408x2048 with 16 and 20 columns on average 55 / 57 and
-// 63 / 58, 8 of 4096x11008 (segments of 8) with 6, 8 and 12 53 / 68, 69 / 66 and
-// 75 / 66.
+// Measured, this kernel against the other: 4096x4096 at 64 tokens 16 / 25 us,
+// 4096x11008 (segments of 8) at 32 27 / 37; 64 experts of 1408x2048 with 16 and
+// 20 columns on average 55 / 57 and 63 / 58, 8 of 4096x11008 (segments of 8)
+// with 6, 8 and 12 53 / 68, 69 / 66 and 75 / 66.
 int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
   const int fit = dec_fits(p.cin, 16, 1) ? 16 : dec_fits(p.cin, 8, 1) ? 8 : 0;
