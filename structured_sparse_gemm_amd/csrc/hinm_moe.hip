@@ -26,8 +26,8 @@
 // What bounds them (8 experts of 11008x4096, bf16, 32 tokens, 107 and 77 us for
 // 418 and 209 MB): a compute unit's 64 outstanding cache lines, of which the
 // gathered rows of h are most in the down kernel.  One token (28 and 21 us for
-// 104 and 52 MB): a third is the chain from the logits to the first products,
-// code that is run once and fetched, some two cycles a byte.
+// 104 and 52 MB): a third is the chain ahead of the first products - arguments,
+// logits, choices, the segments' list, first loads, each after the one before.
 //
 // h is a matrix operand and so bf16, but rounded once it would cost the output
 // as much as its own rounding (relative error of the layer 0.0024, against
