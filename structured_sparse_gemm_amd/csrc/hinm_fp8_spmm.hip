@@ -74,8 +74,7 @@ __device__ inline uint32_t larger2(uint32_t m, uint32_t v) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(i16x2, m), __builtin_bit_cast(i16x2, v)));
 }
 __device__ inline uint32_t larger(uint32_t m, uint32_t v) {        // v: two bf16 values
-  const i16x2 w = __builtin_bit_cast(i16x2, v & 0x7fff7fffu) + i16x2{0x80, 0x80};
-  return larger2(m, __builtin_bit_cast(uint32_t, w));
+  return larger2(m, (v & 0x7fff7fffu) + kLeast);                   // no carry between the halves
 }
 template <int CTRL>
 __device__ inline uint32_t moved(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp((int)kLeast, (int)v, CTRL, 0xf, 0xf, false); }
@@ -103,10 +102,9 @@ __device__ inline fp8_u32x2 column_codes(u32x4 v, const float (&inv)[8]) {
 // Workgroup: 256 columns (32 threads of 8), 8 rows at a time of one piece, whose
 // rows (up to 8 a thread) are all in flight at once: four at a time, and loads
 // under a condition, took 25 and 23 us for 11008 x 2047 values, this 11 and 17,
-// 4.2 and 4.0 TB/s.  A thread's columns are
-// the window's last eight where it has no eight more, so that two threads may
-// write the same values; of a window of fewer than eight columns one thread
-// reads and writes single ones.
+// 4.2 and 4.0 TB/s.  A thread's columns are the window's last eight where it has
+// no eight more, so that two threads may write the same values; a window of
+// fewer than eight columns is read one by one.
 constexpr int kRowsHeld = 8;
 __device__ __forceinline__ void load_rows(const Fp8Args& a, int n, int r0, int r1, u32x4 (&v)[kRowsHeld]) {
   const int first = r0 + (threadIdx.x >> 5);
@@ -696,7 +694,6 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
 template <int F, bool TOKEN>
 __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int columns) {
   const int width = TOKEN ? 8 : columns;
-  touch(a);
   constexpr int kDepth = F == 1 ? 8 : F == 2 ? 6 : 4;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kDecLds];
   __shared__ __attribute__((aligned(16))) uint32_t top[kDecWaves * 8];

@@ -61,6 +61,17 @@ static_assert((kMaxChannels + 1) * 8 <= kSlab, "four columns of the most channel
 // Floats between the waves' sums of F fragments, the 8 for reads free of bank conflicts.
 constexpr int sums_pitch(int f) { return 256 * f + 8; }
 
+// Reads a word of every 64 bytes of a kernel's arguments, so that they are in
+// the scalar cache when they are wanted, and waited for once (a token, 2 of 8
+// experts of 11008: 47.2 us without, 46.4 with).
+template <class Args>
+__device__ __forceinline__ void touch(const Args& a) {
+  uint32_t x = 0;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Args) + 63) / 64; ++i) x ^= reinterpret_cast<const uint32_t*>(&a)[16 * i];
+  asm volatile("" ::"s"(x));
+}
+
 // One stack of packed weights; strides are bytes of one expert.
 struct MoeStack {
   const uint8_t *val_d, *val_s, *scale_d, *scale_s, *meta, *idx_d, *idx_s;

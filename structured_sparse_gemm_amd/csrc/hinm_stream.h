@@ -13,18 +13,6 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 // A barrier that waits for this wave's LDS operations, not for its loads.
 __device__ inline void step_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Reads a word of every 64 bytes of a kernel's arguments, so that they are in
-// the scalar cache when they are wanted: they come from the host's memory, some
-// two thousand cycles for each part that is read for the first time, all at
-// once here.
-template <class Args>
-__device__ __forceinline__ void touch(const Args& a) {
-  uint32_t x = 0;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(Args) + 63) / 64; ++i) x ^= reinterpret_cast<const uint32_t*>(&a)[16 * i];
-  asm volatile("" ::"s"(x));
-}
-
 // The thread's number, as a value that the compiler takes for new: what is
 // computed from it stays where it is used, and out of the code ahead of a loop
 // that uses it once.
@@ -44,14 +32,16 @@ __device__ inline const uint8_t* pick(bool c, const uint8_t* a, const uint8_t* b
 // While DEPTH of a wave's blocks are multiplied the next DEPTH blocks' operands
 // are on their way, across the items' ends too.  For item i:
 //   open(i)       names the wave's blocks, first, first + NW, ... below end, and
-//                 where they lie; the item has one block at least (for some
-//                 wave), and no memory is read (loads that only sometimes
-//                 happen would make every wait one for all loads in flight);
+//                 where they lie (the item has one block at least, for some
+//                 wave), and where the item begins a segment asks for its
+//                 activations, ahead of the weight;
 //   load(s, b, o) loads block b's operands;
 //   multiply(b, o) adds its products;
 //   begin(i), finish(i): before its first and after its last product, in step
 //                 for the whole workgroup.
-// One loop body serves the first loads, the products and the items' ends.
+// One loop body serves the first loads, the products and the items' ends.  The
+// weight's loads are under no condition: loads that only sometimes happen would
+// make every wait one for all loads in flight.
 template <class Operand, class Source, int DEPTH, int NW, class Open, class Load, class Multiply, class Begin, class Finish>
 __device__ __forceinline__ void stream(int items, Open open, Load load, Multiply multiply, Begin begin, Finish finish) {
   if (items <= 0) return;
