@@ -82,16 +82,16 @@ def test_product_statuses():
     lib, p = hinm.library(), _plan(4096, 4096, 64, 0.5, 0.25)
     q = _fake(p)
 
-    def one(st=q, x=4096, n=64, ldx=64, y=4096, ldy=64, ws=1 << 20, size=1 << 40):
+    def one(st=q, x=4096, n=640, ldx=640, y=4096, ldy=640, ws=1 << 20, size=1 << 40):
         return lib.hinm_spmm_fp8(ctypes.byref(st), x, n, ldx, y, ldy, ws, size, None)
 
     def many(st=q, e=4, starts=4096, counts=4096, n=640, ws=1 << 20, size=1 << 40):
         return lib.hinm_spmm_experts_fp8(ctypes.byref(st), e, 4096, n, n, starts, counts, 4096, n, ws, size, None)
 
     need = ctypes.c_size_t()
-    assert lib.hinm_spmm_fp8_workspace_bytes(ctypes.byref(p.raw), 64, ctypes.byref(need)) == 0 and need.value > 4096 * 64
+    assert lib.hinm_spmm_fp8_workspace_bytes(ctypes.byref(p.raw), 640, ctypes.byref(need)) == 0 and need.value > 4096 * 640
     assert one(n=-1) == 2 and one(n=(1 << 24) + 1, ldx=1 << 25, ldy=1 << 25) == 2
-    assert one(ldx=63) == 2 and one(ldy=63) == 2 and one(ldx=1 << 31) == 2
+    assert one(ldx=639) == 2 and one(ldy=639) == 2 and one(ldx=1 << 31) == 2
     assert one(x=None) == 1 and one(y=None) == 1 and one(x=4097) == 5 and one(y=4097) == 5
     assert one(st=_fake(p, base=(1 << 20) + 8)) == 5 and one(st=hinm.Fp8T(p.raw)) == 1
     assert one(ws=None) == 6 and one(size=need.value - 1) == 6 and one(ws=(1 << 20) + 16) == 5
