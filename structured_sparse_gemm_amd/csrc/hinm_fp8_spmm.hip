@@ -694,7 +694,7 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
 template <int F, bool TOKEN>
 __global__ __launch_bounds__(kDecThreads) void fp8_decode_kernel(Fp8Args a, int columns) {
   const int width = TOKEN ? 8 : columns;
-  constexpr int kDepth = F == 1 ? 8 : F == 2 ? 6 : 4;
+  constexpr int kDepth = 2;           // 1, 2, 3, 4 and 6: 64 experts of 1408x2048 with 8 columns 29, 30, 33, 37 and 51 us
   __shared__ __attribute__((aligned(16))) uint8_t slab[kDecLds];
   __shared__ __attribute__((aligned(16))) uint32_t top[kDecWaves * 8];
   __shared__ int pre[HINM_MAX_EXPERTS + 1];
@@ -843,17 +843,19 @@ int token_block(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
 // Columns of a decode segment, 16, or 8 where 16 do not fit in LDS or one weight
 // has no more (of experts, some have more than eight where eight are the
 // average: 8 of 11008x4096 51 us, against 41), or 0 where the many-token kernel
-// is taken: of one weight up to four segments, of experts one on average.
-// Measured, this kernel against the other: 4096x4096 at 64 tokens 16 / 25 us,
-// 4096x11008 (segments of 8) at 32 27 / 37; 64 experts of 1408x2048 with 16 and
-// 20 columns on average 55 / 57 and 63 / 58, 8 of 4096x11008 (segments of 8)
-// with 6, 8 and 12 53 / 68, 69 / 66 and 75 / 66.
+// is taken.  Measured, this kernel against the other: one weight of 11008x4096
+// at 80 and 128 tokens 29 / 30 and 34 / 31 us, 4096x4096 20 / 26 and 19 / 26,
+// 4096x11008 (segments of 8) at 32 and 64 27 / 37 and 44 / 37; 64 experts of
+// 1408x2048 with 24 and 32 columns on average 55 / 59 and 66 / 58, 8 of
+// 11008x4096 57 / 80 and 72 / 80, 8 of 4096x11008 (segments of 8) with 4, 8 and
+// 12 46 / 68, 69 / 68 and 74 / 68.
 int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
   const int64_t avg = (n_cols + n_experts - 1) / n_experts;
   const int fit = dec_fits(p.cin, 16, 1) ? 16 : dec_fits(p.cin, 8, 1) ? 8 : 0;
   if (fit == 0 || p.cin < 8 || p.n_dense + p.n_24 == 0 || n_cols * (p.cout / 16) >= (int64_t)1 << 31) return 0;
   const int width = n_experts == 1 && n_cols <= 8 ? 8 : fit;
-  return avg <= (n_experts == 1 ? 4 : 1) * width ? width : 0;
+  const int most = n_experts == 1 ? (fit == 16 ? 96 : 32) : (fit == 16 ? 24 : 8);
+  return avg <= most ? width : 0;
 }
 
 // Workspace: none for few tokens.  Arrival counters and the partial sums of
@@ -940,12 +942,12 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
     a.x = static_cast<const uint16_t*>(x);
     a.y = static_cast<uint16_t*>(y);
     // Rows an item, 16 f: those that leave the busiest workgroup the least to do.  An item costs as much as another
-    // seven fragments of 16 rows (11008x4096 at one token, 3, 2 and 1 items of 1, 2 and 4 fragments: 14.6, 12.0 and
-    // 10.3 us; 4096x4096, one item each: 9.5, 9.8 and 10.4).
+    // five fragments of 16 rows (11008x4096 at one token, 3, 2 and 1 items of 1, 2 and 4 fragments: 11.8, 10.7 and
+    // 9.3 us; 4096x4096, one item each: 8.0, 8.0 and 8.8).
     const int64_t segs = n_experts == 1 ? (n_cols + width - 1) / width : std::min<int64_t>(n_experts, n_cols);
     auto cost = [&](int f) {
       const int64_t n_rb = p.cout / (16 * f), share = std::max<int64_t>(kCus / segs, 1);
-      return dec_fits(p.cin, width, f) ? (n_rb + share - 1) / share * (f + 7) : INT64_MAX;
+      return dec_fits(p.cin, width, f) ? (n_rb + share - 1) / share * (f + 5) : INT64_MAX;
     };
     const int f = cost(1) <= cost(2) && cost(1) <= cost(4) ? 1 : cost(2) <= cost(4) ? 2 : 4;
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(kCus), dim3(kDecThreads), 0, stream, a, width); };

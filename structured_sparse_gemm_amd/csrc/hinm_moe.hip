@@ -447,10 +447,12 @@ __device__ __forceinline__ void put_x(const MoeArgs& a, uint32_t mask, int g, in
     }
 }
 
-// Items are (segment, 16 F rows of the inner channels).
+// Items are (segment, 16 F rows of the inner channels).  A turn of three blocks: of
+// two, three and four, a token's layer 46.1, 45.2 and 46.8 us (bf16), 39.9, 38.9
+// and 41.9 (8 bits).
 template <int VALUES, int F>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
-  constexpr int R = 16 * F, kPitch = sums_pitch(2), kDepth = VALUES == HINM_VALUES_BF16 || F == 4 ? 4 : 6;
+  constexpr int R = 16 * F, kPitch = sums_pitch(2), kDepth = 3;
   __shared__ __attribute__((aligned(16))) uint8_t slab[kSlab];
   __shared__ __attribute__((aligned(16))) union {
     float red[kWaves * kPitch];
@@ -572,9 +574,11 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 // the rows and values of the next ones, by indices that it asked for a turn
 // before, and for the indices of those after.  No load is under a condition:
 // waits are for a known number of loads.
+// A turn of two blocks: of two, three and four, a token's layer 43.5, 44.5 and
+// 46.7 us (bf16), 39.1, 40 and 41.9 (8 bits).
 template <int VALUES, int WIDE>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
-  constexpr int F = 4, kPitch = sums_pitch(F), kDepth = 4, kRow = 2 * WIDE, kSlot = 64 * kRow;
+  constexpr int F = 4, kPitch = sums_pitch(F), kDepth = 2, kRow = 2 * WIDE, kSlot = 64 * kRow;
   typedef std::conditional_t<WIDE == 4, u32x2, u32x4> Piece;
   constexpr int kPieces = kRow / sizeof(Piece);    // of a row, which as many adjacent lanes read: they share a cache line
   __shared__ __attribute__((aligned(16))) uint8_t slots[kWaves * 2 * kSlot];
@@ -829,11 +833,11 @@ int plan_of(const char* whose, const void* stack, const hinm_plan_t*& p) {
 // Fragments of 16 rows of the up kernel's items: what leaves the busiest
 // workgroup the least to do, by an item's cost of its own, in half fragments.
 // Measured with two and with four (8 experts of 11008x4096, top 2): bf16 at 1
-// and 32 tokens 46 / 50 and 178 / 178 us, 8 bits 41.5 / 42.8 and 151 / 147, 4
-// bits 38 / 36 and 112 / 100.
+// and 32 tokens 43 / 46 and 175 / 175 us, 8 bits 37 / 40 and 141 / 143, 4 bits
+// 35 / 33 and 110 / 96.
 int fragments_of(const MoeArgs& a, int values) {
   const int64_t segs = std::min<int64_t>(a.n_experts, (int64_t)a.n_tokens * a.top_k);
-  const int own = values == HINM_VALUES_BF16 ? 0 : values == HINM_VALUES_FP8 ? 3 : 6;
+  const int own = values == HINM_VALUES_MX4 ? 6 : 0;
   auto cost = [&](int f) { return (segs * (a.up.cout / (16 * f)) + kCus - 1) / kCus * (2 * f + own); };
   return cost(2) <= cost(4) ? 2 : 4;
 }
