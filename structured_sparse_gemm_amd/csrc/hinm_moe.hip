@@ -21,11 +21,11 @@
 //                the router's weights and added to the tokens' in LDS, and the
 //                shares meet in the workspace.  (With h in LDS a segment held
 //                two tokens of 11008 channels, and 8 experts of 8 tokens each
-//                took 145 us, four reads of each expert's weight; now 77.)
+//                took 145 us, four reads of each expert's weight; now 75.)
 //
-// What bounds them (8 experts of 11008x4096, bf16, 32 tokens, 107 and 77 us for
+// What bounds them (8 experts of 11008x4096, bf16, 32 tokens, 105 and 75 us for
 // 418 and 209 MB): a compute unit's 64 outstanding cache lines, of which the
-// gathered rows of h are most in the down kernel.  One token (28 and 21 us for
+// gathered rows of h are most in the down kernel.  One token (26 and 19 us for
 // 104 and 52 MB): a third is the chain ahead of the first products - arguments,
 // logits, choices, the segments' list, first loads, each after the one before.
 //
