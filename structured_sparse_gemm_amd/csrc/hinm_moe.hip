@@ -51,7 +51,7 @@ using hinm::fail;
 
 namespace {
 
-constexpr int kWaves = 8;                          // of a workgroup; one workgroup a compute unit (16: slower, see stream())
+constexpr int kWaves = 8;                          // of a workgroup; one workgroup a compute unit (16: slower)
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTokens = HINM_MOE_MAX_TOKENS;
 constexpr int kPairs = kTokens * HINM_MAX_TOP_K;   // (token, expert) pairs at most; a segment holds at least one

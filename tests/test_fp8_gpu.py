@@ -292,7 +292,7 @@ def test_product_last_channels(n):
 
 
 @pytest.mark.parametrize("experts", [1, 2, 31, 33, 64, 300])
-@pytest.mark.parametrize("most", [1, 8, 19])
+@pytest.mark.parametrize("most", [1, 8, 19, 45])
 def test_experts_few_tokens(experts, most):
     """Up to 32 segments share the workgroups evenly, more in contiguous ranges; some of none."""
     rng = np.random.default_rng(experts + most)
@@ -388,3 +388,14 @@ def test_experts_in_windows():
             used[s:s + c] = True
         _check_some(out, e, x, [c for c in (5, 301, 8100, 16379, 16383, 16384, 16400, 16599) if used[c]])
         assert bool((out[:, torch.from_numpy(~used).to(DEV)] == 7).all())
+
+
+@pytest.mark.parametrize("n", [65, 95, 96, 97])
+def test_product_several_segments(n):
+    """One weight's columns in up to six segments of sixteen, and the first count that takes the other kernel."""
+    q = hinm.quantize_fp8(_packed(320, 600, 0.75, 0.55, seed=n))
+    x = _x(600, n, n).to(DEV)
+    y = hinm.spmm(q, x)
+    torch.cuda.synchronize()
+    _check(y, _dense(q), x, q.plan.n_dense + q.plan.n_24 // 2)
+    assert torch.equal(hinm.spmm(q, x), y)
