@@ -691,11 +691,11 @@ int hinm_spmm_experts_mx4(const hinm_mx4_t* stack, int32_t n_experts, const void
  * rounded to nearest even, magnitudes above 448 to 448; a NaN or an infinity
  * becomes the NaN code and does not enter the scale.  A power of two changes
  * no mantissa, so the rounding is that of E4M3 alone, and every value but NaN
- * is a bf16 value.
+ * is a bf16 value (448 * 2^119 is 1.75 * 2^127, what larger finite values
+ * saturate to).
  *   weights:     128 kept values of a row = four K-blocks of one region (the
  *                region's last block may have fewer);
- *   activations: one token's column, all channels (scales up to 2^120, so that
- *                none saturates).  The product gathers channels in the order of
+ *   activations: one token's column, all channels.  The product gathers channels in the order of
  *                the tile's lists: a scale of some channels could not be taken
  *                out of its sums; the token's can.
  */

@@ -9,8 +9,7 @@ namespace {
 typedef uint32_t fp8_u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 fp8_bf16x2 __attribute__((ext_vector_type(2)));
 
-// 2^(e - 127) for 1 <= e <= 254: every scale of weights (3 .. 246) and of
-// activations (3 .. 247).
+// 2^(e - 127) for 1 <= e <= 254: every scale is of 3 .. 246.
 __device__ inline float fp8_scale(uint32_t e) { return __uint_as_float(e << 23); }
 __device__ inline float fp8_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 

@@ -79,12 +79,31 @@ __device__ inline uint32_t larger(uint32_t m, uint32_t v) {        // v: two bf1
 template <int CTRL>
 __device__ inline uint32_t moved(uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp((int)kLeast, (int)v, CTRL, 0xf, 0xf, false); }
 
-// A token's scale byte from the largest magnitude as held above.  Up to 2^120: no
-// activation saturates.
-__device__ inline uint32_t column_scale(uint32_t held) {
-  const uint32_t top = held - 0x80u;
-  const int e = (int)(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-  return (uint32_t)max(e, 3);
+// A token's scale byte from the largest magnitude as held above.
+__device__ inline uint32_t column_scale(uint32_t held) { return fp8_scale_of(held - 0x80u); }
+
+// Whether a token, or one of two, has values past 448 * 2^119, the largest
+// code at the largest scale (at 2^120 the codes of bf16's largest values would
+// stand for 2^128, which bf16 does not have); and two values saturated there,
+// what is not finite left as it is.  The largest magnitudes are known where the
+// scales are, so that only such tokens pay for it.
+constexpr uint32_t kMostHeld = 0x7f60u + 0x80u;
+__device__ inline bool far2(uint32_t held) { return (held & 0xffffu) > kMostHeld || held >> 16 > kMostHeld; }
+__device__ inline uint32_t saturated(uint32_t v) {
+  const uint32_t lo = v & 0x7fffu, hi = v & 0x7fff0000u;
+  if (lo > 0x7f60u && lo < 0x7f80u) v = (v & 0xffff8000u) | 0x7f60u;
+  if (hi > 0x7f600000u && hi < 0x7f800000u) v = (v & 0x8000ffffu) | 0x7f600000u;
+  return v;
+}
+__device__ inline u32x4 saturated(u32x4 v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = saturated(v[k]);
+  return v;
+}
+template <int N>
+__device__ inline void saturate(u32x4 (&v)[N]) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) v[u] = saturated(v[u]);
 }
 
 // Eight values as codes; the conversion makes NaN of what is not finite.
@@ -169,12 +188,14 @@ __global__ __launch_bounds__(256) void fp8_columns_kernel(Fp8Args a, const uint1
     e[u] = column_scale((m[u >> 1] >> (16 * (u & 1))) & 0xffffu);
     inv[u] = fp8_inverse(e[u]);
   }
+  const bool far = far2(m[0]) || far2(m[1]) || far2(m[2]) || far2(m[3]);
   if (blockIdx.y == 0 && threadIdx.x < 32)
     for (int u = 0; u < 8; ++u) xs[n + u] = (uint8_t)e[u];
   for (int r = r0;;) {
 #pragma unroll
     for (int u = 0; u < kRowsHeld; ++u) {
       const int row = r + (threadIdx.x >> 5) + 8 * u;
+      if (far) v[u] = saturated(v[u]);
       if (row < r1) *reinterpret_cast<any_u32x2*>(x8 + (int64_t)row * a.ld8 + n) = column_codes(v[u], inv);
     }
     if ((r += 8 * kRowsHeld) >= r1) break;
@@ -650,6 +671,7 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
   r = larger2(r, (uint32_t)__shfl_xor((int)r, 16));
   r = larger2(r, (uint32_t)__shfl_xor((int)r, 32));
   const uint32_t e0 = column_scale(r & 0xffffu), e1 = column_scale(r >> 16);
+  const bool far = __ballot(far2(r)) != 0;                   // of the whole segment
   if (tid < 8) *reinterpret_cast<uint16_t*>(scales + 2 * tid) = (uint16_t)(e0 | e1 << 8);
   const uint32_t i0 = __float_as_uint(fp8_inverse(e0)), i1 = __float_as_uint(fp8_inverse(e1));
   float inv[8];
@@ -661,6 +683,7 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
   }
   if (tid < width / 8) *reinterpret_cast<fp8_u32x2*>(slab + a.cin * width + 8 * tid) = fp8_u32x2{0u, 0u};
   if constexpr (TOKEN) {
+    if (far) saturate(v);
 #pragma unroll
     for (int u = 0; u < kHeld<TOKEN>; ++u) {
       const int c = 8 * (tid + u * kDecThreads);
@@ -677,6 +700,7 @@ __device__ __forceinline__ void round_x(const Fp8Args& a, const Segment& sg, int
   }
 #pragma nounroll
   for (int pass = passes - 1;;) {
+    if (far) saturate(v);
 #pragma unroll
     for (int u = 0; u < kHeld<TOKEN>; ++u) {
       const int c = first + ((pass * kChannelLoads + u) << shift);
