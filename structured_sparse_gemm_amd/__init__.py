@@ -1410,9 +1410,10 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, gate, up, down, top_k: int,
     ldy = _matrix(out, pd.cout, n, dev, "out")
     lib, stream = library(), _stream_ptr(dev)
     needs = gate.__dict__.setdefault("_moe_need", {})
-    need = needs.get((n, top_k))
+    key = (n, top_k, pu.cin, pu.cout)      # what the size depends on; other shapes than gate's are refused by the call
+    need = needs.get(key)
     if need is None:
-        need = needs[(n, top_k)] = moe_layer_workspace_bytes(pu, pd, e, n, top_k)
+        need = needs[key] = moe_layer_workspace_bytes(pu, pd, e, n, top_k)
     ws = _sized_workspace(dev, stream, need) if workspace is None else _given_workspace(workspace, dev)
     _call(dev, lib.hinm_moe_layer, logits.data_ptr(), HINM_BF16 if logits.dtype == torch.bfloat16 else HINM_FP32,
           max(ldl, n), x.data_ptr(), n, ldx, e, top_k, int(renormalize), _VALUES[kind], ctypes.byref(gate.struct()),
