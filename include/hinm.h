@@ -747,7 +747,7 @@ int hinm_fp8_dequantize(const hinm_fp8_t* packed, int32_t n_weights, hinm_packed
  * as NaN.  At most 2^24 columns, ldx below 2^31 (HINM_ESHAPE otherwise).
  * Everything else is as there; the workspace (its first 64 KiB zero-filled
  * before its first use) has the size these queries give, whatever X's
- * alignment. */
+ * alignment, and one that serves some columns serves fewer of them. */
 int hinm_spmm_fp8_workspace_bytes(const hinm_plan_t* plan, int64_t batch, size_t* bytes);
 int hinm_spmm_fp8(const hinm_fp8_t* packed, const void* x_bf16, int64_t batch, int64_t ldx, void* y_bf16, int64_t ldy,
                   void* workspace, size_t workspace_bytes, void* stream);

@@ -883,7 +883,7 @@ int decode_width(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) {
 }
 
 // Workspace: none for few tokens.  Arrival counters and the partial sums of
-// kMaxWgs workgroups, where a launch may split; then the rounded activations of
+// kMaxWgs workgroups, where this launch or one of fewer columns may split; then the rounded activations of
 // one window of columns (at most 2^30 bytes, a multiple of 256 columns), their
 // scales and the pieces' largest magnitudes.
 struct Workspace {
@@ -900,7 +900,10 @@ Workspace workspace_of(const hinm_plan_t& p, int32_t n_experts, int64_t n_cols) 
   const int nt = token_block(p, n_experts, n_cols);
   const int64_t fewest = (p.cout / 64) * (n_experts == 1 ? (w.window + nt - 1) / nt : 1);   // items, if any
   w.split = fewest * 2 <= kMaxWgs;
-  w.x8 = hinm::kWsCounterBytes + (w.split ? (int64_t)kMaxWgs * nt * 64 * 4 : 0);
+  // Where one weight's smallest launches may split, larger ones keep their room, so that a workspace that serves some
+  // columns serves fewer; of experts all may or none.
+  const int room = std::max(w.split ? nt : 0, n_experts == 1 && (p.cout / 64) * 2 <= kMaxWgs ? 128 : 0);
+  w.x8 = hinm::kWsCounterBytes + (int64_t)kMaxWgs * room * 64 * 4;
   w.xs = w.x8 + p.cin * w.ld8;
   w.part = w.xs + w.ld8;
   w.bytes = w.part + (int64_t)w.chunks * w.ld8 * 2;
