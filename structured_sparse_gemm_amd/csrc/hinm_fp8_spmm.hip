@@ -247,10 +247,10 @@ constexpr int kTiles = 3, kRing = 5, kMeta = 2048, kScale = kMeta + 512, kIndex 
 // zeros; sc0 as in load_lds16), and from an address.
 __device__ inline void lds_load(u32x4 buffer, uint32_t lds, uint32_t offset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen sc0 lds"
-               :: "s"(lds), "v"(offset), "s"(buffer) : "memory");
+               :: "s"(lds), "v"(offset), "s"(buffer) : "m0", "memory");
 }
 __device__ inline void lds_load(const uint8_t* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(src) : "m0", "memory");
 }
 
 // An item: row block rb of tile t of an expert, blocks d0 .. d0 + nd - 1 of its
