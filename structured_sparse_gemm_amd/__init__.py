@@ -1364,7 +1364,10 @@ def spmm_experts(experts, x: torch.Tensor, routing: Routing, out: Optional[torch
     return out
 
 
-_VALUES = {"Experts": 0, "HinmMx4": 1, "HinmFp8": 2}   # HINM_VALUES_*
+def _values_of(w) -> Optional[int]:
+    """The HINM_VALUES_* of a stack of experts; None for what is none."""
+    kind = 0 if isinstance(w, Experts) else 1 if isinstance(w, HinmMx4) else 2 if isinstance(w, HinmFp8) else None
+    return None if kind is None or w.n_experts is None else kind
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1389,9 +1392,8 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, gate, up, down, top_k: int,
     [inter x hidden] weights, down of [hidden x inter]: Experts, or all three quantize_mx4 or quantize_fp8 stacks.
     Returns (or fills) bf16 [hidden, tokens].  Asynchronous on the current stream; workspace as in spmm_experts.  More
     tokens go through route, dispatch, spmm_experts and combine."""
-    kind = type(gate).__name__
-    if kind not in _VALUES or type(up) is not type(gate) or type(down) is not type(gate) or any(
-            w.n_experts is None for w in (gate, up, down)):
+    kind = _values_of(gate)
+    if kind is None or _values_of(up) != kind or _values_of(down) != kind:
         raise ValueError("gate, up and down must be stacks of experts of one kind (Experts, quantize_mx4's or "
                          "quantize_fp8's)")
     pg, pu, pd, dev, e = gate.plan, up.plan, down.plan, gate.idx_24.device, gate.n_experts
@@ -1416,7 +1418,7 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, gate, up, down, top_k: int,
         need = needs[key] = moe_layer_workspace_bytes(pu, pd, e, n, top_k)
     ws = _sized_workspace(dev, stream, need) if workspace is None else _given_workspace(workspace, dev)
     _call(dev, lib.hinm_moe_layer, logits.data_ptr(), HINM_BF16 if logits.dtype == torch.bfloat16 else HINM_FP32,
-          max(ldl, n), x.data_ptr(), n, ldx, e, top_k, int(renormalize), _VALUES[kind], ctypes.byref(gate.struct()),
+          max(ldl, n), x.data_ptr(), n, ldx, e, top_k, int(renormalize), kind, ctypes.byref(gate.struct()),
           ctypes.byref(up.struct()), ctypes.byref(down.struct()), out.data_ptr(), ldy,
           ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
     return out

@@ -33,3 +33,21 @@ def test_workspace_is_of_the_call_at_hand(asked):
     small = hinm.moe_layer_workspace_bytes(hinm.plan(192, 128, 64, 0.75, 0.55), hinm.plan(128, 192, 64, 0.75, 0.55), 4, 3, 2)
     need = hinm.moe_layer_workspace_bytes(up.plan, down.plan, 4, 3, 2)
     assert asked == [small, need, need] and small < need
+
+
+class _Tagged(hinm.Experts):
+    """A user's own stack."""
+
+
+def test_a_subclass_is_a_stack_of_its_kind(asked):
+    """Stacks are told apart by their class, not by its name."""
+    gate, up, down = _stack(192, 128), _stack(192, 128), _stack(128, 192)
+    tagged = _Tagged(gate.plan, **{k: getattr(gate, k) for k in hinm._packed_shapes(gate.plan)})
+    x, logits = torch.zeros(128, 3, dtype=BF16), torch.zeros(4, 3)
+    hinm.moe_layer(x, logits, tagged, up, down, 2)
+    assert len(asked) == 1
+
+    class Experts:
+        n_experts = 4
+    with pytest.raises(ValueError, match="of one kind"):
+        hinm.moe_layer(x, logits, Experts(), Experts(), Experts(), 2)
