@@ -25,8 +25,9 @@
  *   - Functions return a hinm_status and never throw.  On failure a message is
  *     available from hinm_last_error() in the calling thread.  Argument errors
  *     are detected on the host before anything is launched.
- *   - Functions are re-entrant; calls that share output or workspace buffers
- *     must not overlap in time.
+ *   - Functions are re-entrant; work that shares output or workspace buffers
+ *     must not overlap in time.  Calls of several host threads on one stream
+ *     do not: each call's kernels are enqueued together.
  */
 #ifndef HINM_H_
 #define HINM_H_

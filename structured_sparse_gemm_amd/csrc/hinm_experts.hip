@@ -885,6 +885,7 @@ int launch(const hinm_plan_t& p, int32_t n_experts, ExpArgs a, const void* x, in
   a.nkb_s = p.n_24_pad / HINM_KB_24;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
   a.x_end = 1;
+  const hinm::EnqueueLock whole(workspace);
   if (w.copy) {
     uint16_t* copy = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + w.copy_at());
     const dim3 grid((unsigned)((w.ld + 2047) / 2048), (unsigned)std::min(p.cin, 4096));

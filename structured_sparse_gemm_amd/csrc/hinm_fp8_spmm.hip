@@ -987,6 +987,7 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
   float* const part = reinterpret_cast<float*>(ws + hinm::kWsCounterBytes);
   unsigned* const counters = reinterpret_cast<unsigned*>(ws);
   const int nt = token_block(p, n_experts, n_cols);
+  const hinm::EnqueueLock whole(workspace);
   for (int64_t c0 = 0; c0 < n_cols; c0 += w.window) {
     a.before = (int)c0;
     a.n_cols = (int)std::min(n_cols - c0, w.window);

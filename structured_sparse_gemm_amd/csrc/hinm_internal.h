@@ -5,6 +5,8 @@
 #include <stdarg.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "hinm.h"
 
 namespace hinm {
@@ -53,6 +55,20 @@ SpmmShape spmm_shape(const hinm_plan_t* p, int64_t batch);
 
 // Current value of a launch-shape option (HINM_OPT_*).
 int64_t option(int key);
+
+// Held by a call of several kernels, which hand results on in its workspace,
+// from its first launch to its last: host threads that call on one stream with
+// one workspace (the binding's default is the stream's) would otherwise enqueue
+// them in turn, and one call's second kernel read what another's first one left.
+// One of several, by the workspace, so that streams rarely wait for each other.
+class EnqueueLock {
+ public:
+  explicit EnqueueLock(const void* workspace) : lock_(mutex_of(workspace)) {}
+
+ private:
+  static std::mutex& mutex_of(const void* workspace);
+  std::lock_guard<std::mutex> lock_;
+};
 
 // Current device is a gfx950 part (checked once per device); HINM_OK or
 // HINM_EDEVICE / HINM_EHIP with the message recorded.

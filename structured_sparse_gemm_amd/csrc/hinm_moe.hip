@@ -922,6 +922,7 @@ extern "C" int hinm_moe_layer(const void* logits, int32_t logits_type, int64_t l
   a.up_cap = columns_of(pu->cin);
   a.wide = wide_of(n_tokens);
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
+  const hinm::EnqueueLock whole(workspace);
   if (values == HINM_VALUES_BF16) launch<HINM_VALUES_BF16>(a, stream);
   else if (values == HINM_VALUES_MX4) launch<HINM_VALUES_MX4>(a, stream);
   else launch<HINM_VALUES_FP8>(a, stream);

@@ -252,6 +252,12 @@ extern "C" const char* hinm_last_error(void) { return hinm::g_last_error; }
 //  - otherwise the generic kernel, which splits K over workgroups when there
 //    are too few of them and reduces the partials through the workspace.
 namespace hinm {
+
+std::mutex& EnqueueLock::mutex_of(const void* workspace) {
+  static std::mutex m[61];         // workspaces are at least 256 bytes apart
+  return m[(reinterpret_cast<uintptr_t>(workspace) >> 8) % 61];
+}
+
 SpmmShape spmm_shape(const hinm_plan_t* p, int64_t batch) {
   SpmmShape s;
   s.n_rblocks = (p->tile_rows + 63) / 64;

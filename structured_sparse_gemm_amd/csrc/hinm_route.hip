@@ -709,6 +709,7 @@ extern "C" int hinm_route(const void* logits, int32_t logits_type, int64_t n_tok
   a.hist = static_cast<int32_t*>(workspace);
   a.total = a.hist ? a.hist + (size_t)a.n_blocks * n_experts : nullptr;
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_);
+  const hinm::EnqueueLock whole(workspace);
   if (top_k == 1) return launch_route<1>(a, stream);
   if (top_k == 2) return launch_route<2>(a, stream);
   if (top_k <= 4) return launch_route<4>(a, stream);

@@ -1920,6 +1920,7 @@ static int spmm_impl(const hinm_plan_t& p, const PackedView& packed_v, const voi
     }
   } else {
     const dim3 grid(sh.n_tblocks, p.n_tiles * sh.n_rblocks, sh.splits), block(kWaves * 64);
+    const hinm::EnqueueLock whole(workspace);
     switch (sh.nt) {
       case 16: hipLaunchKernelGGL(spmm_kernel<16>, grid, block, 0, stream, a); break;
       case 32: hipLaunchKernelGGL(spmm_kernel<32>, grid, block, 0, stream, a); break;
