@@ -1202,7 +1202,6 @@ class HinmFp8:
         st = self.__dict__.get("_struct")
         if st is None:
             st = self.__dict__["_struct"] = Fp8T(self.plan.raw, *[_ptr(getattr(self, k)) for k in _MX4_BUFFERS])
-            self.__dict__["_need"] = {}
         return st
 
     def dequantize(self):
@@ -1278,7 +1277,7 @@ def _given_workspace(workspace: torch.Tensor, dev: torch.device) -> torch.Tensor
 
 
 def _fp8_need(w: HinmFp8, cols: int) -> int:
-    needs = w.__dict__["_need"]
+    needs = w.__dict__.setdefault("_need", {})
     need = needs.get(cols)
     if need is None:
         n = ctypes.c_size_t()

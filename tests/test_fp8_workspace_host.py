@@ -26,3 +26,11 @@ def test_never_smaller_than_for_fewer_columns(cout, cin, experts):
     sizes = _sizes(p, experts, cols)
     fell = [(a, b) for a, b, s, t in zip(cols, cols[1:], sizes, sizes[1:]) if t < s]
     assert not fell, fell[:5]
+
+
+def test_sizes_are_asked_for_in_any_order():
+    """Remembering sizes needs nothing that another call on the weight has set up (another thread may be half-way)."""
+    import torch
+    p = hinm.plan(128, 256, 64, 0.75, 0.55)
+    q = hinm.HinmFp8(p, **{k: torch.zeros(s, dtype=t) for k, (s, t) in hinm._fp8_shapes(p).items()})
+    assert hinm._fp8_need(q, 640) == hinm._fp8_need(q, 640) == _sizes(p, 1, [640])[0]
