@@ -7,7 +7,6 @@
 namespace {
 
 typedef uint32_t fp8_u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 fp8_bf16x2 __attribute__((ext_vector_type(2)));
 
 // 2^(e - 127) for 1 <= e <= 254: every scale is of 3 .. 246.
 __device__ inline float fp8_scale(uint32_t e) { return __uint_as_float(e << 23); }
@@ -32,10 +31,10 @@ __device__ inline uint32_t fp8_max_finite(uint32_t m, uint32_t v) {
 // half of `old`.  The product is exact, the conversion rounds to nearest even;
 // the clamp saturates (only values past 448 * 2^119 reach it).
 template <bool HIGH>
-__device__ inline uint32_t fp8_codes(uint32_t old, uint32_t v, float inverse0, float inverse1) {
+__device__ inline uint32_t fp8_codes(uint32_t old, uint32_t v, float inverse) {
   const float a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xffff0000u);
-  const float x = __builtin_fminf(__builtin_fmaxf(a * inverse0, -448.f), 448.f);
-  const float y = __builtin_fminf(__builtin_fmaxf(b * inverse1, -448.f), 448.f);
+  const float x = __builtin_fminf(__builtin_fmaxf(a * inverse, -448.f), 448.f);
+  const float y = __builtin_fminf(__builtin_fmaxf(b * inverse, -448.f), 448.f);
   uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, y, (int)old, HIGH);
   constexpr int at = HIGH ? 16 : 0;
   if ((v & 0x7f80u) == 0x7f80u) c = (c & ~(0xffu << at)) | (0x7fu << at);
@@ -46,8 +45,8 @@ __device__ inline uint32_t fp8_codes(uint32_t old, uint32_t v, float inverse0, f
 // Eight bf16 values of one block.
 __device__ inline fp8_u32x2 fp8_codes8(u32x4 v, float inverse) {
   fp8_u32x2 c;
-  c[0] = fp8_codes<true>(fp8_codes<false>(0u, v[0], inverse, inverse), v[1], inverse, inverse);
-  c[1] = fp8_codes<true>(fp8_codes<false>(0u, v[2], inverse, inverse), v[3], inverse, inverse);
+  c[0] = fp8_codes<true>(fp8_codes<false>(0u, v[0], inverse), v[1], inverse);
+  c[1] = fp8_codes<true>(fp8_codes<false>(0u, v[2], inverse), v[3], inverse);
   return c;
 }
 
