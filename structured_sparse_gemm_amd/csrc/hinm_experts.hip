@@ -14,6 +14,8 @@
 #include "hinm_mx4.h"
 #include "hinm_ragged.h"
 
+using hinm::Buf;
+using hinm::check_bufs;
 using hinm::fail;
 
 namespace {
@@ -780,21 +782,6 @@ int check_args(const hinm_plan_t& p, int32_t n_experts, const void* x, int64_t n
   return HINM_OK;
 }
 
-struct Buf {
-  const void* ptr;
-  int64_t bytes;
-  const char* name;
-};
-
-int check_bufs(const Buf* b, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (b[i].bytes > 0 && !b[i].ptr)
-      return fail(HINM_EINVAL, "%s is NULL but holds %lld bytes", b[i].name, (long long)b[i].bytes);
-    if (!hinm::aligned(b[i].ptr, 16)) return fail(HINM_EALIGN, "%s is not 16-byte aligned", b[i].name);
-  }
-  return HINM_OK;
-}
-
 // Tokens a workgroup takes, from the columns an expert has on average (the
 // counts themselves are on the device): 16 or 32 in the decode kernel, 128 or
 // 256 in the prefill kernel.  The decode kernel is the better one for few
@@ -935,7 +922,7 @@ int run_mx4(const hinm_mx4_t* k, int32_t n_experts, const void* x, int64_t n_col
                     {k->scale_24, p.bytes_val_24, "scale_24"}, {k->meta_24, p.bytes_meta_24, "meta_24"},
                     {k->idx_24, p.bytes_idx_24, "idx_24"}};
   if (n_cols == 0) return HINM_OK;
-  st = check_bufs(b, 7);
+  st = check_bufs(b, 7, "");
   if (st) return st;
   ExpArgs a{};
   a.val_d = reinterpret_cast<const uint8_t*>(k->val_dense);
@@ -991,7 +978,7 @@ extern "C" int hinm_spmm_experts(const hinm_packed_t* stack, int32_t n_experts, 
                     {stack->val_24, p.bytes_val_24, "val_24"}, {stack->meta_24, p.bytes_meta_24, "meta_24"},
                     {stack->idx_24, p.bytes_idx_24, "idx_24"}};
   if (n_cols == 0) return HINM_OK;
-  st = check_bufs(b, 5);
+  st = check_bufs(b, 5, "");
   if (st) return st;
   ExpArgs a{};
   a.val_d = static_cast<const uint8_t*>(stack->val_dense);

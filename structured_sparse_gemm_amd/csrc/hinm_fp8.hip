@@ -9,6 +9,8 @@
 #include "hinm_fp8.h"
 #include "hinm_internal.h"
 
+using hinm::Buf;
+using hinm::check_bufs;
 using hinm::fail;
 
 namespace {
@@ -99,21 +101,6 @@ __global__ __launch_bounds__(256) void fp8_dequantize_kernel(Fp8Region d, Fp8Reg
       if (k < u.blocks)
         *reinterpret_cast<u32x4*>(r.val + u.val + k * u.stride + 8 * threadIdx.x) = fp8_expand(c[k], scale);
   }
-}
-
-struct Buf {
-  const void* ptr;
-  int64_t bytes;
-  const char* name;
-};
-
-int check_bufs(const Buf* b, int n, const char* whose) {
-  for (int i = 0; i < n; ++i) {
-    if (b[i].bytes > 0 && !b[i].ptr)
-      return fail(HINM_EINVAL, "%s: %s is NULL but holds %lld bytes", whose, b[i].name, (long long)b[i].bytes);
-    if (!hinm::aligned(b[i].ptr, 16)) return fail(HINM_EALIGN, "%s: %s is not 16-byte aligned", whose, b[i].name);
-  }
-  return HINM_OK;
 }
 
 int convert(const hinm_plan_t& p, int64_t n, const hinm_packed_t& full, const hinm_fp8_t& eight, bool quantize,

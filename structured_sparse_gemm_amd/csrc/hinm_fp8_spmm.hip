@@ -13,6 +13,8 @@
 #include "hinm_ragged.h"
 #include "hinm_stream.h"
 
+using hinm::Buf;
+using hinm::check_bufs;
 using hinm::fail;
 
 namespace {
@@ -916,14 +918,12 @@ int launch(const hinm_fp8_t* k, int32_t n_experts, const void* x, int64_t n_cols
   int st = check_args(p, n_experts, x, n_cols, ldx, y, ldy);
   if (st) return st;
   if (n_cols == 0) return HINM_OK;
-  const struct { const void* ptr; int64_t bytes; const char* name; } bufs[7] = {
+  const Buf bufs[7] = {
       {k->val_dense, p.bytes_val_dense, "val_dense"}, {k->scale_dense, p.bytes_val_dense, "scale_dense"},
       {k->idx_dense, p.bytes_idx_dense, "idx_dense"}, {k->val_24, p.bytes_val_24, "val_24"},
       {k->scale_24, p.bytes_val_24, "scale_24"}, {k->meta_24, p.bytes_meta_24, "meta_24"}, {k->idx_24, p.bytes_idx_24, "idx_24"}};
-  for (const auto& b : bufs) {
-    if (b.bytes > 0 && !b.ptr) return fail(HINM_EINVAL, "%s is NULL but holds %lld bytes", b.name, (long long)b.bytes);
-    if (!hinm::aligned(b.ptr, 16)) return fail(HINM_EALIGN, "%s is not 16-byte aligned", b.name);
-  }
+  st = check_bufs(bufs, 7, "");
+  if (st) return st;
   const Workspace w = workspace_of(p, n_experts, n_cols);
   if (w.bytes > 0 && (!workspace || workspace_bytes < (size_t)w.bytes))
     return fail(HINM_EWORKSPACE, "workspace of %zu bytes given, %lld needed", workspace_bytes, (long long)w.bytes);

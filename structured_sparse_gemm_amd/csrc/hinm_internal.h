@@ -27,6 +27,15 @@ hinm_plan_t shape_plan(const hinm_tplan_t& p);
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// A weight's device buffer: present where it holds bytes, and 16-byte aligned.
+// The messages begin with `whose` ("" for none).
+struct Buf {
+  const void* ptr;
+  int64_t bytes;
+  const char* name;
+};
+int check_bufs(const Buf* b, int n, const char* whose);
+
 // Split of the reduction dimension chosen for a batch (1 = no split) and the
 // token-block width; shared by hinm_spmm and hinm_spmm_workspace_bytes so the
 // workspace size always matches what the launch uses.

@@ -47,6 +47,8 @@
 #include "hinm_ragged.h"
 #include "hinm_stream.h"
 
+using hinm::Buf;
+using hinm::check_bufs;
 using hinm::fail;
 
 namespace {
@@ -766,12 +768,6 @@ int check_shapes(const hinm_plan_t& up, const hinm_plan_t& down, int32_t n_exper
   return HINM_OK;
 }
 
-struct Buf {
-  const void* ptr;
-  int64_t bytes;
-  const char* name;
-};
-
 // Checks one stack and fills in its kernel view.
 int stack_of(const char* whose, const hinm_plan_t& p, int32_t values, const void* stack, MoeStack& s) {
   s = MoeStack{};
@@ -816,11 +812,7 @@ int stack_of(const char* whose, const hinm_plan_t& p, int32_t values, const void
   const Buf b[7] = {{s.val_d, s.b_val_d, "val_dense"}, {s.scale_d, s.b_scale_d, "scale_dense"}, {s.idx_d, s.b_idx_d, "idx_dense"},
                     {s.val_s, s.b_val_s, "val_24"}, {s.scale_s, s.b_scale_s, "scale_24"}, {s.meta, s.b_meta, "meta_24"},
                     {s.idx_s, s.b_idx_s, "idx_24"}};
-  for (const Buf& q : b) {
-    if (q.bytes > 0 && !q.ptr) return fail(HINM_EINVAL, "%s: %s is NULL but holds %lld bytes", whose, q.name, (long long)q.bytes);
-    if (!hinm::aligned(q.ptr, 16)) return fail(HINM_EALIGN, "%s: %s is not 16-byte aligned", whose, q.name);
-  }
-  return HINM_OK;
+  return check_bufs(b, 7, whose);
 }
 
 // The plan is every stack struct's first member.

@@ -12,6 +12,8 @@
 #include "hinm_internal.h"
 #include "hinm_mx4.h"
 
+using hinm::Buf;
+using hinm::check_bufs;
 using hinm::fail;
 
 namespace {
@@ -154,21 +156,6 @@ __global__ __launch_bounds__(256) void dequantize_kernel(Mx4Region d, Mx4Region 
     }
     __syncthreads();
   }
-}
-
-struct Buf {
-  const void* ptr;
-  int64_t bytes;
-  const char* name;
-};
-
-int check_bufs(const Buf* b, int n, const char* whose) {
-  for (int i = 0; i < n; ++i) {
-    if (b[i].bytes > 0 && !b[i].ptr)
-      return fail(HINM_EINVAL, "%s: %s is NULL but holds %lld bytes", whose, b[i].name, (long long)b[i].bytes);
-    if (!hinm::aligned(b[i].ptr, 16)) return fail(HINM_EALIGN, "%s: %s is not 16-byte aligned", whose, b[i].name);
-  }
-  return HINM_OK;
 }
 
 int convert(const hinm_plan_t& p, int64_t n, const hinm_packed_t& full, const hinm_mx4_t& four, bool quantize,

@@ -253,6 +253,16 @@ extern "C" const char* hinm_last_error(void) { return hinm::g_last_error; }
 //    are too few of them and reduces the partials through the workspace.
 namespace hinm {
 
+int check_bufs(const Buf* b, int n, const char* whose) {
+  const char* const sep = *whose ? ": " : "";
+  for (int i = 0; i < n; ++i) {
+    if (b[i].bytes > 0 && !b[i].ptr)
+      return fail(HINM_EINVAL, "%s%s%s is NULL but holds %lld bytes", whose, sep, b[i].name, (long long)b[i].bytes);
+    if (!aligned(b[i].ptr, 16)) return fail(HINM_EALIGN, "%s%s%s is not 16-byte aligned", whose, sep, b[i].name);
+  }
+  return HINM_OK;
+}
+
 std::mutex& EnqueueLock::mutex_of(const void* workspace) {
   static std::mutex m[61];         // workspaces are at least 256 bytes apart
   return m[(reinterpret_cast<uintptr_t>(workspace) >> 8) % 61];
