@@ -1390,7 +1390,11 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, gate, up, down, top_k: int,
     x bf16 [hidden, tokens], logits bf16 or fp32 [experts, tokens] (as route takes them), gate and up stacks of
     [inter x hidden] weights, down of [hidden x inter]: Experts, or all three quantize_mx4 or quantize_fp8 stacks.
     Returns (or fills) bf16 [hidden, tokens].  Asynchronous on the current stream; workspace as in spmm_experts.  More
-    tokens go through route, dispatch, spmm_experts and combine."""
+    tokens go through route, dispatch, spmm_experts and combine.
+
+    With 8-bit stacks the activations stay bf16 here, where spmm_experts rounds them to 8 bits: a program that uses this
+    layer up to 32 tokens and the products beyond, and wants one kind of numbers, gives the products
+    ``stack.dequantize()``, the same values with bf16 activations."""
     kind = _values_of(gate)
     if kind is None or _values_of(up) != kind or _values_of(down) != kind:
         raise ValueError("gate, up and down must be stacks of experts of one kind (Experts, quantize_mx4's or "

@@ -23,7 +23,7 @@
 //                two tokens of 11008 channels, and 8 experts of 8 tokens each
 //                took 145 us, four reads of each expert's weight; now 75.)
 //
-// What bounds them (8 experts of 11008x4096, bf16, 32 tokens, 105 and 75 us for
+// What bounds them (8 experts of 11008x4096, bf16, 32 tokens, 104 and 75 us for
 // 418 and 209 MB): a compute unit's 64 outstanding cache lines, of which the
 // gathered rows of h are most in the down kernel.  One token (26 and 19 us for
 // 104 and 52 MB): a third is the chain ahead of the first products - arguments,
@@ -65,7 +65,7 @@ constexpr int sums_pitch(int f) { return 256 * f + 8; }
 
 // Reads a word of every 64 bytes of a kernel's arguments, so that they are in
 // the scalar cache when they are wanted, and waited for once (a token, 2 of 8
-// experts of 11008: 47.2 us without, 46.4 with).
+// experts of 11008: 48.2 us without, 47.5 with).
 template <class Args>
 __device__ __forceinline__ void touch(const Args& a) {
   uint32_t x = 0;
@@ -450,8 +450,9 @@ __device__ __forceinline__ void put_x(const MoeArgs& a, uint32_t mask, int g, in
 }
 
 // Items are (segment, 16 F rows of the inner channels).  A turn of three blocks: of
-// two, three and four, a token's layer 46.1, 45.2 and 46.8 us (bf16), 39.9, 38.9
-// and 41.9 (8 bits).
+// two, three and four, a token's layer 49.0, 47.5 and 49.7 us (bf16), 41.9, 40.6
+// and 42.0 (8 bits), 32 tokens 179, 176 and 179, 152, 149 and 153 (this and the
+// figures below: three sets of inputs in turn).
 template <int VALUES, int F>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
   constexpr int R = 16 * F, kPitch = sums_pitch(2), kDepth = 3;
@@ -576,8 +577,8 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
 // the rows and values of the next ones, by indices that it asked for a turn
 // before, and for the indices of those after.  No load is under a condition:
 // waits are for a known number of loads.
-// A turn of two blocks: of two, three and four, a token's layer 43.5, 44.5 and
-// 46.7 us (bf16), 39.1, 40 and 41.9 (8 bits).
+// A turn of two blocks: of two, three and four, a token's layer 47.5, 48.4 and
+// 50.4 us (bf16), 40.6, 41.6 and 43.5 (8 bits).
 template <int VALUES, int WIDE>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   constexpr int F = 4, kPitch = sums_pitch(F), kDepth = 2, kRow = 2 * WIDE, kSlot = 64 * kRow;
@@ -595,7 +596,8 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
   __syncthreads();
   const MoeStack& w = a.down;
   const int n_rb = w.cout / 64, nd = w.nkb_d, nblk = nd + w.nkb_s, n_seg = uniform(table.n_seg), units = n_seg * nblk;
-  // shares of a row block's K-blocks: as many as leave no compute unit idle, and a block for each wave
+  // shares of a row block's K-blocks: as many as one round of workgroups holds, with a block for each wave (of 256
+  // workgroups all at 4096 hidden channels, 240 at 5120, 192 at 6144, 224 at 7168)
   const int splits = max(1, min(kCus / n_rb, units / kWaves));
   uint8_t* const slot = slots + wave * 2 * kSlot;
 #pragma nounroll
@@ -825,8 +827,8 @@ int plan_of(const char* whose, const void* stack, const hinm_plan_t*& p) {
 // Fragments of 16 rows of the up kernel's items: what leaves the busiest
 // workgroup the least to do, by an item's cost of its own, in half fragments.
 // Measured with two and with four (8 experts of 11008x4096, top 2): bf16 at 1
-// and 32 tokens 43 / 46 and 175 / 175 us, 8 bits 37 / 40 and 141 / 143, 4 bits
-// 35 / 33 and 110 / 96.
+// and 32 tokens 48 / 52 and 176 / 176 us, 8 bits 41 / 45 and 149 / 150, 4 bits
+// 34 / 33 and 127 / 113.
 int fragments_of(const MoeArgs& a, int values) {
   const int64_t segs = std::min<int64_t>(a.n_experts, (int64_t)a.n_tokens * a.top_k);
   const int own = values == HINM_VALUES_MX4 ? 6 : 0;
